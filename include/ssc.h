@@ -364,6 +364,131 @@ int ssc_scatter_i32(const int32_t *in, const int32_t *ranks, int32_t *out, int64
  * allowed. */
 int ssc_copy_i32(const int32_t *in, int32_t *out, int64_t n, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rows moved by a key, and the choice of the next token: the same work
+ * (flags or keys, counts, scans, stable placement, selection) for the token
+ * path of a language model. Element types of rows: */
+typedef enum ssc_dtype {
+    SSC_F32 = 0,
+    SSC_BF16 = 1,
+    SSC_F16 = 2
+} ssc_dtype;
+/* Conventions of these calls beside the shared ones above:
+ *   - Rows are contiguous, `width` elements (1 <= width <= 2^28) of one
+ *     type; arrays need the alignment of their element only.
+ *   - Row, token and group counts are at most INT32_MAX (groups and vocab of
+ *     the grouping and the gradient: INT32_MAX - 1); larger ones give
+ *     SSC_ERR_SIZE.
+ *   - Scratch needs no initialisation and keeps nothing between calls; one
+ *     buffer must not serve two calls that may run at the same time. Where
+ *     the size function returns 0 it may be NULL.
+ *   - Ids, ranks and positions read from device memory are checked there: one
+ *     out of its range moves nothing and adds nothing, and nothing outside the
+ *     arrays is touched.
+ *   - Inputs may overlap each other; an output must not overlap any other
+ *     array of the call (SSC_ERR_ALIAS).
+ *   - Sums are held in fp32 and rounded to the output's type once; their order
+ *     depends on the sizes and the ranks only, so a call repeats bit for bit.
+ */
+
+/* Scratch bytes of a grouping of n keys (0 for up to 16,384 keys). */
+size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
+
+/* Stable partition into `groups` groups: key k belongs to group k, and one
+ * outside [0, groups) to none (give -1 for padding or a dropped assignment).
+ *   offsets[g] = keys of groups below g, for g in [0, groups]; the last
+ *                entry is the number of keys that belong to a group
+ *   ranks[i]   = the slot of key i: offsets[keys[i]] + equal keys before i;
+ *                -1 for a key of no group                        (nullable)
+ *   order[s]   = the i with ranks[i] = s, for s < offsets[groups]; the
+ *                entries past that are not written               (nullable)
+ * The many-way form of ssc_partition_i32: one counting and one scattering
+ * step per 9 bits of group number (a single launch for up to 16,384 keys). */
+int ssc_group_by_key_i32(const int32_t *keys, int64_t n, int64_t groups, int32_t *order,
+                         int32_t *ranks, int32_t *offsets, void *scratch, size_t scratch_bytes,
+                         void *stream);
+int ssc_group_by_key_i64(const int64_t *keys, int64_t n, int64_t groups, int32_t *order,
+                         int32_t *ranks, int32_t *offsets, void *scratch, size_t scratch_bytes,
+                         void *stream);
+
+/* Embedding lookup: out[i] = scale * table[ids[i]] for n ids, the table
+ * holding `vocab` rows; an id outside [0, vocab) gives a row of zeros. */
+int ssc_embed_rows_i32(const void *table, int dtype, int64_t vocab, int64_t width,
+                       const int32_t *ids, int64_t n, float scale, void *out, void *stream);
+int ssc_embed_rows_i64(const void *table, int dtype, int64_t vocab, int64_t width,
+                       const int64_t *ids, int64_t n, float scale, void *out, void *stream);
+
+/* Scratch bytes of the embedding's gradient: fp32 sums of blocks of 16, 256
+ * and 4096 sorted tokens (0 for fewer than 256 tokens). */
+size_t ssc_embed_grad_scratch_bytes(int64_t n, int64_t width);
+
+/* Gradient of the lookup with respect to the table, by sorted tokens:
+ * grad[v] = scale * (sum of dout[i] over all i with ids[i] = v), given the
+ * grouping of the ids (`order` and `offsets` of ssc_group_by_key with groups
+ * = vocab). accumulate = 0 writes every row of grad, zeros where no token
+ * has the id; otherwise the sum is added to the row, and rows without tokens
+ * are not touched. grad_dtype is dtype or SSC_F32. */
+int ssc_embed_rows_grad_i32(const void *dout, int dtype, int64_t n, int64_t width,
+                            const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                            int64_t vocab, float scale, void *grad, int grad_dtype, int accumulate,
+                            void *scratch, size_t scratch_bytes, void *stream);
+int ssc_embed_rows_grad_i64(const void *dout, int dtype, int64_t n, int64_t width,
+                            const int64_t *ids, const int32_t *order, const int32_t *offsets,
+                            int64_t vocab, float scale, void *grad, int grad_dtype, int accumulate,
+                            void *scratch, size_t scratch_bytes, void *stream);
+
+/* Rows to their groups: out[ranks[t, k]] = x[t] for t < tokens, k < per, with
+ * ranks (tokens x per, distinct, as the grouping of the tokens' expert ids
+ * gives them) below `rows`, the rows of out; rows that no rank names are not
+ * written. Its gradient is ssc_combine_rows without weights. */
+int ssc_dispatch_rows(const void *x, int dtype, int64_t tokens, int64_t per, int64_t width,
+                      const int32_t *ranks, int64_t rows, void *out, void *stream);
+
+/* Rows back from their groups: out[t] = sum over k of weights[t, k] *
+ * y[ranks[t, k]] (weights nullable: all one). A rank outside [0, rows) adds
+ * nothing; a token with no rank inside gets a row of zeros. */
+int ssc_combine_rows(const void *y, int dtype, int64_t rows, int64_t width, const int32_t *ranks,
+                     const float *weights, int64_t tokens, int64_t per, void *out, void *stream);
+
+/* Gradients of ssc_combine_rows: dy[ranks[t, k]] = weights[t, k] * dout[t] and
+ * dweights[t, k] = <dout[t], y[ranks[t, k]]> (0 for a rank outside); rows of dy
+ * that no rank names are not written. One pass over dout and y. Ranks must be
+ * distinct. */
+int ssc_combine_rows_grad(const void *dout, const void *y, int dtype, int64_t rows, int64_t width,
+                          const int32_t *ranks, const float *weights, int64_t tokens, int64_t per,
+                          void *dy, float *dweights, void *stream);
+
+/* Scratch bytes of ssc_sample_rows. */
+size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
+
+/* The next token of each row of logits (row r at logits + r * stride
+ * elements, stride >= vocab), from a given random number u[r] in [0, 1). With
+ * the row's tokens ordered by logit, largest first, equal ones by index, and
+ * w_i = exp((logit_i - largest) / temperature), the kept tokens are
+ *   the first top_k of the order (top_k < 1: all);
+ *   of these, each one before which the weights sum to less than top_p times
+ *     the sum over all of them (top_p >= 1: all);
+ *   of these, those with w_i >= min_p;
+ * and always the first of the order. tokens[r] is the first index, in index
+ * order, at which the running sum of the kept weights exceeds u[r] times their
+ * sum. A temperature that is not above 0 keeps the first of the order alone.
+ * A logit of NaN or -infinity is no token; +infinity shares the row's
+ * weight evenly among the logits of +infinity. A row with no token gives
+ * tokens[r] = -1, kept[r] = 0, logprobs[r] = -infinity. A u outside [0, 1) is
+ * taken as the nearest end (NaN as 0), a top_p of NaN as 1, of 0 or less as one
+ * that keeps the first only, a min_p of NaN as 0.
+ * The settings are arrays of one value a row, each nullable: temperature 1,
+ * no top_k, no top_p, no min_p. kept[r] (nullable) is the number of kept
+ * tokens, logprobs[r] (nullable) the logarithm of the chosen weight over the
+ * kept ones' sum. Weights are computed in fp64 and summed as fixed-point
+ * integers of at least 40 fractional bits, so that neither the order of
+ * a sum nor the split of a row changes a result. 1 <= vocab <= 2^22 and at
+ * most 65,535 rows. */
+int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                    const float *u, const float *temperature, const int32_t *top_k,
+                    const float *top_p, const float *min_p, int32_t *tokens, int32_t *kept,
+                    float *logprobs, void *scratch, size_t scratch_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssc_status_str(int status);
 

@@ -24,6 +24,7 @@ STRESS_LIB_PATH = os.path.join(_PKG, "libssc_stress.so")    # race-test build, 3
 
 PRED = {"nonzero": 0, "odd": 1, "even": 2, "bit_set": 3, "bit_clear": 4, "mod_lt": 5,
         "f32_nonzero": 6, "f32_gt": 7, "f32_lt": 8, "f32_in": 9}
+DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # element types of rows
 STATUS = {0: "SSC_OK", 1: "SSC_ERR_ARG", 2: "SSC_ERR_SIZE", 3: "SSC_ERR_ALIAS",
           4: "SSC_ERR_SCRATCH", 5: "SSC_ERR_HIP", 6: "SSC_ERR_DEVICE"}
 
@@ -68,6 +69,19 @@ SIGNATURES = {
     "ssc_compact_kv_f32": (_INT, [_P, _P, _P, _P, _I64, _INT, _F32, _F32, _P, _P, _SZ, _P]),
     "ssc_compact_i64": (_INT, [_P, _P, _I64, _INT, _I32, _P, _P, _SZ, _P]),
     "ssc_select_index_i64": (_INT, [_P, _P, _I64, _INT, _I32, _P, _P, _SZ, _P]),
+    "ssc_group_scratch_bytes": (_SZ, [_I64, _I64]),
+    "ssc_group_by_key_i32": (_INT, [_P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_group_by_key_i64": (_INT, [_P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_embed_rows_i32": (_INT, [_P, _INT, _I64, _I64, _P, _I64, _F32, _P, _P]),
+    "ssc_embed_rows_i64": (_INT, [_P, _INT, _I64, _I64, _P, _I64, _F32, _P, _P]),
+    "ssc_embed_grad_scratch_bytes": (_SZ, [_I64, _I64]),
+    "ssc_embed_rows_grad_i32": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _I64, _F32, _P, _INT, _INT, _P, _SZ, _P]),
+    "ssc_embed_rows_grad_i64": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _I64, _F32, _P, _INT, _INT, _P, _SZ, _P]),
+    "ssc_dispatch_rows": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "ssc_combine_rows": (_INT, [_P, _INT, _I64, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "ssc_combine_rows_grad": (_INT, [_P, _P, _INT, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "ssc_sample_scratch_bytes": (_SZ, [_I64, _I64]),
+    "ssc_sample_rows": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "ssc_status_str": (ctypes.c_char_p, [_INT]),
     "ssc_last_hip_error": (_INT, []),
 }
@@ -615,3 +629,263 @@ def compact_kv(keys: torch.Tensor, vals: torch.Tensor, pred="nonzero", pa=0, pb=
           vals_out, n, _pred(pred), pa, pb, count, scratch,
           scratch.numel(), _stream(keys))
     return keys_out, vals_out, count
+
+
+# ---- rows moved by a key, and the choice of the next token ----------------
+# These calls compute outside autograd: a gradient is a call of its own.
+
+
+def _rows(x: torch.Tensor, name: str) -> tuple[int, int]:
+    """(rows, width) of a 2-d tensor of rows that the row calls take."""
+    if x.dtype not in DTYPE:
+        raise TypeError(f"{name} holds float32, bfloat16 or float16 rows, not {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} is 2-d (rows, width)")
+    return x.shape[0], x.shape[1]
+
+
+def _ids(x: torch.Tensor, name: str) -> str:
+    """The suffix of the entry points for ids of x's type."""
+    if x.dtype == torch.int64:
+        return "i64"
+    if x.dtype == torch.int32:
+        return "i32"
+    raise TypeError(f"{name} must be int32 or int64, not {x.dtype}")
+
+
+def _row_call(name: str, like: torch.Tensor, *args) -> None:
+    """_call on like's stream, with its device current."""
+    if like.get_device() == torch.cuda.current_device():
+        _call(name, getattr(lib(), name), *args, _stream(like))
+    else:
+        with torch.cuda.device(like.device):
+            _call(name, getattr(lib(), name), *args, _stream(like))
+
+
+def _work_bytes(scratch, like: torch.Tensor, nbytes: int) -> torch.Tensor | None:
+    """The caller's scratch, or a new one that needs no zeros (None for none)."""
+    if scratch is not None:
+        return _scratch(scratch, like, nbytes)
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
+def _numel(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.numel()
+
+
+def _optional(t, name: str, like: torch.Tensor, n: int) -> torch.Tensor | None:
+    """An int32 output that is wanted (True, or the tensor to write) or not."""
+    if t is True:
+        return torch.empty(n, dtype=torch.int32, device=like.device)
+    if t is None or t is False:
+        return None
+    return _need(t, name, like, (torch.int32,), n)
+
+
+def group_scratch_bytes(n: int, groups: int) -> int:
+    return int(lib().ssc_group_scratch_bytes(n, groups))
+
+
+def group_by_key(keys: torch.Tensor, groups: int, *, order=True, ranks=True,
+                 offsets: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
+    """(order, ranks, offsets): stable partition of int32 or int64 keys into
+    `groups` groups. ranks (of keys' shape) is each key's slot, -1 for a key
+    outside [0, groups); order[s] is the position (in the flattened keys) of
+    the key in slot s, its entries past offsets[groups] not written;
+    offsets[g] is the first slot of group g, offsets[groups] the number of
+    slots taken. order and ranks are True (a new tensor), False (None is
+    returned) or the int32 tensor to write."""
+    _dev(keys)
+    n = keys.numel()
+    name = "ssc_group_by_key_" + _ids(keys, "keys")
+    if not 1 <= groups < 2**31 - 1:
+        raise ValueError(f"groups must be in [1, 2^31 - 2], not {groups}")
+    order = _optional(order, "order", keys, n)
+    made = ranks is True
+    ranks = _optional(ranks, "ranks", keys, n)
+    if made and keys.dim() != 1:
+        ranks = ranks.view(keys.shape)
+    offsets = (torch.empty(groups + 1, dtype=torch.int32, device=keys.device) if offsets is None
+               else _need(offsets, "offsets", keys, (torch.int32,), groups + 1))
+    scratch = _work_bytes(scratch, keys, group_scratch_bytes(n, groups))
+    _row_call(name, keys, keys, n, groups, order, ranks, offsets, scratch, _numel(scratch))
+    return order, ranks, offsets
+
+
+def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[i] = scale * table[ids[i]], of shape (*ids.shape, width) and the
+    table's type (float32, bfloat16 or float16); an id outside the table
+    gives a row of zeros. ids are int32 or int64."""
+    _dev(table)
+    vocab, width = _rows(table, "table")
+    name = "ssc_embed_rows_" + _ids(ids, "ids") if isinstance(ids, torch.Tensor) else ""
+    n = _need(ids, "ids", table, None, 0).numel()
+    out = (torch.empty(*ids.shape, width, dtype=table.dtype, device=table.device) if out is None
+           else _need(out, "out", table, (table.dtype,), n * width))
+    _row_call(name, table, table, DTYPE[table.dtype], vocab, width, ids, n, scale, out)
+    return out
+
+
+def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, offsets: torch.Tensor,
+                    scale: float = 1.0, *, dtype: torch.dtype | None = None,
+                    out: torch.Tensor | None = None, accumulate: bool = False,
+                    scratch: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of embed_rows with respect to the table: out[v] = scale *
+    (sum of dout[i] over ids[i] = v), given order and offsets of
+    group_by_key(ids, vocab). dout is (*ids.shape, width); the gradient is
+    (vocab, width), of dout's type or float32 (`dtype`, or that of `out`).
+    accumulate=True adds to `out` and leaves its rows without tokens as they are."""
+    _dev(dout)
+    if dout.dtype not in DTYPE:
+        raise TypeError(f"dout holds float32, bfloat16 or float16 rows, not {dout.dtype}")
+    if dout.dim() < 1:
+        raise ValueError("dout is (*ids.shape, width)")
+    n = _need(ids, "ids", dout, None, 0).numel()
+    name = "ssc_embed_rows_grad_" + _ids(ids, "ids")
+    width = dout.shape[-1]
+    if dout.numel() != n * width:
+        raise ValueError("dout holds one row per id")
+    _need(order, "order", dout, (torch.int32,), n)
+    _need(offsets, "offsets", dout, (torch.int32,), 2)
+    vocab = offsets.numel() - 1
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to a given out")
+        out = torch.empty(vocab, width, dtype=dout.dtype if dtype is None else dtype, device=dout.device)
+    else:
+        _need(out, "out", dout, None, vocab * width)
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out is {out.dtype}, not {dtype}")
+    if out.dtype not in (dout.dtype, torch.float32):
+        raise TypeError("the gradient is of dout's dtype or float32")
+    scratch = _work_bytes(scratch, dout, int(lib().ssc_embed_grad_scratch_bytes(n, width)))
+    _row_call(name, dout, dout, DTYPE[dout.dtype], n, width, ids, order, offsets, vocab, scale, out,
+              DTYPE[out.dtype], int(accumulate), scratch, _numel(scratch))
+    return out
+
+
+def _routed(ranks: torch.Tensor, like: torch.Tensor, tokens: int | None) -> tuple[int, int]:
+    """(tokens, per) of ranks (tokens,) or (tokens, per)."""
+    _need(ranks, "ranks", like, (torch.int32,), 0)
+    if ranks.dim() not in (1, 2):
+        raise ValueError("ranks is (tokens,) or (tokens, per)")
+    if tokens is not None and ranks.shape[0] != tokens:
+        raise ValueError(f"ranks holds {ranks.shape[0]} tokens, the rows {tokens}")
+    return ranks.shape[0], ranks.shape[1] if ranks.dim() == 2 else 1
+
+
+def dispatch_rows(x: torch.Tensor, ranks: torch.Tensor, *, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[ranks[t, k]] = x[t]: each token's row to the slots that
+    group_by_key gave its assignments (ranks of shape (tokens, per) or
+    (tokens,)). out has tokens * per rows unless one is given; ranks that it
+    does not hold move nothing, and rows that no rank names are not written."""
+    _dev(x)
+    tokens, width = _rows(x, "x")
+    tokens, per = _routed(ranks, x, tokens)
+    if out is None:
+        out = torch.empty(tokens * per, width, dtype=x.dtype, device=x.device)
+    else:
+        _need(out, "out", x, (x.dtype,), 0)
+        if out.dim() != 2 or out.shape[1] != width:
+            raise ValueError("out has rows of x's width")
+    _row_call("ssc_dispatch_rows", x, x, DTYPE[x.dtype], tokens, per, width, ranks, out.shape[0], out)
+    return out
+
+
+def _weights(weights, like: torch.Tensor, ranks: torch.Tensor) -> torch.Tensor:
+    _need(weights, "weights", like, (torch.float32,), 0)
+    if weights.shape != ranks.shape:
+        raise ValueError("one weight per rank")
+    return weights
+
+
+def combine_rows(y: torch.Tensor, ranks: torch.Tensor, weights: torch.Tensor | None = None, *,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = sum over k of weights[t, k] * y[ranks[t, k]], (tokens, width):
+    the rows of a token's assignments weighted (float32; None for ones) and
+    summed in float32. A rank that y does not hold adds nothing."""
+    _dev(y)
+    rows, width = _rows(y, "y")
+    tokens, per = _routed(ranks, y, None)
+    if weights is not None:
+        _weights(weights, y, ranks)
+    out = (torch.empty(tokens, width, dtype=y.dtype, device=y.device) if out is None
+           else _need(out, "out", y, (y.dtype,), tokens * width))
+    _row_call("ssc_combine_rows", y, y, DTYPE[y.dtype], rows, width, ranks, weights, tokens, per, out)
+    return out
+
+
+def dispatch_rows_grad(dout: torch.Tensor, ranks: torch.Tensor, *,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of dispatch_rows with respect to x: dx[t] = sum over k of
+    dout[ranks[t, k]] (combine_rows without weights)."""
+    return combine_rows(dout, ranks, out=out)
+
+
+def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, ranks: torch.Tensor, weights: torch.Tensor, *,
+                      dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None):
+    """(dy, dweights): the gradients of combine_rows with respect to y and the
+    weights: dy[ranks[t, k]] = weights[t, k] * dout[t], dweights[t, k] =
+    <dout[t], y[ranks[t, k]]> (0 for a rank that y does not hold). Rows of dy
+    that no rank names are not written. Without weights the gradient is
+    dispatch_rows(dout, ranks)."""
+    _dev(dout)
+    tokens, width = _rows(dout, "dout")
+    tokens, per = _routed(ranks, dout, tokens)
+    _need(y, "y", dout, (dout.dtype,), 0)
+    rows, ywidth = _rows(y, "y")
+    if ywidth != width:
+        raise ValueError("y has rows of dout's width")
+    _weights(weights, dout, ranks)
+    dy = torch.empty_like(y) if dy is None else _need(dy, "dy", dout, (dout.dtype,), rows * width)
+    dweights = (torch.empty_like(weights) if dweights is None
+                else _need(dweights, "dweights", dout, (torch.float32,), tokens * per))
+    _row_call("ssc_combine_rows_grad", dout, dout, y, DTYPE[dout.dtype], rows, width, ranks, weights, tokens, per,
+              dy, dweights)
+    return dy, dweights
+
+
+def sample_scratch_bytes(rows: int, vocab: int) -> int:
+    return int(lib().ssc_sample_scratch_bytes(rows, vocab))
+
+
+def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+                top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                min_p: torch.Tensor | None = None, *, tokens: torch.Tensor | None = None,
+                kept: torch.Tensor | None = None, logprobs: torch.Tensor | None = None,
+                scratch: torch.Tensor | None = None):
+    """(tokens, kept, logprobs): the next token of each row of logits (rows,
+    vocab), from a random number u (float32, [0, 1)) and the row's settings,
+    one value a row each (None: off; top_k int32, the others float32). tokens
+    is int32, -1 for a row without a token; kept the number of tokens that the
+    filters left; logprobs the logarithm of the token's share of their weight.
+    The rows may lie apart (a stride of the first dimension of at least vocab);
+    include/ssc.h states the rules."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("arguments must be torch tensors")
+    if not logits.is_cuda:
+        raise ValueError("tensors must be on the GPU (no CPU path)")
+    rows, vocab = _rows(logits, "logits")
+    stride = logits.stride(0) if rows > 1 else max(vocab, 1)
+    if (vocab > 1 and logits.stride(1) != 1) or stride < vocab:
+        raise ValueError("a row of logits is contiguous, and rows do not overlap")
+    settings = []
+    for t, name, dt in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
+                        (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                        (min_p, "min_p", torch.float32)):
+        if t is None and name != "u":
+            settings.append(None)
+            continue
+        _need(t, name, logits, (dt,), rows)
+        if t.numel() != rows:
+            raise ValueError(f"{name} holds one value a row")
+        settings.append(t)
+    tokens, kept, logprobs = (
+        torch.empty(rows, dtype=dt, device=logits.device) if t is None else _need(t, name, logits, (dt,), rows)
+        for t, name, dt in ((tokens, "tokens", torch.int32), (kept, "kept", torch.int32),
+                            (logprobs, "logprobs", torch.float32)))
+    scratch = _work_bytes(scratch, logits, sample_scratch_bytes(rows, vocab))
+    _row_call("ssc_sample_rows", logits, logits, DTYPE[logits.dtype], rows, vocab, stride, *settings, tokens, kept,
+              logprobs, scratch, _numel(scratch))
+    return tokens, kept, logprobs

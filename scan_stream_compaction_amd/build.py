@@ -18,10 +18,13 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "ssc.hip")
+CSRC = os.path.join(PKG, "csrc")
+SOURCE = "ssc.hip"                          # its code follows the test builds' switches
+SHARED_SOURCES = ("rows.hip", "sample.hip")  # the same in every build
 LIB = os.path.join(PKG, "libssc.so")
 PERTURB_LIB = os.path.join(PKG, "libssc_perturb.so")
 STRESS_LIB = os.path.join(PKG, "libssc_stress.so")
@@ -42,37 +45,45 @@ def flags() -> list[str]:
         # Packed fp32 instructions stay off: the compiler must not form them.
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall", "-Wno-unused-command-line-argument",
-        "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+        "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     ]
 
 
-def _command(out: str, defines: list[str], asm_dir: str | None) -> tuple[list[str], str]:
-    cmd = [hipcc(), *flags(), *defines, "-shared", SRC, "-o", out]
+def _compile(name: str, defines: list[str], out: str, asm_dir: str | None) -> subprocess.Popen:
+    cmd = [hipcc(), *flags(), *defines, "-c", os.path.join(CSRC, name), "-o", out]
     cwd = ROOT
     if asm_dir:
         # intermediate files (device ISA included) go next to the output
         os.makedirs(asm_dir, exist_ok=True)
         cmd += ["-save-temps=cwd"]
         cwd = asm_dir
-    return cmd, cwd
+    return subprocess.Popen(cmd, cwd=cwd)
 
 
 def build(asm_dir: str | None = None, only: str | None = None) -> list[str]:
-    """Compile the library and the two test builds (or only the one named)
-    in parallel; each output is replaced only once it is complete."""
-    jobs = []
-    for name, out, defines in (("lib", LIB, []), ("perturb", PERTURB_LIB, ["-DSSC_PERTURB=1"]),
-                               ("stress", STRESS_LIB, ["-DSSC_STRESS_TILES=1"])):
-        if only and only != name:
-            continue
-        cmd, cwd = _command(out + ".tmp", defines, asm_dir if name == "lib" else None)
-        jobs.append((out, subprocess.Popen(cmd, cwd=cwd)))
-    failed = [out for out, p in jobs if p.wait() != 0]
-    if failed:
-        raise RuntimeError(f"hipcc failed for {', '.join(failed)}")
-    for out, _ in jobs:
-        os.replace(out + ".tmp", out)
-    return [out for out, _ in jobs]
+    """Compile the library and the two test builds (or only the one named);
+    the sources compile in parallel, those that the test builds' switches do
+    not touch once. Each library is replaced only once it is complete."""
+    wanted = [v for v in (("lib", LIB, []), ("perturb", PERTURB_LIB, ["-DSSC_PERTURB=1"]),
+                          ("stress", STRESS_LIB, ["-DSSC_STRESS_TILES=1"])) if not only or only == v[0]]
+    with tempfile.TemporaryDirectory() as tmp:
+        jobs = []
+        for name in SHARED_SOURCES:
+            jobs.append((name, _compile(name, [], os.path.join(tmp, name + ".o"), asm_dir)))
+        for variant, _, defines in wanted:
+            jobs.append((f"{SOURCE} ({variant})",
+                         _compile(SOURCE, defines, os.path.join(tmp, variant + ".o"),
+                                  asm_dir if variant == "lib" else None)))
+        failed = [name for name, p in jobs if p.wait() != 0]
+        if failed:
+            raise RuntimeError(f"hipcc failed for {', '.join(failed)}")
+        shared = [os.path.join(tmp, name + ".o") for name in SHARED_SOURCES]
+        for variant, out, _ in wanted:
+            subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC",
+                            os.path.join(tmp, variant + ".o"), *shared, "-o", out + ".tmp"],
+                           cwd=ROOT, check=True)
+            os.replace(out + ".tmp", out)
+    return [out for _, out, _ in wanted]
 
 
 if __name__ == "__main__":
