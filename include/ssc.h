@@ -379,8 +379,8 @@ typedef enum ssc_dtype {
  *   - Row, token and group counts are at most INT32_MAX (groups and vocab of
  *     the grouping and the gradient: INT32_MAX - 1); larger ones give
  *     SSC_ERR_SIZE.
- *   - Scratch needs no initialisation and keeps nothing between calls; one
- *     buffer must not serve two calls that may run at the same time. Where
+ *   - Scratch is 16-byte aligned, needs no initialisation and keeps nothing
+ *     between calls; one buffer must not serve two calls that may run at the same time. Where
  *     the size function returns 0 it may be NULL.
  *   - Ids, ranks and positions read from device memory are checked there: one
  *     out of its range moves nothing and adds nothing, and nothing outside the
@@ -391,7 +391,8 @@ typedef enum ssc_dtype {
  *     depends on the sizes and the ranks only, so a call repeats bit for bit.
  */
 
-/* Scratch bytes of a grouping of n keys (0 for up to 16,384 keys). */
+/* Scratch bytes of a grouping of n keys (0 for up to 4096 keys of at most 511
+ * groups). */
 size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
 
 /* Stable partition into `groups` groups: key k belongs to group k, and one
@@ -403,7 +404,8 @@ size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
  *   order[s]   = the i with ranks[i] = s, for s < offsets[groups]; the
  *                entries past that are not written               (nullable)
  * The many-way form of ssc_partition_i32: one counting and one scattering
- * step per 9 bits of group number (a single launch for up to 16,384 keys). */
+ * step per 9 bits of group number (a single launch for up to 4096 keys of at
+ * most 511 groups). */
 int ssc_group_by_key_i32(const int32_t *keys, int64_t n, int64_t groups, int32_t *order,
                          int32_t *ranks, int32_t *offsets, void *scratch, size_t scratch_bytes,
                          void *stream);

@@ -25,6 +25,8 @@
 namespace ssc {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // =============================================== stable partition by key ---
 // An LSD sort of (key, position) by digits of at most 9 bits: `groups`
 // values and one more for keys outside [0, groups), which sort last and are
@@ -37,9 +39,7 @@ constexpr int kGroupBlock = 1024;
 constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kGroupSmall = 16 * kGroupBlock;   // keys one workgroup sorts alone
-constexpr int kGroupItems = 8;                  // keys per thread and step of the tiled form
-constexpr int kGroupStep = kGroupItems * kGroupBlock;
+constexpr int kGroupSmall = 4 * kGroupBlock;    // keys one workgroup sorts alone
 constexpr int kGroupTiles = 256;                // most workgroups of a tiled pass
 
 template <class K>
@@ -93,58 +93,18 @@ __device__ __forceinline__ uint32_t counts_before(uint32_t (*cnt)[kDigits], uint
     return total;
 }
 
-// offsets[v] for every v whose first sorted position lies in [s0, s1), with
-// position n standing for the group after the last: the position s with key
-// k after key p starts groups p + 1 .. k. Long gaps between present keys are
-// filled by the whole workgroup.
-struct GapList {
-    uint32_t count;
-    uint32_t lo[kGroupBlock], hi[kGroupBlock], at[kGroupBlock];
-};
-constexpr uint32_t kGapLong = 32;
-
-template <class F>
-__device__ __forceinline__ void fill_offsets(F key, uint32_t s0, uint32_t s1, uint32_t n, uint32_t groups,
-                                             int32_t *__restrict__ offsets, GapList &gaps) {
-    for (uint32_t base = s0; base < s1; base += kGroupBlock) {
-        if (threadIdx.x == 0) gaps.count = 0;
-        __syncthreads();
-        const uint32_t s = base + threadIdx.x;
-        if (s < s1) {
-            const uint32_t lo = s == 0 ? 0u : key(s - 1) + 1u;
-            const uint32_t end = (s < n ? key(s) : groups) + 1u;  // keys stop at groups <= INT32_MAX
-            if (lo < end) {
-                if (end - lo <= kGapLong) {
-                    for (uint32_t v = lo; v < end; ++v) offsets[v] = static_cast<int32_t>(s);
-                } else {
-                    const uint32_t e = __hip_atomic_fetch_add(&gaps.count, 1u, __ATOMIC_RELAXED,
-                                                              __HIP_MEMORY_SCOPE_WORKGROUP);
-                    gaps.lo[e] = lo;
-                    gaps.hi[e] = end;
-                    gaps.at[e] = s;
-                }
-            }
-        }
-        __syncthreads();
-        for (uint32_t e = 0; e < gaps.count; ++e)
-            for (uint32_t v = gaps.lo[e] + threadIdx.x; v < gaps.hi[e]; v += kGroupBlock)
-                offsets[v] = static_cast<int32_t>(gaps.at[e]);
-        __syncthreads();
-    }
-}
-
-// Up to 16,384 keys: one workgroup holds (key, position) in registers and
+// Up to 4096 keys: one workgroup holds (key, position) in registers and
 // exchanges them through LDS between passes.
 template <class K, int ITEMS>
 __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
     const K *__restrict__ keys, uint32_t n, uint32_t groups, int passes, int bits,
-    int32_t *__restrict__ order, int32_t *__restrict__ ranks, int32_t *__restrict__ offsets) {
+    int32_t *__restrict__ order, int32_t *__restrict__ ranks, int32_t *__restrict__ offsets,
+    uint32_t *__restrict__ sorted_out) {
     __shared__ uint32_t s_key[ITEMS * kGroupBlock];
     __shared__ uint16_t s_pos[ITEMS * kGroupBlock];
     __shared__ uint32_t s_cnt[kGroupWaves][kDigits];
     __shared__ uint32_t s_start[kDigits];
     __shared__ uint32_t s_wave[kGroupWaves];
-    __shared__ GapList s_gaps;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t digits = 1u << bits;
@@ -175,10 +135,11 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
             if (first + j * kWave >= n) continue;
             const uint32_t d = (key[j] >> shift) & (digits - 1);
             const uint32_t at = s_start[d] + s_cnt[w][d] + rk[j];
-            s_key[at] = key[j];
             if (!last) {
+                s_key[at] = key[j];
                 s_pos[at] = static_cast<uint16_t>(pos[j]);
             } else {
+                if (passes > 1) sorted_out[at] = key[j];
                 const bool kept = key[j] < groups;
                 if (order != nullptr && kept) order[at] = static_cast<int32_t>(pos[j]);
                 if (ranks != nullptr) ranks[pos[j]] = kept ? static_cast<int32_t>(at) : -1;
@@ -196,15 +157,12 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
             }
         }
     }
-    if (passes == 1) {  // the digit starts are the offsets
-        if (threadIdx.x <= groups) offsets[threadIdx.x] = static_cast<int32_t>(s_start[threadIdx.x]);
-    } else {
-        fill_offsets([&](uint32_t s) { return s_key[s]; }, 0, n + 1, n, groups, offsets, s_gaps);
-    }
+    // the digit starts of a single pass are the offsets
+    if (passes == 1 && threadIdx.x <= groups) offsets[threadIdx.x] = static_cast<int32_t>(s_start[threadIdx.x]);
 }
 
 // The tiled form: a pass is a counting launch and a scattering launch, each
-// of up to 256 workgroups that take one span of the keys in steps of 8192.
+// of up to 256 workgroups that take one span of the keys in steps.
 // table[t][d] = keys of span t with digit d.
 template <class K>
 __device__ __forceinline__ uint32_t pass_key(const K *keys, const uint32_t *sorted, uint32_t i, uint32_t groups) {
@@ -229,41 +187,41 @@ __global__ __launch_bounds__(kGroupBlock) void group_count_kernel(
     if (threadIdx.x < digits) table[blockIdx.x * digits + threadIdx.x] = s_cnt[threadIdx.x];
 }
 
-template <class K>
+template <class K, int ITEMS>
 __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
     const K *__restrict__ keys, const uint32_t *__restrict__ sorted, const uint32_t *__restrict__ positions,
     uint32_t n, uint32_t span, uint32_t groups, int shift, int bits, const uint32_t *__restrict__ table,
     uint32_t *__restrict__ sorted_out, uint32_t *__restrict__ positions_out,
     int32_t *__restrict__ order, int32_t *__restrict__ ranks, int32_t *__restrict__ offsets) {
     __shared__ uint32_t s_cnt[kGroupWaves][kDigits];
-    __shared__ uint32_t s_part[2][2][kDigits];
+    __shared__ __attribute__((aligned(16))) uint32_t s_part[2][4 * kGroupBlock];
     __shared__ uint32_t s_base[kDigits];
     __shared__ uint32_t s_wave[kGroupWaves];
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t digits = 1u << bits;
     // where this span's first key of each digit goes: the keys of smaller
-    // digits, then those of the same digit in earlier spans; each half of
-    // the workgroup sums half of the table
+    // digits, then those of the same digit in earlier spans; a thread sums
+    // four digits over every parts-th row of the table
     {
-        const uint32_t d = threadIdx.x % kDigits, half = threadIdx.x / kDigits;
-        uint32_t before = 0, all = 0;
-        if (d < digits) {
-#pragma unroll 8
-            for (uint32_t t = half; t < gridDim.x; t += 2) {
-                const uint32_t c = table[t * digits + d];
-                all += c;
-                before += t < blockIdx.x ? c : 0u;
-            }
+        const uint32_t d = (4 * threadIdx.x) & (digits - 1), parts = (4 * kGroupBlock) >> bits;
+        u32x4 before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+#pragma unroll 16
+        for (uint32_t t = (4 * threadIdx.x) >> bits; t < gridDim.x; t += parts) {
+            const u32x4 c = *reinterpret_cast<const u32x4 *>(table + t * digits + d);
+            all += c;
+            before += t < blockIdx.x ? c : u32x4{0, 0, 0, 0};
         }
-        s_part[half][0][d] = before;
-        s_part[half][1][d] = all;
+        *reinterpret_cast<u32x4 *>(&s_part[0][4 * threadIdx.x]) = before;
+        *reinterpret_cast<u32x4 *>(&s_part[1][4 * threadIdx.x]) = all;
     }
     __syncthreads();
     uint32_t total = 0, base = 0;
     if (threadIdx.x < digits) {
-        total = s_part[0][1][threadIdx.x] + s_part[1][1][threadIdx.x];
-        base = s_part[0][0][threadIdx.x] + s_part[1][0][threadIdx.x];
+        for (uint32_t i = threadIdx.x; i < 4 * kGroupBlock; i += digits) {
+            base += s_part[0][i];
+            total += s_part[1][i];
+        }
     }
     const uint32_t start = block_exclusive(total, s_wave);
     if (threadIdx.x < digits) {
@@ -273,25 +231,25 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
     }
     const uint32_t begin = blockIdx.x * span;
     const uint32_t end = n - begin < span ? n : begin + span;
-    for (uint32_t step = begin; step < end; step += kGroupStep) {
+    for (uint32_t step = begin; step < end; step += ITEMS * kGroupBlock) {
         for (uint32_t d = threadIdx.x; d < digits * kGroupWaves; d += kGroupBlock)
             s_cnt[d >> bits][d & (digits - 1)] = 0;
-        const uint32_t first = step + static_cast<uint32_t>(w) * kWave * kGroupItems + lane;
-        uint32_t key[kGroupItems], rk[kGroupItems];
+        const uint32_t first = step + static_cast<uint32_t>(w) * kWave * ITEMS + lane;
+        uint32_t key[ITEMS], rk[ITEMS];
 #pragma unroll
-        for (int j = 0; j < kGroupItems; ++j) {
+        for (int j = 0; j < ITEMS; ++j) {
             const uint32_t i = first + j * kWave;
             key[j] = i < end ? pass_key(keys, sorted, i, groups) : 0u;
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kGroupItems; ++j)
+        for (int j = 0; j < ITEMS; ++j)
             rk[j] = digit_rank((key[j] >> shift) & (digits - 1), first + j * kWave < end, bits, s_cnt[w]);
         __syncthreads();
         const uint32_t count = counts_before(s_cnt, digits);
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kGroupItems; ++j) {
+        for (int j = 0; j < ITEMS; ++j) {
             const uint32_t i = first + j * kWave;
             if (i >= end) continue;
             const uint32_t d = (key[j] >> shift) & (digits - 1);
@@ -312,13 +270,38 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
     }
 }
 
+// offsets[v] = number of sorted keys below v, by bisection: first among up
+// to 4096 keys at even distances, in LDS, then between two of them.
+constexpr uint32_t kSamples = 4096;
+
 __global__ __launch_bounds__(kGroupBlock) void group_offsets_kernel(const uint32_t *__restrict__ sorted,
                                                                    uint32_t n, uint32_t groups,
                                                                    int32_t *__restrict__ offsets) {
-    __shared__ GapList s_gaps;
-    const uint32_t s0 = blockIdx.x * kGroupBlock;
-    const uint32_t s1 = n + 1 - s0 < kGroupBlock ? n + 1 : s0 + kGroupBlock;
-    fill_offsets([&](uint32_t s) { return sorted[s]; }, s0, s1, n, groups, offsets, s_gaps);
+    __shared__ uint32_t s_key[kSamples];
+    const uint32_t stride = (n + kSamples - 1) / kSamples;
+    const uint32_t samples = n / stride;  // the last of each whole stride
+    for (uint32_t i = threadIdx.x; i < samples; i += kGroupBlock) s_key[i] = sorted[(i + 1) * stride - 1];
+    __syncthreads();
+    const uint32_t v = blockIdx.x * kGroupBlock + threadIdx.x;
+    if (v > groups) return;
+    uint32_t lo = 0, hi = samples;  // strides that end below v
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (s_key[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    hi = lo < samples ? (lo + 1) * stride - 1 : n;
+    lo *= stride;
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (sorted[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    offsets[v] = static_cast<int32_t>(lo);
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(uint32_t *__restrict__ p, int64_t words) {
@@ -333,37 +316,60 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(uint32_t *__restrict__ p
 // no alignment beyond their element's: gfx950 takes unaligned 16-byte
 // global accesses.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 template <class T, bool VEC>
 struct Chunk {
     static constexpr int kN = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
-    float f[kN];
+    typedef T V __attribute__((ext_vector_type(kN)));
+    using Raw = std::conditional_t<VEC, u32x4, T>;
 
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) f[e] = 0.0f;
+    __device__ static __forceinline__ Raw load(const T *p) {
+        if constexpr (VEC)
+            return *reinterpret_cast<const u32x4_any *>(p);
+        else
+            return *p;
     }
-    __device__ __forceinline__ void load(const T *p) {
-        typedef T V __attribute__((ext_vector_type(kN)));
+    __device__ static __forceinline__ void store(T *p, Raw r) {
+        if constexpr (VEC)
+            *reinterpret_cast<u32x4_any *>(p) = r;
+        else
+            *p = r;
+    }
+    // what a call reads or writes once goes past the caches
+    __device__ static __forceinline__ Raw load_stream(const T *p) {
+        if constexpr (VEC)
+            return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+        else
+            return *p;
+    }
+    __device__ static __forceinline__ void store_stream(T *p, Raw r) {
+        if constexpr (VEC)
+            __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any *>(p));
+        else
+            *p = r;
+    }
+    __device__ static __forceinline__ Raw none() {
+        if constexpr (VEC)
+            return u32x4{0, 0, 0, 0};
+        else
+            return static_cast<T>(0.0f);
+    }
+    __device__ static __forceinline__ void unpack(Raw r, float *f) {
         if constexpr (VEC) {
-            const u32x4 r = *reinterpret_cast<const u32x4_any *>(p);
             const V v = __builtin_bit_cast(V, r);
 #pragma unroll
             for (int e = 0; e < kN; ++e) f[e] = static_cast<float>(v[e]);
         } else {
-            f[0] = static_cast<float>(*p);
+            f[0] = static_cast<float>(r);
         }
     }
-    __device__ __forceinline__ void store(T *p) const {
-        typedef T V __attribute__((ext_vector_type(kN)));
+    __device__ static __forceinline__ Raw pack(const float *f) {
         if constexpr (VEC) {
             V v;
 #pragma unroll
             for (int e = 0; e < kN; ++e) v[e] = static_cast<T>(f[e]);
-            *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4, v);
+            return __builtin_bit_cast(u32x4, v);
         } else {
-            *p = static_cast<T>(f[0]);
+            return static_cast<T>(f[0]);
         }
     }
 };
@@ -371,31 +377,21 @@ struct Chunk {
 // N fp32 values to and from consecutive elements of type G.
 template <class G, int N>
 __device__ __forceinline__ void load_values(const G *p, float *f) {
-    constexpr bool VEC = sizeof(G) * N % 16 == 0;
-    using C = Chunk<G, VEC>;
+    using C = Chunk<G, sizeof(G) * N % 16 == 0>;
 #pragma unroll
-    for (int i = 0; i < N / C::kN; ++i) {
-        C v;
-        v.load(p + i * C::kN);
-#pragma unroll
-        for (int e = 0; e < C::kN; ++e) f[i * C::kN + e] = v.f[e];
-    }
+    for (int i = 0; i < N / C::kN; ++i) C::unpack(C::load(p + i * C::kN), f + i * C::kN);
 }
 template <class G, int N>
 __device__ __forceinline__ void store_values(G *p, const float *f) {
-    constexpr bool VEC = sizeof(G) * N % 16 == 0;
-    using C = Chunk<G, VEC>;
+    using C = Chunk<G, sizeof(G) * N % 16 == 0>;
 #pragma unroll
-    for (int i = 0; i < N / C::kN; ++i) {
-        C v;
-#pragma unroll
-        for (int e = 0; e < C::kN; ++e) v.f[e] = f[i * C::kN + e];
-        v.store(p + i * C::kN);
-    }
+    for (int i = 0; i < N / C::kN; ++i) C::store_stream(p + i * C::kN, C::pack(f + i * C::kN));
 }
 
 // Which row and which of its chunks a thread works on: 2^lg threads to a
-// row, the column blocks in gridDim.y.
+// row, the column blocks in gridDim.y. WAVE: whole wavefronts to a row (lg >=
+// 6), whose ids, ranks and weights then come through scalar loads. CH: chunks
+// that a thread has in flight at a time.
 struct RowMap {
     int lg;          // log2 of the threads of a row (0 .. 8)
     int chunks;      // chunks of a row
@@ -403,90 +399,117 @@ struct RowMap {
 };
 constexpr int kRowBlock = 256;
 
+template <bool WAVE>
 __device__ __forceinline__ int64_t row_of(const RowMap &m) {
     const uint32_t sub = threadIdx.x >> m.lg;
-    return (static_cast<int64_t>(blockIdx.x) << (8 - m.lg)) + (m.lg >= 6 ? uniform(sub) : sub);
+    return (static_cast<int64_t>(blockIdx.x) << (8 - m.lg)) + (WAVE ? uniform(sub) : sub);
 }
 __device__ __forceinline__ int col_of(const RowMap &m) {
     return static_cast<int>((blockIdx.y << m.lg) + (threadIdx.x & ((1u << m.lg) - 1u)));
 }
 __device__ __forceinline__ int col_step(const RowMap &m) { return static_cast<int>(gridDim.y << m.lg); }
 
+// Where chunk c starts; one past the last stands for the last, which a
+// thread may read again but does not write.
 template <int N>
-__device__ __forceinline__ int chunk_start(int c, int width) {
-    const int at = c * N;
-    return at + N <= width ? at : width - N;
+__device__ __forceinline__ int chunk_start(int c, const RowMap &m) {
+    const int at = (c < m.chunks ? c : m.chunks - 1) * N;
+    return at + N <= m.width ? at : m.width - N;
 }
 
-template <class T, bool VEC, class I>
+template <class T, bool VEC, bool WAVE, int CH, class I>
 __global__ __launch_bounds__(kRowBlock) void embed_kernel(const T *__restrict__ table, int64_t vocab,
                                                           const I *__restrict__ ids, int64_t n, float scale,
                                                           T *__restrict__ out, RowMap m) {
     using C = Chunk<T, VEC>;
-    const int64_t row = row_of(m);
+    const int64_t row = row_of<WAVE>(m);
     if (row >= n) return;
     const int64_t id = ids[row];
     const bool inside = id >= 0 && id < vocab;
     const T *src = table + (inside ? id : 0) * m.width;
     T *dst = out + row * m.width;
-    for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-        const int at = chunk_start<C::kN>(c, m.width);
-        C x;
-        x.zero();
-        if (inside) x.load(src + at);
+    const int step = col_step(m);
+    for (int c0 = col_of(m); c0 < m.chunks; c0 += CH * step) {
+        typename C::Raw r[CH];
 #pragma unroll
-        for (int e = 0; e < C::kN; ++e) x.f[e] *= scale;
-        x.store(dst + at);
-    }
-}
-
-template <class T, bool VEC>
-__global__ __launch_bounds__(kRowBlock) void dispatch_kernel(const T *__restrict__ x, int64_t tokens, int per,
-                                                             const int32_t *__restrict__ ranks, int64_t rows,
-                                                             T *__restrict__ out, RowMap m) {
-    using C = Chunk<T, VEC>;
-    const int64_t t = row_of(m);
-    if (t >= tokens) return;
-    const T *src = x + t * m.width;
-    const int32_t *rk = ranks + t * per;
-    for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-        const int at = chunk_start<C::kN>(c, m.width);
-        C v;
-        v.load(src + at);
-        for (int k = 0; k < per; ++k) {
-            const int64_t r = rk[k];
-            if (r >= 0 && r < rows) v.store(out + r * m.width + at);
+        for (int j = 0; j < CH; ++j) r[j] = inside ? C::load(src + chunk_start<C::kN>(c0 + j * step, m)) : C::none();
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float f[C::kN];
+            C::unpack(r[j], f);
+#pragma unroll
+            for (int e = 0; e < C::kN; ++e) f[e] = inside ? f[e] * scale : 0.0f;
+            if (c0 + j * step < m.chunks) C::store_stream(dst + chunk_start<C::kN>(c0 + j * step, m), C::pack(f));
         }
     }
 }
 
-template <class T, bool VEC, bool WEIGHTED>
+template <class T, bool VEC, bool WAVE, int CH>
+__global__ __launch_bounds__(kRowBlock) void dispatch_kernel(const T *__restrict__ x, int64_t tokens, int per,
+                                                             const int32_t *__restrict__ ranks, int64_t rows,
+                                                             T *__restrict__ out, RowMap m) {
+    using C = Chunk<T, VEC>;
+    const int64_t t = row_of<WAVE>(m);
+    if (t >= tokens) return;
+    const T *src = x + t * m.width;
+    const int32_t *rk = ranks + t * per;
+    const int step = col_step(m);
+    for (int c0 = col_of(m); c0 < m.chunks; c0 += CH * step) {
+        typename C::Raw r[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) r[j] = C::load(src + chunk_start<C::kN>(c0 + j * step, m));
+        for (int k = 0; k < per; ++k) {
+            const int64_t slot = rk[k];
+            if (slot < 0 || slot >= rows) continue;
+            T *dst = out + slot * m.width;
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (c0 + j * step < m.chunks) C::store_stream(dst + chunk_start<C::kN>(c0 + j * step, m), r[j]);
+        }
+    }
+}
+
+// The rows of kPer assignments are in flight together; an assignment without
+// a row loads row 0 and adds nothing.
+constexpr int kPer = 8;
+
+template <class T, bool VEC, bool WAVE, bool WEIGHTED>
 __global__ __launch_bounds__(kRowBlock) void combine_kernel(const T *__restrict__ y, int64_t rows,
                                                             const int32_t *__restrict__ ranks,
                                                             const float *__restrict__ weights, int64_t tokens,
                                                             int per, T *__restrict__ out, RowMap m) {
     using C = Chunk<T, VEC>;
-    const int64_t t = row_of(m);
+    const int64_t t = row_of<WAVE>(m);
     if (t >= tokens) return;
     const int32_t *rk = ranks + t * per;
     const float *wt = weights + t * per;
     for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-        const int at = chunk_start<C::kN>(c, m.width);
-        C acc;
-        acc.zero();
-#pragma unroll 4
-        for (int k = 0; k < per; ++k) {
-            const int64_t r = rk[k];
-            const bool ok = r >= 0 && r < rows;
-            const float w = WEIGHTED ? wt[k] : 1.0f;
-            if (ok) {
-                C v;
-                v.load(y + r * m.width + at);
+        const int at = chunk_start<C::kN>(c, m);
+        float acc[C::kN];
 #pragma unroll
-                for (int e = 0; e < C::kN; ++e) acc.f[e] = __builtin_fmaf(w, v.f[e], acc.f[e]);
+        for (int e = 0; e < C::kN; ++e) acc[e] = 0.0f;
+        for (int k0 = 0; rows > 0 && k0 < per; k0 += kPer) {
+            typename C::Raw r[kPer];
+            float w[kPer];
+            bool ok[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (k0 + j >= per) continue;
+                const int64_t slot = rk[k0 + j];
+                ok[j] = slot >= 0 && slot < rows;
+                w[j] = WEIGHTED ? wt[k0 + j] : 1.0f;
+                r[j] = C::load_stream(y + (ok[j] ? slot : 0) * m.width + at);
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (k0 + j >= per || !ok[j]) continue;
+                float v[C::kN];
+                C::unpack(r[j], v);
+#pragma unroll
+                for (int e = 0; e < C::kN; ++e) acc[e] = __builtin_fmaf(w[j], v[e], acc[e]);
             }
         }
-        acc.store(out + t * m.width + at);
+        C::store_stream(out + t * m.width + at, C::pack(acc));
     }
 }
 
@@ -505,54 +528,62 @@ __device__ __forceinline__ float row_sum(float v, int lg, float *s_wave) {
 }
 
 // One token's dout row meets its `per` rows of y: each chunk of dout is read
-// once for up to kGradPer of them.
-constexpr int kGradPer = 8;
-
-template <class T, bool VEC>
+// once for up to kPer of them.
+template <class T, bool VEC, bool WAVE>
 __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
     const T *__restrict__ dout, const T *__restrict__ y, int64_t rows, const int32_t *__restrict__ ranks,
     const float *__restrict__ weights, int64_t tokens, int per, T *__restrict__ dy,
     float *__restrict__ dweights, RowMap m) {
     using C = Chunk<T, VEC>;
     __shared__ float s_wave[kRowBlock / kWave];
-    const int64_t row = row_of(m);
-    const bool live = row < tokens;       // threads of no row still meet the barriers
-    const int64_t t = live ? row : tokens - 1;
+    const int64_t row = row_of<WAVE>(m);
+    const bool live = row < tokens && rows > 0;  // the other threads still meet the barriers
+    const int64_t t = row < tokens ? row : tokens - 1;
     const int32_t *rk = ranks + t * per;
     const float *wt = weights + t * per;
     const T *src = dout + t * m.width;
-    for (int k0 = 0; k0 < per; k0 += kGradPer) {
-        float dot[kGradPer];
+    for (int k0 = 0; k0 < per; k0 += kPer) {
+        float dot[kPer];
 #pragma unroll
-        for (int j = 0; j < kGradPer; ++j) dot[j] = 0.0f;
+        for (int j = 0; j < kPer; ++j) dot[j] = 0.0f;
         if (live) {
             for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-                const int at = chunk_start<C::kN>(c, m.width);
+                const int at = chunk_start<C::kN>(c, m);
                 const int skip = c * C::kN - at;
-                C d;
-                d.load(src + at);
+                const typename C::Raw dr = C::load(src + at);
+                typename C::Raw r[kPer];
 #pragma unroll
-                for (int j = 0; j < kGradPer; ++j) {
+                for (int j = 0; j < kPer; ++j) {
                     if (k0 + j >= per) continue;
-                    const int64_t r = rk[k0 + j];
-                    if (r < 0 || r >= rows) continue;
+                    const int64_t slot = rk[k0 + j];
+                    r[j] = C::load_stream(y + (slot >= 0 && slot < rows ? slot : 0) * m.width + at);
+                }
+                float d[C::kN], own[C::kN];
+                C::unpack(dr, d);
+#pragma unroll
+                for (int e = 0; e < C::kN; ++e) own[e] = e >= skip ? d[e] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (k0 + j >= per) continue;
+                    const int64_t slot = rk[k0 + j];
+                    if (slot < 0 || slot >= rows) continue;
                     const float w = wt[k0 + j];
-                    C v, g;
-                    v.load(y + r * m.width + at);
+                    float v[C::kN], g[C::kN];
+                    C::unpack(r[j], v);
 #pragma unroll
                     for (int e = 0; e < C::kN; ++e) {
-                        g.f[e] = w * d.f[e];
-                        dot[j] = __builtin_fmaf(e >= skip ? d.f[e] : 0.0f, e >= skip ? v.f[e] : 0.0f, dot[j]);
+                        g[e] = w * d[e];
+                        dot[j] = __builtin_fmaf(own[e], e >= skip ? v[e] : 0.0f, dot[j]);
                     }
-                    g.store(dy + r * m.width + at);
+                    C::store_stream(dy + slot * m.width + at, C::pack(g));
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < kGradPer; ++j) {
+        for (int j = 0; j < kPer; ++j) {
             if (k0 + j >= per) break;  // the same in every thread
             const float s = row_sum(dot[j], m.lg, s_wave);
-            if (live && (threadIdx.x & ((1u << m.lg) - 1u)) == 0) dweights[t * per + k0 + j] = s;
+            if (row < tokens && (threadIdx.x & ((1u << m.lg) - 1u)) == 0) dweights[t * per + k0 + j] = s;
         }
     }
 }
@@ -567,6 +598,7 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
 // an order that the offsets fix.
 constexpr int kSumLevels = 3;
 constexpr int kSumLg = 4;  // 16 positions to a block, 16 blocks to a block of the next level
+constexpr int kSumRows = 1 << kSumLg;
 
 struct BlockSums {
     float *level[kSumLevels];  // [n / 16^(l + 1)][width]
@@ -583,61 +615,76 @@ __device__ __forceinline__ bool one_id(const I *ids, const int32_t *order, int64
     return a == b && a >= 0 && a < vocab;
 }
 
-template <class T, bool VEC, class I>
+template <class T, bool VEC, bool WAVE, class I>
 __global__ __launch_bounds__(kRowBlock) void grad_blocks_kernel(
     const T *__restrict__ dout, const I *__restrict__ ids, const int32_t *__restrict__ order,
     const int32_t *__restrict__ offsets, uint32_t n, int64_t vocab, int level, BlockSums sums, RowMap m) {
     using C = Chunk<T, VEC>;
+    constexpr int N = C::kN;
     const int lg = kSumLg * (level + 1);
-    const int64_t block = row_of(m);
+    const int64_t block = row_of<WAVE>(m);
     const int64_t lo = block << lg, hi = lo + (int64_t{1} << lg) - 1;
     const int64_t kept = offsets[vocab] < static_cast<int64_t>(n) ? offsets[vocab] : n;
     if (hi >= kept || !one_id(ids, order, lo, hi, n, vocab)) return;
     float *dst = sums.level[level] + block * m.width;
     for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-        const int at = chunk_start<C::kN>(c, m.width);
-        float acc[C::kN];
+        const int at = chunk_start<N>(c, m);
+        float acc[N];
 #pragma unroll
-        for (int e = 0; e < C::kN; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < (1 << kSumLg); ++j) {
-            if (level == 0) {
+        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        if (level == 0) {
+            typename C::Raw r[kSumRows];
+            bool ok[kSumRows];
+#pragma unroll
+            for (int j = 0; j < kSumRows; ++j) {
                 const uint32_t i = static_cast<uint32_t>(order[lo + j]);
-                if (i >= n) continue;
-                C v;
-                v.load(dout + static_cast<int64_t>(i) * m.width + at);
+                ok[j] = i < n;
+                r[j] = C::load_stream(dout + static_cast<int64_t>(ok[j] ? i : 0) * m.width + at);
+            }
 #pragma unroll
-                for (int e = 0; e < C::kN; ++e) acc[e] += v.f[e];
-            } else {
-                float p[C::kN];
-                load_values<float, C::kN>(sums.level[level - 1] + ((block << kSumLg) + j) * m.width + at, p);
+            for (int j = 0; j < kSumRows; ++j) {
+                float v[N];
+                C::unpack(r[j], v);
 #pragma unroll
-                for (int e = 0; e < C::kN; ++e) acc[e] += p[e];
+                for (int e = 0; e < N; ++e) acc[e] += ok[j] ? v[e] : 0.0f;
+            }
+        } else {
+            const float *p = sums.level[level - 1] + (block << kSumLg) * m.width + at;
+#pragma unroll 4
+            for (int j = 0; j < kSumRows; ++j) {
+                float v[N];
+                load_values<float, N>(p + static_cast<int64_t>(j) * m.width, v);
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[e] += v[e];
             }
         }
-        store_values<float, C::kN>(dst + at, acc);
+        store_values<float, N>(dst + at, acc);
     }
 }
 
-template <class T, bool VEC, class G>
+template <class T, bool VEC, bool WAVE, int CH, class G>
 __global__ __launch_bounds__(kRowBlock) void embed_grad_kernel(
     const T *__restrict__ dout, const int32_t *__restrict__ order, const int32_t *__restrict__ offsets,
     uint32_t n, int64_t vocab, float scale, int accumulate, BlockSums sums, G *__restrict__ grad, RowMap m) {
     using C = Chunk<T, VEC>;
     constexpr int N = C::kN;
-    const int64_t v = row_of(m);
+    const int64_t v = row_of<WAVE>(m);
     if (v >= vocab) return;
     const uint32_t a = static_cast<uint32_t>(offsets[v]);
     uint32_t b = static_cast<uint32_t>(offsets[v + 1]);
     if (b > n) b = n;
     if (accumulate && a >= b) return;
     G *dst = grad + v * m.width;
-    for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
-        const int at = chunk_start<N>(c, m.width);
-        const int skip = c * N - at;
-        float acc[N];
+    const int step = col_step(m);
+    for (int c0 = col_of(m); c0 < m.chunks; c0 += CH * step) {
+        int at[CH];
+        float acc[CH][N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        for (int q = 0; q < CH; ++q) {
+            at[q] = chunk_start<N>(c0 + q * step, m);
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[q][e] = 0.0f;
+        }
         for (uint32_t s = a; s < b;) {
             // the largest block that starts here and ends inside, and the
             // run of its level up to the next larger block
@@ -648,46 +695,61 @@ __global__ __launch_bounds__(kRowBlock) void embed_grad_kernel(
             const int lg = kSumLg * l;
             uint32_t count = (b - s) >> lg;
             if (l < sums.levels) {
-                const uint32_t left = (1u << kSumLg) - ((s >> lg) & ((1u << kSumLg) - 1u));
+                const uint32_t left = kSumRows - ((s >> lg) & (kSumRows - 1u));
                 count = count < left ? count : left;
             }
             if (l == 0) {
-#pragma unroll 4
+#pragma unroll 2
                 for (uint32_t j = 0; j < count; ++j) {
                     const uint32_t i = static_cast<uint32_t>(order[s + j]);
                     if (i >= n) continue;
-                    C x;
-                    x.load(dout + static_cast<int64_t>(i) * m.width + at);
+                    const T *src = dout + static_cast<int64_t>(i) * m.width;
+                    typename C::Raw r[CH];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] += x.f[e];
+                    for (int q = 0; q < CH; ++q) r[q] = C::load_stream(src + at[q]);
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) {
+                        float x[N];
+                        C::unpack(r[q], x);
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[q][e] += x[e];
+                    }
                 }
             } else {
-                const float *p = sums.level[l - 1] + static_cast<int64_t>(s >> lg) * m.width + at;
-#pragma unroll 4
-                for (uint32_t j = 0; j < count; ++j) {
-                    float x[N];
-                    load_values<float, N>(p + static_cast<int64_t>(j) * m.width, x);
+                const float *p = sums.level[l - 1] + static_cast<int64_t>(s >> lg) * m.width;
+                for (uint32_t j = 0; j < count; ++j, p += m.width) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] += x[e];
+                    for (int q = 0; q < CH; ++q) {
+                        float x[N];
+                        load_values<float, N>(p + at[q], x);
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[q][e] += x[e];
+                    }
                 }
             }
             s += count << lg;
         }
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] *= scale;
-        if (skip == 0) {
-            if (accumulate) {
+        for (int q = 0; q < CH; ++q) {
+            const int c = c0 + q * step;
+            if (c >= m.chunks) continue;
+            const int skip = c * N - at[q];
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[q][e] *= scale;
+            if (!accumulate) {
+                store_values<G, N>(dst + at[q], acc[q]);
+            } else if (skip == 0) {
                 float old[N];
-                load_values<G, N>(dst + at, old);
+                load_values<G, N>(dst + at[q], old);
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] += old[e];
-            }
-            store_values<G, N>(dst + at, acc);
-        } else {  // elements that another lane owns are not added to twice
+                for (int e = 0; e < N; ++e) acc[q][e] += old[e];
+                store_values<G, N>(dst + at[q], acc[q]);
+            } else {  // elements that another lane owns are not added to twice
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (e < skip) continue;
-                dst[at + e] = static_cast<G>(accumulate ? static_cast<float>(dst[at + e]) + acc[e] : acc[e]);
+                for (int e = 0; e < N; ++e) {
+                    G *p = dst + at[q] + e;
+                    if (e >= skip) *p = static_cast<G>(static_cast<float>(*p) + acc[q][e]);
+                }
             }
         }
     }
@@ -707,8 +769,12 @@ GroupPlan group_plan(int64_t n, int64_t groups) {
     const int all = bits_of(static_cast<uint64_t>(groups));  // values 0 .. groups
     p.passes = (all + kDigitBits - 1) / kDigitBits;
     p.bits = (all + p.passes - 1) / p.passes;
-    if (n <= kGroupSmall) return p;
-    int64_t tiles = (n + kGroupStep - 1) / kGroupStep;
+    if (p.bits < 2) p.bits = 2;  // the table is read four digits at a time
+    if (n <= kGroupSmall) {
+        p.bytes = p.passes > 1 ? static_cast<size_t>(n) * 4 : 0;  // the sorted keys
+        return p;
+    }
+    int64_t tiles = (n + kGroupBlock - 1) / kGroupBlock;
     if (tiles > kGroupTiles) tiles = kGroupTiles;
     int64_t span = (n + tiles - 1) / tiles;
     span = (span + kGroupBlock - 1) / kGroupBlock * kGroupBlock;
@@ -725,20 +791,25 @@ bool group_sizes_ok(int64_t n, int64_t groups) {
     return n >= 0 && n <= INT32_MAX && groups >= 1 && groups <= INT32_MAX - 1;
 }
 
+int launch_offsets(const uint32_t *sorted, uint32_t n, uint32_t groups, int32_t *offsets, hipStream_t s) {
+    hipLaunchKernelGGL(group_offsets_kernel, dim3(groups / kGroupBlock + 1), dim3(kGroupBlock), 0, s, sorted, n,
+                       groups, offsets);
+    return launched();
+}
+
 template <class K>
 int launch_small(const K *keys, uint32_t n, uint32_t groups, const GroupPlan &p, int32_t *order, int32_t *ranks,
-                 int32_t *offsets, hipStream_t s) {
-    const dim3 one(1), block(kGroupBlock);
+                 int32_t *offsets, uint32_t *sorted, hipStream_t s) {
+    const auto launch = [&](auto items) {
+        hipLaunchKernelGGL((group_small_kernel<K, decltype(items)::value>), dim3(1), dim3(kGroupBlock), 0, s, keys, n,
+                           groups, p.passes, p.bits, order, ranks, offsets, sorted);
+        return launched();
+    };
     if (n <= kGroupBlock)
-        hipLaunchKernelGGL((group_small_kernel<K, 1>), one, block, 0, s, keys, n, groups, p.passes, p.bits, order,
-                           ranks, offsets);
-    else if (n <= 4 * kGroupBlock)
-        hipLaunchKernelGGL((group_small_kernel<K, 4>), one, block, 0, s, keys, n, groups, p.passes, p.bits, order,
-                           ranks, offsets);
+        SSC_TRY(launch(std::integral_constant<int, 1>{}));
     else
-        hipLaunchKernelGGL((group_small_kernel<K, 16>), one, block, 0, s, keys, n, groups, p.passes, p.bits, order,
-                           ranks, offsets);
-    return launched();
+        SSC_TRY(launch(std::integral_constant<int, 4>{}));
+    return p.passes > 1 ? launch_offsets(sorted, n, groups, offsets, s) : SSC_OK;
 }
 
 template <class K>
@@ -752,7 +823,7 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
         return SSC_ERR_ARG;
     const GroupPlan p = group_plan(n, groups);
     const size_t bytes = static_cast<size_t>(n) * 4;
-    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 8) || scratch_bytes < p.bytes))
+    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < p.bytes))
         return SSC_ERR_SCRATCH;
     const Span arrays[] = {{keys, static_cast<size_t>(n) * sizeof(K)},
                            {order, bytes},
@@ -769,7 +840,7 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
         return launched();
     }
     const uint32_t un = static_cast<uint32_t>(n), ug = static_cast<uint32_t>(groups);
-    if (n <= kGroupSmall) return launch_small(keys, un, ug, p, order, ranks, offsets, s);
+    if (n <= kGroupSmall) return launch_small(keys, un, ug, p, order, ranks, offsets, static_cast<uint32_t *>(scratch), s);
     uint32_t *table = static_cast<uint32_t *>(scratch);
     uint32_t *buf[2][2];  // keys and positions of the two sides
     uint32_t *at = table + p.table_bytes / 4;
@@ -782,19 +853,19 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
         hipLaunchKernelGGL((group_count_kernel<K>), grid, block, 0, s, keys, sorted, un, p.span, ug, q * p.bits,
                            p.bits, table);
         SSC_TRY(launched());
-        hipLaunchKernelGGL((group_scatter_kernel<K>), grid, block, 0, s, keys, sorted, positions, un, p.span, ug,
-                           q * p.bits, p.bits, static_cast<const uint32_t *>(table),
-                           p.passes == 1 ? nullptr : buf[q & 1][0], last ? nullptr : buf[q & 1][1],
-                           last ? order : nullptr, last ? ranks : nullptr, p.passes == 1 ? offsets : nullptr);
-        SSC_TRY(launched());
+        const auto scatter = [&](auto items) {
+            hipLaunchKernelGGL((group_scatter_kernel<K, decltype(items)::value>), grid, block, 0, s, keys, sorted,
+                               positions, un, p.span, ug, q * p.bits, p.bits, static_cast<const uint32_t *>(table),
+                               p.passes == 1 ? nullptr : buf[q & 1][0], last ? nullptr : buf[q & 1][1],
+                               last ? order : nullptr, last ? ranks : nullptr, p.passes == 1 ? offsets : nullptr);
+            return launched();
+        };
+        SSC_TRY(p.span >= 4 * kGroupBlock ? scatter(std::integral_constant<int, 4>{})
+                                          : scatter(std::integral_constant<int, 1>{}));
         sorted = buf[q & 1][0];
         positions = buf[q & 1][1];
     }
-    if (p.passes > 1) {
-        hipLaunchKernelGGL(group_offsets_kernel, dim3(un / kGroupBlock + 1), block, 0, s, sorted, un, ug, offsets);
-        return launched();
-    }
-    return SSC_OK;
+    return p.passes > 1 ? launch_offsets(sorted, un, ug, offsets, s) : SSC_OK;
 }
 
 size_t elem_bytes(int dtype) { return dtype == SSC_F32 ? 4 : 2; }
@@ -811,12 +882,14 @@ int with_type(int dtype, int64_t width, F f) {
     }
 }
 
-// A wavefront to a row, or the few threads that a short row needs; where the
-// rows are too few to fill the chip (fewer than two workgroups a compute
-// unit), more threads to a row, and columns over several workgroups (split).
+// One chunk to a thread, up to a workgroup to a row; where the rows are too few
+// to fill the chip (fewer than two workgroups a compute unit), columns over
+// several workgroups (split).
 struct RowLaunch {
     RowMap map;
     dim3 grid;
+    bool wave;   // whole wavefronts to a row
+    int deep;    // chunks to a thread, as 1, 2 or 4
 };
 
 RowLaunch row_launch(int64_t rows, int64_t width, int per_chunk, bool split) {
@@ -825,15 +898,26 @@ RowLaunch row_launch(int64_t rows, int64_t width, int per_chunk, bool split) {
     r.map.chunks = static_cast<int>((width + per_chunk - 1) / per_chunk);
     const int64_t enough = 512;
     int lg = 0;
-    while (lg < 6 && (1 << lg) < r.map.chunks) ++lg;
-    while (lg < 8 && (1 << lg) < r.map.chunks && (rows >> (8 - lg)) < enough) ++lg;
+    while (lg < 8 && (1 << lg) < r.map.chunks) ++lg;
     r.map.lg = lg;
     const int64_t blocks = (rows + (256 >> lg) - 1) >> (8 - lg);
     int64_t cols = 1;
-    const int64_t most = (r.map.chunks + (1 << lg) - 1) >> lg;
-    while (split && cols < most && cols < 64 && blocks * cols < enough) ++cols;
+    const int64_t parts = (r.map.chunks + (1 << lg) - 1) >> lg;
+    while (split && cols < parts && cols < 64 && blocks * cols < enough) ++cols;
     r.grid = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cols));
+    r.wave = lg >= 6;
+    const int64_t each = (parts + cols - 1) / cols;
+    r.deep = !r.wave || each == 1 ? 1 : (each == 2 ? 2 : 4);
     return r;
+}
+
+// Calls f with the launch's WAVE and its chunks in flight.
+template <class F>
+int with_shape(const RowLaunch &r, F f) {
+    if (r.deep == 4) return f(std::true_type{}, std::integral_constant<int, 4>{});
+    if (r.deep == 2) return f(std::true_type{}, std::integral_constant<int, 2>{});
+    if (r.wave) return f(std::true_type{}, std::integral_constant<int, 1>{});
+    return f(std::false_type{}, std::integral_constant<int, 1>{});
 }
 
 // Element type and width of a row; byte extents of INT32_MAX rows then fit
@@ -863,9 +947,12 @@ int embed_impl(const void *table, int dtype, int64_t vocab, int64_t width, const
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
         const RowLaunch r = row_launch(n, width, Chunk<T, V>::kN, true);
-        hipLaunchKernelGGL((embed_kernel<T, V, I>), r.grid, dim3(kRowBlock), 0, static_cast<hipStream_t>(stream),
-                           static_cast<const T *>(table), vocab, ids, n, scale, static_cast<T *>(out), r.map);
-        return launched();
+        return with_shape(r, [&](auto wave, auto ch) {
+            hipLaunchKernelGGL((embed_kernel<T, V, decltype(wave)::value, decltype(ch)::value, I>), r.grid,
+                               dim3(kRowBlock), 0, static_cast<hipStream_t>(stream), static_cast<const T *>(table),
+                               vocab, ids, n, scale, static_cast<T *>(out), r.map);
+            return launched();
+        });
     });
 }
 
@@ -897,7 +984,7 @@ int embed_grad_impl(const void *dout, int dtype, int64_t n, int64_t width, const
         !aligned(offsets, 4))
         return SSC_ERR_ARG;
     const size_t need = grad_scratch(n, width);
-    if (need > 0 && (scratch == nullptr || !aligned(scratch, 8) || scratch_bytes < need)) return SSC_ERR_SCRATCH;
+    if (need > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < need)) return SSC_ERR_SCRATCH;
     const Span written[] = {{grad, static_cast<size_t>(vocab) * width * gs}, {scratch, need}};
     const Span read[] = {{dout, static_cast<size_t>(n) * width * es},
                          {ids, static_cast<size_t>(n) * sizeof(I)},
@@ -923,20 +1010,25 @@ int embed_grad_impl(const void *dout, int dtype, int64_t n, int64_t width, const
         }
         for (int l = 0; l < sums.levels; ++l) {
             const RowLaunch r = row_launch(n >> (kSumLg * (l + 1)), width, Chunk<T, V>::kN, true);
-            hipLaunchKernelGGL((grad_blocks_kernel<T, V, I>), r.grid, dim3(kRowBlock), 0, s,
-                               static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
+            if (r.wave)
+                hipLaunchKernelGGL((grad_blocks_kernel<T, V, true, I>), r.grid, dim3(kRowBlock), 0, s,
+                                   static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
+            else
+                hipLaunchKernelGGL((grad_blocks_kernel<T, V, false, I>), r.grid, dim3(kRowBlock), 0, s,
+                                   static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
             SSC_TRY(launched());
         }
         const RowLaunch r = row_launch(vocab, width, Chunk<T, V>::kN, true);
-        if (grad_dtype == dtype)
-            hipLaunchKernelGGL((embed_grad_kernel<T, V, T>), r.grid, dim3(kRowBlock), 0, s,
-                               static_cast<const T *>(dout), order, offsets, un, vocab, scale, accumulate, sums,
-                               static_cast<T *>(grad), r.map);
-        else
-            hipLaunchKernelGGL((embed_grad_kernel<T, V, float>), r.grid, dim3(kRowBlock), 0, s,
-                               static_cast<const T *>(dout), order, offsets, un, vocab, scale, accumulate, sums,
-                               static_cast<float *>(grad), r.map);
-        return launched();
+        const auto launch = [&](auto *g) {
+            using G = std::remove_pointer_t<decltype(g)>;
+            return with_shape(r, [&](auto wave, auto ch) {
+                hipLaunchKernelGGL((embed_grad_kernel<T, V, decltype(wave)::value, decltype(ch)::value, G>), r.grid,
+                                   dim3(kRowBlock), 0, s, static_cast<const T *>(dout), order, offsets, un, vocab,
+                                   scale, accumulate, sums, g, r.map);
+                return launched();
+            });
+        };
+        return grad_dtype == dtype ? launch(static_cast<T *>(grad)) : launch(static_cast<float *>(grad));
     });
 }
 
@@ -1013,10 +1105,12 @@ int ssc_dispatch_rows(const void *x, int dtype, int64_t tokens, int64_t per, int
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
         const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true);
-        hipLaunchKernelGGL((dispatch_kernel<T, V>), r.grid, dim3(kRowBlock), 0, static_cast<hipStream_t>(stream),
-                           static_cast<const T *>(x), tokens, static_cast<int>(per), ranks, rows,
-                           static_cast<T *>(out), r.map);
-        return launched();
+        return with_shape(r, [&](auto wave, auto ch) {
+            hipLaunchKernelGGL((dispatch_kernel<T, V, decltype(wave)::value, decltype(ch)::value>), r.grid,
+                               dim3(kRowBlock), 0, static_cast<hipStream_t>(stream), static_cast<const T *>(x),
+                               tokens, static_cast<int>(per), ranks, rows, static_cast<T *>(out), r.map);
+            return launched();
+        });
     });
 }
 
@@ -1036,15 +1130,15 @@ int ssc_combine_rows(const void *y, int dtype, int64_t rows, int64_t width, cons
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
         const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true);
+        const auto launch = [&](auto wave, auto weighted) {
+            hipLaunchKernelGGL((combine_kernel<T, V, decltype(wave)::value, decltype(weighted)::value>), r.grid,
+                               dim3(kRowBlock), 0, static_cast<hipStream_t>(stream), static_cast<const T *>(y), rows,
+                               ranks, weights, tokens, static_cast<int>(per), static_cast<T *>(out), r.map);
+            return launched();
+        };
         if (weights != nullptr)
-            hipLaunchKernelGGL((combine_kernel<T, V, true>), r.grid, dim3(kRowBlock), 0,
-                               static_cast<hipStream_t>(stream), static_cast<const T *>(y), rows, ranks, weights,
-                               tokens, static_cast<int>(per), static_cast<T *>(out), r.map);
-        else
-            hipLaunchKernelGGL((combine_kernel<T, V, false>), r.grid, dim3(kRowBlock), 0,
-                               static_cast<hipStream_t>(stream), static_cast<const T *>(y), rows, ranks, weights,
-                               tokens, static_cast<int>(per), static_cast<T *>(out), r.map);
-        return launched();
+            return r.wave ? launch(std::true_type{}, std::true_type{}) : launch(std::false_type{}, std::true_type{});
+        return r.wave ? launch(std::true_type{}, std::false_type{}) : launch(std::false_type{}, std::false_type{});
     });
 }
 
@@ -1075,10 +1169,14 @@ int ssc_combine_rows_grad(const void *dout, const void *y, int dtype, int64_t ro
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
         const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, false);
-        hipLaunchKernelGGL((combine_grad_kernel<T, V>), r.grid, dim3(kRowBlock), 0, static_cast<hipStream_t>(stream),
-                           static_cast<const T *>(dout), static_cast<const T *>(y), rows, ranks, weights, tokens,
-                           static_cast<int>(per), static_cast<T *>(dy), dweights, r.map);
-        return launched();
+        const auto launch = [&](auto wave) {
+            hipLaunchKernelGGL((combine_grad_kernel<T, V, decltype(wave)::value>), r.grid, dim3(kRowBlock), 0,
+                               static_cast<hipStream_t>(stream), static_cast<const T *>(dout),
+                               static_cast<const T *>(y), rows, ranks, weights, tokens, static_cast<int>(per),
+                               static_cast<T *>(dy), dweights, r.map);
+            return launched();
+        };
+        return r.wave ? launch(std::true_type{}) : launch(std::false_type{});
     });
 }
 

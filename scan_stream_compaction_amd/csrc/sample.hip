@@ -717,7 +717,7 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
         !aligned(logprobs, 4))
         return SSC_ERR_ARG;
     const SamplePlan p = sample_plan(rows, vocab);
-    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 8) || scratch_bytes < p.bytes))
+    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < p.bytes))
         return SSC_ERR_SCRATCH;
     const size_t each = static_cast<size_t>(rows) * 4;
     const Span written[] = {{tokens, each}, {kept, each}, {logprobs, each}, {scratch, p.bytes}};

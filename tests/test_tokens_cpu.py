@@ -35,17 +35,20 @@ def test_group_refusals(name):
     assert _call(name, d, ranks=B + 3996) == ALIAS
     assert _call(name, d, offsets=C) == ALIAS
     assert _call(name, d, n=20_000, scratch=None) == SCRATCH
-    assert _call(name, d, n=20_000, scratch=S + 4) == SCRATCH
+    assert _call(name, d, n=20_000, scratch=S + 8) == SCRATCH
     assert _call(name, d, n=20_000, sbytes=ssc.group_scratch_bytes(20_000, 10) - 1) == SCRATCH
     assert _call(name, d, n=20_000, scratch=A) == ALIAS
 
 
 def test_scratch_sizes():
-    assert ssc.group_scratch_bytes(16_384, 100) == 0
-    # 3 spans of up to 8192 keys x 128 digits of 7 bits (100 groups and one more)
-    assert ssc.group_scratch_bytes(16_385, 100) == 3 * 128 * 4
+    assert ssc.group_scratch_bytes(4096, 511) == 0
+    assert ssc.group_scratch_bytes(1000, 512) == 4000  # two passes leave their sorted keys
+    # 17 spans of 1024 keys x 128 digits of 7 bits (100 groups and one more)
+    assert ssc.group_scratch_bytes(16_385, 100) == 17 * 128 * 4
     # two passes of 9 bits: the table, (key, position) once, sorted keys
-    assert ssc.group_scratch_bytes(65_536, 131_072) == 8 * 512 * 4 + 3 * 4 * 65_536
+    assert ssc.group_scratch_bytes(65_536, 131_072) == 64 * 512 * 4 + 3 * 4 * 65_536
+    # at most 256 spans
+    assert ssc.group_scratch_bytes(2 ** 20 + 1, 100) == 205 * 128 * 4
     assert ssc.group_scratch_bytes(-1, 5) == 0 and ssc.group_scratch_bytes(5, 0) == 0
     L = ssc.lib()
     assert L.ssc_embed_grad_scratch_bytes(255, 64) == 0
