@@ -143,6 +143,7 @@ def _check(call: str, rc: int) -> None:
         raise SSCError(call, rc, detail)
 
 
+_Tensor = torch.Tensor
 _recording = None  # list of library calls being recorded by prepared(), or None
 
 
@@ -151,10 +152,12 @@ def _call(name: str, fn, *args) -> None:
     Tensor arguments are passed as their device pointers; a recording keeps
     the tensors themselves, so every buffer a recorded call touches (scratch
     an op allocated for itself included) lives as long as the recording."""
-    raw = tuple(a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args)
+    raw = [a.data_ptr() if isinstance(a, _Tensor) else a for a in args]
     if _recording is not None:
         _recording.append((name, fn, raw, args))
-    _check(name, fn(*raw))
+    rc = fn(*raw)
+    if rc != 0:
+        _check(name, rc)
 
 
 def prepared(op, *args, **kwargs):
@@ -210,7 +213,7 @@ def _need(t, name: str, like: torch.Tensor, dtypes, numel: int) -> torch.Tensor:
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU (no CPU path)")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, the input on {like.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -231,7 +234,14 @@ def _count(count, like: torch.Tensor) -> torch.Tensor:
     return _need(count, "count", like, (torch.int32,), 1)
 
 
+# The current stream's handle without a Stream object around it: 0.1 us of
+# host time a call against 2.0.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -656,10 +666,10 @@ def _ids(x: torch.Tensor, name: str) -> str:
 def _row_call(name: str, like: torch.Tensor, *args) -> None:
     """_call on like's stream, with its device current."""
     if like.get_device() == torch.cuda.current_device():
-        _call(name, getattr(lib(), name), *args, _stream(like))
+        _call(name, getattr(_lib or lib(), name), *args, _stream(like))
     else:
         with torch.cuda.device(like.device):
-            _call(name, getattr(lib(), name), *args, _stream(like))
+            _call(name, getattr(_lib or lib(), name), *args, _stream(like))
 
 
 def _work_bytes(scratch, like: torch.Tensor, nbytes: int) -> torch.Tensor | None:
@@ -721,7 +731,7 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
     vocab, width = _rows(table, "table")
     name = "ssc_embed_rows_" + _ids(ids, "ids") if isinstance(ids, torch.Tensor) else ""
     n = _need(ids, "ids", table, None, 0).numel()
-    out = (torch.empty(*ids.shape, width, dtype=table.dtype, device=table.device) if out is None
+    out = (table.new_empty((*ids.shape, width)) if out is None
            else _need(out, "out", table, (table.dtype,), n * width))
     _row_call(name, table, table, DTYPE[table.dtype], vocab, width, ids, n, scale, out)
     return out
@@ -784,7 +794,7 @@ def dispatch_rows(x: torch.Tensor, ranks: torch.Tensor, *, out: torch.Tensor | N
     tokens, width = _rows(x, "x")
     tokens, per = _routed(ranks, x, tokens)
     if out is None:
-        out = torch.empty(tokens * per, width, dtype=x.dtype, device=x.device)
+        out = x.new_empty((tokens * per, width))
     else:
         _need(out, "out", x, (x.dtype,), 0)
         if out.dim() != 2 or out.shape[1] != width:
@@ -810,7 +820,7 @@ def combine_rows(y: torch.Tensor, ranks: torch.Tensor, weights: torch.Tensor | N
     tokens, per = _routed(ranks, y, None)
     if weights is not None:
         _weights(weights, y, ranks)
-    out = (torch.empty(tokens, width, dtype=y.dtype, device=y.device) if out is None
+    out = (y.new_empty((tokens, width)) if out is None
            else _need(out, "out", y, (y.dtype,), tokens * width))
     _row_call("ssc_combine_rows", y, y, DTYPE[y.dtype], rows, width, ranks, weights, tokens, per, out)
     return out

@@ -3,21 +3,22 @@
 // their part of the C ABI in include/ssc.h.
 //
 // Every filter keeps a prefix of the row in the order (logit descending,
-// index ascending), so the kept set is {key > t} and the ties {key = t} up to
-// an index, with `key` the logit's bits as an ordered integer. No row is
-// sorted: the border t is found digit by digit in histograms of the keys
-// (11 bits each: two steps for 16-bit logits, three for fp32) that hold each
-// bin's count and weight, which is also what makes it exact. The token is then
+// index ascending). No row is sorted: a histogram over 2048 bins of distance
+// from the row's maximum shows which bin a filter's border falls into, the few
+// logits of that bin are collected (a compaction) and sorted alone, and
+// everything in better bins is kept without a look at its order. The token is
 // the first index at which the running kept weight exceeds u times its sum:
-// a selection by a scan, over the sums of parts of the row and then inside
-// one part.
+// a selection by a scan, over the sums of parts of the row, then inside one
+// part.
 //
 // Weights exp((x - max) / T) are computed in fp64 and held as integers with
 // 62 - bits(vocab) fractional bits (at most 50): integer sums do not depend
 // on their order, so rows may be split and added with atomics, and a call
 // repeats bit for bit.
 //
-// Launches: row maxima; histograms; borders; kept weight of each part; token.
+// Launches, each over parts of rows except the last: maxima; histograms (only
+// where a filter is given; a row's last workgroup finds the border bins); sums
+// of the better bins with the border bins' logits collected; border and token.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,19 +29,30 @@
 namespace ssc {
 namespace {
 
-constexpr int kPart = 4096;           // logits of a part
+constexpr int kPartLg = 12;
+constexpr int kPart = 1 << kPartLg;   // logits of a part
 constexpr int kPartBlock = 256;
 constexpr int kPartItems = kPart / kPartBlock;
-constexpr int kHistPart = 16384;      // logits a workgroup adds to its row's histogram
+constexpr int kHistPart = 8192;       // logits a workgroup adds to its row's histogram
 constexpr int kHistBlock = 512;
 constexpr int kBins = 2048;
-constexpr int kBorderBlock = 1024;
+constexpr int kTokenBlock = 1024;
+constexpr int kList = 4096;           // collected logits a row has room for
+constexpr int kListTopK = kList / 2;  // up to this top_k, all its logits are collected
+constexpr int64_t kVocabMax = int64_t{1} << 22;
+constexpr int kPartsMax = static_cast<int>(kVocabMax / kPart);
 constexpr uint32_t kNoCut = 0xffffffffu;
 
-// What the border search of a row leaves for the later launches.
+// What is known of a row's border. Bins are numbered from the maximum down:
+// those below `lo` are kept, those in [lo, hi] and `extra` are collected.
 struct RowState {
-    uint32_t border;  // smallest kept key
-    uint32_t cut;     // last index at which that key is kept
+    uint64_t mass;        // weight of the bins below lo ...
+    uint64_t extra_mass;  // ... and below extra
+    uint64_t total;       // of the row, where top_p alone cuts it; else 0
+    uint32_t count, extra_count;  // their logits
+    int32_t lo, hi, extra;        // extra: top_k's border bin, where top_p's lies before it (-1: none)
+    uint32_t listed;      // logits collected so far (may pass kList: the list is then not used)
+    uint32_t done;        // workgroups of the row that have added their histogram
 };
 
 struct SampleArgs {
@@ -51,13 +63,14 @@ struct SampleArgs {
     const int32_t *top_k;
     int32_t *tokens, *kept;
     float *logprobs;
-    // scratch, per row: part maxima (keys), part sums, histogram, state
-    uint32_t *part_max;      // [rows][parts]
+    // scratch
+    float2 *part_range;      // [rows][parts] largest and smallest token logit
     uint64_t *part_mass;     // [rows][parts]
     uint32_t *part_count;    // [rows][parts]
-    uint64_t *hist_mass;     // [rows][kBins]
-    uint32_t *hist_count;    // [rows][kBins]
     RowState *state;         // [rows]
+    uint64_t *hist_mass;     // [rows][kBins], where a filter is given
+    uint32_t *hist_count;    // [rows][kBins]
+    uint64_t *list;          // [rows][kList]
 };
 
 // The logit as an integer of the same order; 0 for NaN and -infinity, which
@@ -71,41 +84,89 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
-// A row's settings, with what is out of range put in its place.
-struct Settings {
-    double inv_t, max, scale, min_w;
-    float top_p;   // 2: off
+// A row's filters, with what is out of range put in its place.
+struct Filters {
+    float t;        // temperature; 0: the first of the order alone
+    float top_p;    // 2: off
     int32_t top_k;  // 0: off
-    bool max_inf;
 
-    __device__ __forceinline__ Settings(const SampleArgs &a, int row, uint32_t max_key) {
-        const float t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
+    __device__ __forceinline__ Filters(const SampleArgs &a, int row) {
+        t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
         const bool greedy = !(t > 0.0f);
-        inv_t = greedy ? 1.0 : 1.0 / static_cast<double>(t);
-        const float m = value_of(max_key);
-        max_inf = m == __builtin_inff();
-        max = max_inf ? 0.0 : static_cast<double>(m);
-        scale = static_cast<double>(uint64_t{1} << a.bits);
-        const float mp = a.min_p != nullptr ? a.min_p[row] : 0.0f;
-        min_w = mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0);
+        if (greedy) t = 0.0f;
         const int32_t k = a.top_k != nullptr ? a.top_k[row] : 0;
         top_k = greedy ? 1 : (k < 1 || k >= a.vocab ? 0 : k);
         const float p = a.top_p != nullptr ? a.top_p[row] : 2.0f;
         top_p = greedy || !(p < 1.0f) ? 2.0f : p;
-        if (top_p <= 0.0f) {
-            top_p = 2.0f;
-            top_k = 1;
-        }
+        if (top_p <= 0.0f) top_k = 1;
+        if (top_k == 1) top_p = 2.0f;
     }
-    // exp((x - max) / T) of a logit that is a token
-    __device__ __forceinline__ double weight(float x) const {
-        if (max_inf) return x == __builtin_inff() ? 1.0 : 0.0;
-        return exp((static_cast<double>(x) - max) * inv_t);
+    __device__ __forceinline__ bool nucleus() const { return top_p < 1.0f; }
+    // one logit needs no histogram, all of them neither
+    __device__ __forceinline__ bool searched() const { return top_k > 1 || nucleus(); }
+    // a small top_k is resolved among its collected logits alone
+    __device__ __forceinline__ bool small_k() const { return top_k > 1 && top_k <= kListTopK; }
+};
+
+// Weights and bins of a row.
+struct Scale {
+    double max, rate, min_w;  // rate: log2(e) / T; min_w at the weights' scale
+    float top, width;         // the maximum; bins per unit of distance from it
+    int bits;
+    bool top_inf;
+
+    __device__ __forceinline__ Scale(const SampleArgs &a, int row, const Filters &f, float2 range) {
+        top = range.x;
+        top_inf = top == __builtin_inff();
+        max = top_inf ? 0.0 : static_cast<double>(top);
+        const double t = f.t > 0.0f ? static_cast<double>(f.t) : 1.0;
+        rate = 1.4426950408889634 / t;
+        bits = a.bits;
+        const float mp = a.min_p != nullptr ? a.min_p[row] : 0.0f;
+        min_w = ldexp(mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0), bits);
+        // the bins span the row, or as far down as weights matter (a NaN from
+        // infinities gives way)
+        const float span = fminf(fminf(top - range.y, 64.0f * static_cast<float>(t)), 0x1.fffffep127f);
+        width = span > 0.0f ? fminf((kBins - 1) / span, 0x1p100f) : 0.0f;
     }
-    // ... as an integer: adding 2^52 leaves the rounded value in the low bits
-    __device__ __forceinline__ uint64_t fixed(double w) const {
-        return static_cast<uint64_t>(__double_as_longlong(__builtin_fma(w, scale, 0x1p52))) & ((uint64_t{1} << 52) - 1);
+    // A token's logit on the axis of the bins: bin b is [b, b + 1), the last
+    // without an end; a larger logit never lies further.
+    __device__ __forceinline__ float place(float x) const {
+        if (top_inf) return x == top ? 0.0f : __builtin_inff();
+        return (top - x) * width;
     }
+    __device__ __forceinline__ int bin(float x) const {
+        return static_cast<int>(fminf(place(x), static_cast<float>(kBins - 1)));
+    }
+    // exp((x - max) / T) * 2^bits, by 2^y = 2^round(y) * 2^(y - round(y)), the
+    // second factor by its Taylor series in fp64: terms up to the 11th leave
+    // 7e-15 of it at most, below the integers' own step for weights of
+    // 2^-3 and less of the largest.
+    __device__ __forceinline__ double scaled(float x) const {
+        if (top_inf) return x == top ? ldexp(1.0, bits) : 0.0;
+        constexpr double kLn2 = 0.69314718055994530942;
+        const double y = fmax((static_cast<double>(x) - max) * rate, -1000.0);
+        const double n = __builtin_rint(y);
+        const double g = (y - n) * kLn2;
+        double s = 1.0 / 39916800;
+        s = __builtin_fma(s, g, 1.0 / 3628800);
+        s = __builtin_fma(s, g, 1.0 / 362880);
+        s = __builtin_fma(s, g, 1.0 / 40320);
+        s = __builtin_fma(s, g, 1.0 / 5040);
+        s = __builtin_fma(s, g, 1.0 / 720);
+        s = __builtin_fma(s, g, 1.0 / 120);
+        s = __builtin_fma(s, g, 1.0 / 24);
+        s = __builtin_fma(s, g, 1.0 / 6);
+        s = __builtin_fma(s, g, 0.5);
+        s = __builtin_fma(s, g, 1.0);
+        s = __builtin_fma(s, g, 1.0);
+        return ldexp(s, static_cast<int>(n) + bits);
+    }
+    // Rounded to an integer: adding 2^52 leaves it in the low bits.
+    __device__ __forceinline__ static uint64_t fixed(double w) {
+        return static_cast<uint64_t>(__double_as_longlong(w + 0x1p52)) & ((uint64_t{1} << 52) - 1);
+    }
+    __device__ __forceinline__ uint64_t weight(float x) const { return fixed(scaled(x)); }
 };
 
 // 16 bytes of logits from any element address.
@@ -140,12 +201,16 @@ __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
     for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(static_cast<unsigned long long>(v), off);
     return v;
 }
-__device__ __forceinline__ uint32_t wave_max32(uint32_t v) {
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint32_t o = __shfl_xor(v, off);
-        v = v > o ? v : o;
-    }
+__device__ __forceinline__ uint32_t wave_sum32(uint32_t v) {
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
     return v;
+}
+__device__ __forceinline__ float2 wave_range(float2 r) {
+    for (int off = 32; off > 0; off >>= 1) {
+        r.x = fmaxf(r.x, __shfl_xor(r.x, off));
+        r.y = fminf(r.y, __shfl_xor(r.y, off));
+    }
+    return r;
 }
 __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
     const int lane = lane_id();
@@ -156,24 +221,29 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
     return v;
 }
 
-// The row's largest key, by every wavefront for itself.
-__device__ __forceinline__ uint32_t row_max(const SampleArgs &a, int row) {
-    uint32_t m = 0;
+// Largest and smallest token logit of a row, by every wavefront for itself;
+// -infinity as the largest: no token.
+__device__ __forceinline__ float2 row_range(const SampleArgs &a, int row) {
+    float2 r = {-__builtin_inff(), __builtin_inff()};
     for (int p = lane_id(); p < a.parts; p += kWave) {
-        const uint32_t v = a.part_max[static_cast<int64_t>(row) * a.parts + p];
-        m = m > v ? m : v;
+        const float2 v = a.part_range[static_cast<int64_t>(row) * a.parts + p];
+        r.x = fmaxf(r.x, v.x);
+        r.y = fminf(r.y, v.y);
     }
-    return uniform(wave_max32(m));
+    r = wave_range(r);
+    r.x = __uint_as_float(uniform(__float_as_uint(r.x)));
+    r.y = __uint_as_float(uniform(__float_as_uint(r.y)));
+    return r;
 }
 
-// ---- largest key of each part; clears the rows' histograms ----
+// ---- range of each part; clears the rows' histograms and sets their state ----
 template <class T>
 __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
-    __shared__ uint32_t s_max[kPartBlock / kWave];
+    __shared__ float2 s_range[kPartBlock / kWave];
     const int row = blockIdx.y, part = blockIdx.x;
     const T *x = row_at<T>(a, row);
     using L = Logits<T>;
-    uint32_t m = 0;
+    float2 r = {-__builtin_inff(), __builtin_inff()};
 #pragma unroll
     for (int j = 0; j < kPartItems / L::kN; ++j) {
         const int i = part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN;
@@ -182,46 +252,126 @@ __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
         v.load(x, i, a.vocab);
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) {
-            const uint32_t k = key_of(v.x[e]);
-            m = m > k ? m : k;
+            r.x = fmaxf(r.x, v.x[e]);  // NaN gives way
+            r.y = fminf(r.y, v.x[e] > -__builtin_inff() ? v.x[e] : __builtin_inff());
         }
     }
-    m = wave_max32(m);
-    if (lane_id() == 0) s_max[threadIdx.x / kWave] = m;
-    if (a.hist_count != nullptr) {
+    r = wave_range(r);
+    if (lane_id() == 0) s_range[threadIdx.x / kWave] = r;
+    const Filters f(a, row);
+    if (a.hist_count != nullptr && f.searched()) {
         for (int b = part * kPartBlock + static_cast<int>(threadIdx.x); b < kBins; b += a.parts * kPartBlock) {
             a.hist_mass[static_cast<int64_t>(row) * kBins + b] = 0;
             a.hist_count[static_cast<int64_t>(row) * kBins + b] = 0;
         }
     }
+    if (part == 0 && threadIdx.x == 0) {
+        RowState s{};
+        s.extra = -1;
+        if (f.top_k == 1) {  // the first of the order is in bin 0
+            s.lo = s.hi = 0;
+        } else {             // everything is kept, unless the histogram says otherwise
+            s.lo = kBins;
+            s.hi = kBins - 1;
+        }
+        a.state[row] = s;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kPartBlock / kWave; ++w) m = m > s_max[w] ? m : s_max[w];
-        a.part_max[static_cast<int64_t>(row) * a.parts + part] = m;
+        for (int w = 1; w < kPartBlock / kWave; ++w) {
+            r.x = fmaxf(r.x, s_range[w].x);
+            r.y = fminf(r.y, s_range[w].y);
+        }
+        a.part_range[static_cast<int64_t>(row) * a.parts + part] = r;
     }
 }
 
-// ---- counts and weights by the keys' top 11 bits ----
+// ---- counts and weights by bin, and the border bins ----
 struct Hist {
     unsigned long long mass[kBins];
     uint32_t count[kBins];
 };
 
-__device__ __forceinline__ void hist_add(Hist &h, uint32_t bin, uint64_t w) {
+__device__ __forceinline__ void hist_count(Hist &h, int bin) {
     __hip_atomic_fetch_add(&h.count[bin], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void hist_mass(Hist &h, int bin, uint64_t w) {
     if (w != 0)
         __hip_atomic_fetch_add(&h.mass[bin], static_cast<unsigned long long>(w), __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
+// Where a running sum over the bins reaches a goal.
+struct Found {
+    int bin;                    // -1: nowhere
+    uint32_t before, count;     // keys in earlier bins, in this one
+    uint64_t before_mass, mass;
+};
+
+template <int BLOCK>
+struct FindShared {
+    unsigned long long wave_mass[BLOCK / kWave];
+    uint32_t wave_count[BLOCK / kWave];
+    Found found[3];
+};
+
+// The first bin at whose end the count reaches `need` (found[0]) and the
+// first at whose end the mass reaches target (found[1], found[2]), from
+// `before` and `before_mass` at the first bin on. REVERSED: from the last bin down.
+template <int BLOCK, bool REVERSED>
+__device__ __forceinline__ void find_bins(const Hist &h, FindShared<BLOCK> &sh, uint32_t need, double target1,
+                                          double target2, uint32_t before, uint64_t before_mass) {
+    constexpr int kEach = kBins / BLOCK;
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    uint32_t c[kEach], cs = 0;
+    uint64_t m[kEach], ms = 0;
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        const int b = static_cast<int>(threadIdx.x) * kEach + s;
+        c[s] = h.count[REVERSED ? kBins - 1 - b : b];
+        m[s] = h.mass[REVERSED ? kBins - 1 - b : b];
+        cs += c[s];
+        ms += m[s];
+    }
+    const uint32_t ci = wave_inclusive_scan<SumU32>(cs);
+    const uint64_t mi = wave_scan64(ms);
+    if (lane == kWave - 1) {
+        sh.wave_count[w] = ci;
+        sh.wave_mass[w] = mi;
+    }
+    if (threadIdx.x < 3) sh.found[threadIdx.x].bin = -1;
+    __syncthreads();
+    uint32_t cr = before + ci - cs;
+    uint64_t mr = before_mass + mi - ms;
+    for (int i = 0; i < w; ++i) {
+        cr += sh.wave_count[i];
+        mr += sh.wave_mass[i];
+    }
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        const int b = static_cast<int>(threadIdx.x) * kEach + s;
+        const Found f{REVERSED ? kBins - 1 - b : b, cr, c[s], mr, m[s]};
+        const double m0 = static_cast<double>(mr), m1 = static_cast<double>(mr + m[s]);
+        // one bin only meets each of these
+        if (cr < need && cr + c[s] >= need) sh.found[0] = f;
+        if (m0 < target1 && m1 >= target1) sh.found[1] = f;
+        if (m0 < target2 && m1 >= target2) sh.found[2] = f;
+        cr += c[s];
+        mr += m[s];
+    }
+    __syncthreads();
+}
+
 template <class T>
 __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     __shared__ Hist h;
+    __shared__ FindShared<kHistBlock> sh;
+    __shared__ bool s_last;
     const int row = blockIdx.y;
-    const uint32_t max_key = row_max(a, row);
-    const Settings st(a, row, max_key);
-    // the largest logit alone needs no histogram
-    if (max_key == 0 || st.top_k == 1 || (st.top_k == 0 && st.top_p > 1.0f)) return;
+    const Filters f(a, row);
+    if (!f.searched()) return;
+    const Scale sc(a, row, f, row_range(a, row));
     for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
         h.mass[b] = 0;
         h.count[b] = 0;
@@ -230,146 +380,292 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     const T *x = row_at<T>(a, row);
     using L = Logits<T>;
     const int begin = blockIdx.x * kHistPart;
-    const int end = a.vocab - begin < kHistPart ? a.vocab : begin + kHistPart;
-    for (int i = begin + static_cast<int>(threadIdx.x) * L::kN; i < end; i += kHistBlock * L::kN) {
+    const bool counts = f.top_k > 0, masses = f.nucleus() && !f.small_k();
+#pragma unroll
+    for (int j = 0; j < kHistPart / (kHistBlock * L::kN); ++j) {
+        const int i = begin + (j * kHistBlock + static_cast<int>(threadIdx.x)) * L::kN;
+        if (i >= a.vocab) continue;
         L v;
         v.load(x, i, a.vocab);
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) {
-            const uint32_t k = key_of(v.x[e]);
-            if (k != 0) hist_add(h, k >> 21, st.fixed(st.weight(v.x[e])));
+            if (!(v.x[e] > -__builtin_inff())) continue;
+            const int b = sc.bin(v.x[e]);
+            if (counts) hist_count(h, b);
+            if (masses) hist_mass(h, b, sc.weight(v.x[e]));
         }
     }
     __syncthreads();
+    unsigned long long *gm = reinterpret_cast<unsigned long long *>(a.hist_mass) + static_cast<int64_t>(row) * kBins;
+    uint32_t *gc = a.hist_count + static_cast<int64_t>(row) * kBins;
     for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
-        if (h.count[b] == 0) continue;
-        __hip_atomic_fetch_add(a.hist_count + static_cast<int64_t>(row) * kBins + b, h.count[b], __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+        if (h.count[b] != 0)
+            __hip_atomic_fetch_add(gc + b, h.count[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (h.mass[b] != 0)
-            __hip_atomic_fetch_add(reinterpret_cast<unsigned long long *>(a.hist_mass) +
-                                       static_cast<int64_t>(row) * kBins + b,
-                                   h.mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_fetch_add(gm + b, h.mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // The workgroup that adds last finds the border bins. Everything it reads
+    // was written by agent-scope atomics, which take effect beyond the XCDs'
+    // own L2 caches: once each wavefront has waited for its own to be
+    // acknowledged, agent-scope loads see them, and no cache has to be written
+    // back (with release fences instead, this kernel took 641 us for 256 rows
+    // of 131,072).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(&a.state[row].done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    uint32_t n = 0;
+    uint64_t total = 0;
+    for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
+        h.count[b] = __hip_atomic_load(gc + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        h.mass[b] = __hip_atomic_load(gm + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        n += h.count[b];
+        total += h.mass[b];
+    }
+    n = wave_sum32(n);
+    total = wave_sum64(total);
+    if (lane_id() == 0) {
+        sh.wave_count[threadIdx.x / kWave] = n;
+        sh.wave_mass[threadIdx.x / kWave] = total;
+    }
+    __syncthreads();
+    n = 0;
+    total = 0;
+    for (int i = 0; i < kHistBlock / kWave; ++i) {
+        n += sh.wave_count[i];
+        total += sh.wave_mass[i];
+    }
+    __syncthreads();
+    RowState *s = a.state + row;
+    const uint32_t k = static_cast<uint32_t>(f.top_k);
+    const double p = static_cast<double>(f.top_p);
+    if (f.small_k()) {
+        // all of the first top_k are collected (all there are, if fewer)
+        find_bins<kHistBlock, false>(h, sh, k < n ? k : n, -1.0, -1.0, 0, 0);
+        if (threadIdx.x == 0) {
+            s->lo = 0;
+            s->hi = sh.found[0].bin;
+        }
+    } else if (f.top_k > 0 && k < n) {
+        find_bins<kHistBlock, false>(h, sh, k, -1.0, -1.0, 0, 0);
+        const Found fk = sh.found[0];
+        __syncthreads();
+        if (!f.nucleus()) {
+            if (threadIdx.x == 0) {
+                s->lo = s->hi = fk.bin;
+                s->count = fk.before;
+            }
+            return;
+        }
+        // top_p's border lies between those that the least and the most
+        // weight of the first top_k would give
+        const double low = p * static_cast<double>(fk.before_mass),
+                     high = p * static_cast<double>(fk.before_mass + fk.mass);
+        find_bins<kHistBlock, false>(h, sh, 0, low, high, 0, 0);
+        if (threadIdx.x == 0) {
+            const Found fl = sh.found[1], fh = sh.found[2];
+            s->lo = fl.bin < 0 ? 0 : fl.bin;
+            s->hi = fh.bin < 0 ? fk.bin : fh.bin;
+            s->mass = fl.bin < 0 ? 0 : fl.before_mass;
+            s->count = fl.bin < 0 ? 0 : fl.before;
+            if (fk.bin > s->hi) {
+                s->extra = fk.bin;
+                s->extra_mass = fk.before_mass;
+                s->extra_count = fk.before;
+            }
+        }
+    } else if (f.nucleus()) {
+        find_bins<kHistBlock, false>(h, sh, 0, p * static_cast<double>(total), -1.0, 0, 0);
+        if (threadIdx.x == 0 && sh.found[1].bin >= 0) {
+            s->lo = s->hi = sh.found[1].bin;
+            s->mass = sh.found[1].before_mass;
+            s->total = total;
+        }
     }
 }
 
-// ---- the border of a row ----
-struct Found {
-    uint32_t bin, count;          // the border's bin, its keys
-    uint32_t above;               // keys in larger bins
-    unsigned long long above_mass, mass;
-};
+// ---- kept weight of the better bins by part, and the logits of the border bins ----
+// An entry of the list orders as the row does, from the largest down.
+__device__ __forceinline__ uint64_t entry_of(uint32_t key, int i) {
+    return static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(i);
+}
 
-struct BorderShared {
-    Hist h;
-    unsigned long long wave_mass[kBorderBlock / kWave];
-    uint32_t wave_count[kBorderBlock / kWave];
-    Found found;
-    uint32_t cut;
-    unsigned long long total_mass;
-};
-
-// The bin, from the largest down, that holds the `need`-th key (by count) or
-// in which the mass before a key reaches `target` (by mass); `before` and
-// `before_mass` lie above all bins. The last bin with keys stands where none does.
-__device__ __forceinline__ Found find_bin(BorderShared &sh, bool by_count, uint32_t need, double target,
-                                          uint32_t before, uint64_t before_mass) {
+template <class T>
+__global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
+    constexpr int kWaves = kPartBlock / kWave;
+    __shared__ float s_x[kWaves][kPart / kWaves];
+    __shared__ unsigned long long s_mass[kWaves];
+    __shared__ uint32_t s_count[kWaves];
+    const int row = blockIdx.y, part = blockIdx.x;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const int b0 = kBins - 1 - 2 * static_cast<int>(threadIdx.x), b1 = b0 - 1;
-    const uint32_t c0 = sh.h.count[b0], c1 = sh.h.count[b1];
-    const uint64_t m0 = sh.h.mass[b0], m1 = sh.h.mass[b1];
-    const uint32_t ci = wave_inclusive_scan<SumU32>(c0 + c1);
-    const uint64_t mi = wave_scan64(m0 + m1);
-    if (lane == kWave - 1) {
-        sh.wave_count[w] = ci;
-        sh.wave_mass[w] = mi;
-    }
-    __syncthreads();
-    uint32_t c = before + ci - c0 - c1;
-    uint64_t m = before_mass + mi - m0 - m1;
-    for (int i = 0; i < w; ++i) {
-        c += sh.wave_count[i];
-        m += sh.wave_mass[i];
-    }
+    const T *x = row_at<T>(a, row);
+    using L = Logits<T>;
+    constexpr int kEach = kPartItems / L::kN;
+    L v[kEach];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const uint32_t cc = s == 0 ? c0 : c1;
-        const uint64_t mm = s == 0 ? m0 : m1;
-        // one bin only meets this: the first whose end reaches the goal
-        const bool start = by_count ? c < need : static_cast<double>(m) < target;
-        const bool stop = by_count ? c + cc >= need : static_cast<double>(m + mm) >= target;
-        if (cc != 0 && start && stop) {
-            sh.found.bin = static_cast<uint32_t>(s == 0 ? b0 : b1);
-            sh.found.count = cc;
-            sh.found.above = c;
-            sh.found.above_mass = m;
-            sh.found.mass = mm;
+    for (int j = 0; j < kEach; ++j)
+        v[j].load(x, part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN, a.vocab);
+    const Filters f(a, row);
+    const Scale sc(a, row, f, row_range(a, row));
+    RowState *st = a.state + row;
+    const int lo = st->lo, hi = st->hi, extra = st->extra;
+    uint64_t mass = 0;
+    uint32_t count = 0;
+    const auto add = [&](float xe) {
+        const double we = sc.scaled(xe);
+        if (we >= sc.min_w || xe == sc.top) {
+            mass += Scale::fixed(we);
+            ++count;
         }
-        c += cc;
-        m += mm;
+    };
+    if (lo >= kBins) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+#pragma unroll
+            for (int e = 0; e < L::kN; ++e)
+                if (v[j].x[e] > -__builtin_inff()) add(v[j].x[e]);
+        }
+    } else {
+        // places in [0, kept) are kept, those in [kept, end) and [far, far_end)
+        // collected; the last bin's end is a NaN, which nothing reaches
+        const float kept = static_cast<float>(lo);
+        const float end = hi >= kBins - 1 ? __builtin_nanf("") : static_cast<float>(hi + 1);
+        const float far = extra < 0 ? __builtin_nanf("") : static_cast<float>(extra);
+        const float far_end = extra >= kBins - 1 ? __builtin_nanf("") : far + 1.0f;
+        uint32_t packed = 0, listed = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+#pragma unroll
+            for (int e = 0; e < L::kN; ++e) {
+                const float xe = v[j].x[e];
+                const bool token = xe > -__builtin_inff();
+                const float pl = sc.place(xe);
+                if (lo > 0) {  // packed first, so that the exponentials run on full wavefronts
+                    const bool keep = token && pl < kept;
+                    const uint64_t mask = ballot(keep);
+                    if (keep) s_x[w][packed + mbcnt64(mask)] = xe;
+                    packed += static_cast<uint32_t>(__builtin_popcountll(mask));
+                }
+                const bool list = token && ((pl >= kept && !(pl >= end)) || (pl >= far && !(pl >= far_end)));
+                listed |= list ? 1u << (j * L::kN + e) : 0u;
+            }
+        }
+        if (ballot(listed != 0) != 0) {
+            const uint32_t mine = static_cast<uint32_t>(__builtin_popcount(listed));
+            const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
+            uint32_t at = 0;
+            if (lane == kWave - 1)
+                at = __hip_atomic_fetch_add(&st->listed, incl, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            at = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(at), kWave - 1)) + incl - mine;
+            uint64_t *list = a.list + static_cast<int64_t>(row) * kList;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                const int i = part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN;
+#pragma unroll
+                for (int e = 0; e < L::kN; ++e) {
+                    if ((listed >> (j * L::kN + e)) & 1u) {
+                        if (at < kList) list[at] = entry_of(key_of(v[j].x[e]), i + e);
+                        ++at;
+                    }
+                }
+            }
+        }
+        for (uint32_t i = lane; i < packed; i += kWave) add(s_x[w][i]);
+    }
+    mass = wave_sum64(mass);
+    count = wave_sum32(count);
+    if (lane == 0) {
+        s_mass[w] = mass;
+        s_count[w] = count;
     }
     __syncthreads();
-    const Found f = sh.found;
-    __syncthreads();
-    return f;
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kWaves; ++i) {
+            mass += s_mass[i];
+            count += s_count[i];
+        }
+        a.part_mass[static_cast<int64_t>(row) * a.parts + part] = mass;
+        a.part_count[static_cast<int64_t>(row) * a.parts + part] = count;
+    }
 }
 
-// Histogram of the keys whose bits above `shift + width` equal `prefix`, by
-// the `width` bits at `shift`.
+// ---- border and token ----
+struct TokenShared {
+    union {
+        struct {
+            unsigned long long entry[kList];
+        } list;
+        Hist h;
+    };
+    FindShared<kTokenBlock> find;
+    unsigned long long mass[kPartsMax];
+    uint32_t count;
+    uint32_t cut;
+    uint32_t border_key, border_cut;
+    int part;
+    unsigned long long goal, total;
+};
+
+// The slow way, for a row whose border bins hold more logits than the list
+// (equal or nearly equal logits in numbers): the border key digit by digit.
 template <class T>
-__device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Settings &st, BorderShared &sh,
+__device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Scale &sc, TokenShared &sh,
                                        uint32_t prefix, int shift, int width) {
-    for (int b = threadIdx.x; b < kBins; b += kBorderBlock) {
+    for (int b = threadIdx.x; b < kBins; b += kTokenBlock) {
         sh.h.mass[b] = 0;
         sh.h.count[b] = 0;
     }
     __syncthreads();
     using L = Logits<T>;
-    for (int i = static_cast<int>(threadIdx.x) * L::kN; i < a.vocab; i += kBorderBlock * L::kN) {
+    for (int i = static_cast<int>(threadIdx.x) * L::kN; i < a.vocab; i += kTokenBlock * L::kN) {
         L v;
         v.load(x, i, a.vocab);
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) {
             const uint32_t k = key_of(v.x[e]);
-            if (k >> (shift + width) == prefix && k != 0)
-                hist_add(sh.h, (k >> shift) & ((1u << width) - 1u), st.fixed(st.weight(v.x[e])));
+            if (k == 0 || (shift + width < 32 && k >> (shift + width) != prefix)) continue;
+            const int b = static_cast<int>((k >> shift) & ((1u << width) - 1u));
+            hist_count(sh.h, b);
+            hist_mass(sh.h, b, sc.weight(v.x[e]));
         }
     }
     __syncthreads();
 }
 
-// The border key of one filter: where the `need`-th key, or the mass
-// `target`, is reached.
+// The key at which the count reaches `need`, or the mass `target` (bin: the
+// key; -1 where neither is reached).
 template <class T>
-__device__ __forceinline__ Found border_key(const SampleArgs &a, int row, const T *x, const Settings &st,
-                                            BorderShared &sh, bool by_count, uint32_t need, double target) {
-    for (int b = threadIdx.x; b < kBins; b += kBorderBlock) {
-        sh.h.mass[b] = a.hist_mass[static_cast<int64_t>(row) * kBins + b];
-        sh.h.count[b] = a.hist_count[static_cast<int64_t>(row) * kBins + b];
+__device__ __forceinline__ Found border_key(const SampleArgs &a, const T *x, const Scale &sc, TokenShared &sh,
+                                            uint32_t need, double target) {
+    const int which = need > 0 ? 0 : 1;
+    uint32_t key = 0, before = 0;
+    uint64_t before_mass = 0;
+    Found f{};
+    for (int level = 0; level < 3; ++level) {
+        const int shift = level == 0 ? 21 : (level == 1 ? 10 : 0), width = level == 2 ? 10 : 11;
+        refine(a, x, sc, sh, key, shift, width);
+        find_bins<kTokenBlock, true>(sh.h, sh.find, need, target, -1.0, before, before_mass);
+        f = sh.find.found[which];
+        __syncthreads();
+        if (f.bin < 0) return f;
+        key = key << width | static_cast<uint32_t>(f.bin);
+        before = f.before;
+        before_mass = f.before_mass;
     }
-    __syncthreads();
-    Found f = find_bin(sh, by_count, need, target, 0, 0);
-    uint32_t key = f.bin;
-    refine(a, x, st, sh, key, 10, 11);
-    f = find_bin(sh, by_count, need, target, f.above, f.above_mass);
-    key = key << 11 | f.bin;
-    if (sizeof(T) == 4) {
-        refine(a, x, st, sh, key, 0, 10);
-        f = find_bin(sh, by_count, need, target, f.above, f.above_mass);
-        key = key << 10 | f.bin;
-    } else {  // a 16-bit logit's low bits follow from its sign
-        key = key << 10 | ((key >> 21) != 0 ? 0u : 0x3ffu);
-    }
-    f.bin = key;
+    f.bin = static_cast<int>(key);
     return f;
 }
 
 // The index of the `need`-th logit, in index order, with this key.
 template <class T>
-__device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, BorderShared &sh, uint32_t key,
+__device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, TokenShared &sh, uint32_t key,
                                               uint32_t need) {
     using L = Logits<T>;
-    constexpr int kWaves = kBorderBlock / kWave;
+    constexpr int kWaves = kTokenBlock / kWave;
     constexpr int kStep = kWave * L::kN;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
@@ -383,11 +679,12 @@ __device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, B
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) count += key_of(v.x[e]) == key ? 1u : 0u;
     }
-    for (int off = 32; off > 0; off >>= 1) count += __shfl_xor(count, off);
-    if (lane == 0) sh.wave_count[w] = count;
+    count = wave_sum32(count);
+    if (threadIdx.x == 0) sh.cut = kNoCut;
+    if (lane == 0) sh.find.wave_count[w] = count;
     __syncthreads();
     uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += sh.wave_count[i];
+    for (int i = 0; i < w; ++i) before += sh.find.wave_count[i];
     if (before < need && before + count >= need) {  // this wavefront holds it
         for (int s = first; s < last; ++s) {
             const int i = s * kStep + lane * L::kN;
@@ -409,154 +706,109 @@ __device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, B
         }
     }
     __syncthreads();
-    return sh.cut;
+    const uint32_t cut = sh.cut;
+    __syncthreads();
+    return cut;
 }
 
+// A kept logit's weight; 0 and not counted for the others.
+struct Border {
+    uint32_t key, cut;  // smallest kept key, last index at which it is kept
+    __device__ __forceinline__ uint64_t weight(const Scale &sc, float x, int i, bool &kept) const {
+        const uint32_t k = key_of(x);
+        kept = false;
+        if (k == 0 || k < key || (k == key && static_cast<uint32_t>(i) > cut)) return 0;
+        const double w = sc.scaled(x);
+        kept = w >= sc.min_w || x == sc.top;
+        return kept ? Scale::fixed(w) : 0;
+    }
+};
+
 template <class T>
-__global__ __launch_bounds__(kBorderBlock) void sample_border_kernel(SampleArgs a) {
-    __shared__ BorderShared sh;
-    const int row = blockIdx.x;
-    const uint32_t max_key = row_max(a, row);
-    const Settings st(a, row, max_key);
-    RowState out{1u, kNoCut};  // every token
-    const T *x = row_at<T>(a, row);
-    if (threadIdx.x == 0) sh.cut = kNoCut;
-    __syncthreads();
-    if (max_key != 0 && st.top_k == 1) {
-        out.border = max_key;
-        out.cut = tie_index(a, x, sh, max_key, 1);
-    } else if (max_key != 0 && (st.top_k > 0 || st.top_p <= 1.0f)) {
-        uint64_t mass = 0;       // of the keys that top_k leaves
-        uint32_t ties = 0, have = 0;
-        if (st.top_k > 0) {
-            // fewer tokens than top_k: all of them
-            uint32_t n = 0;
-            for (int b = threadIdx.x; b < kBins; b += kBorderBlock) {
-                n += a.hist_count[static_cast<int64_t>(row) * kBins + b];
-                mass += a.hist_mass[static_cast<int64_t>(row) * kBins + b];
-            }
-            for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off);
-            mass = wave_sum64(mass);
-            if (lane_id() == 0) {
-                sh.wave_count[threadIdx.x / kWave] = n;
-                sh.wave_mass[threadIdx.x / kWave] = mass;
-            }
-            __syncthreads();
-            n = 0;
-            mass = 0;
-            for (int i = 0; i < kBorderBlock / kWave; ++i) {
-                n += sh.wave_count[i];
-                mass += sh.wave_mass[i];
-            }
-            __syncthreads();
-            if (n > static_cast<uint32_t>(st.top_k)) {
-                const Found f = border_key(a, row, x, st, sh, true, static_cast<uint32_t>(st.top_k), 0.0);
-                out.border = f.bin;
-                ties = static_cast<uint32_t>(st.top_k) - f.above;
-                have = f.count;
-                mass = f.above_mass + ties * st.fixed(st.weight(value_of(f.bin)));
-            }
-        } else {
-            for (int b = threadIdx.x; b < kBins; b += kBorderBlock)
-                mass += a.hist_mass[static_cast<int64_t>(row) * kBins + b];
-            mass = wave_sum64(mass);
-            if (lane_id() == 0) sh.wave_mass[threadIdx.x / kWave] = mass;
-            __syncthreads();
-            mass = 0;
-            for (int i = 0; i < kBorderBlock / kWave; ++i) mass += sh.wave_mass[i];
-            __syncthreads();
+__device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, const Filters &f, const Scale &sc,
+                                              TokenShared &sh) {
+    Border out{1u, kNoCut};
+    uint32_t ties = 0, have = 0;
+    double all = -1.0;  // weight that top_k leaves
+    if (f.top_k == 1) {
+        out.key = key_of(sc.top);
+        out.cut = tie_index(a, x, sh, out.key, 1);
+        return out;
+    }
+    if (f.top_k > 0) {
+        const Found k = border_key(a, x, sc, sh, static_cast<uint32_t>(f.top_k), -1.0);
+        if (k.bin != -1) {
+            out.key = static_cast<uint32_t>(k.bin);
+            ties = static_cast<uint32_t>(f.top_k) - k.before;
+            have = k.count;
+            all = static_cast<double>(k.before_mass + ties * sc.weight(value_of(out.key)));
         }
-        if (st.top_p <= 1.0f) {
-            const double target = static_cast<double>(st.top_p) * static_cast<double>(mass);
-            const Found f = border_key(a, row, x, st, sh, false, 0, target);
-            // ties j = 0, 1, ... are kept while above_mass + j * weight < target
-            const uint64_t wt = st.fixed(st.weight(value_of(f.bin)));
-            uint32_t j = f.count;
+    }
+    if (f.nucleus()) {
+        if (all < 0.0) {  // all of the row's
+            refine(a, x, sc, sh, 0, 21, 11);
+            uint64_t m = 0;
+            for (int b = threadIdx.x; b < kBins; b += kTokenBlock) m += sh.h.mass[b];
+            m = wave_sum64(m);
+            if (lane_id() == 0) sh.find.wave_mass[threadIdx.x / kWave] = m;
+            __syncthreads();
+            m = 0;
+            for (int i = 0; i < kTokenBlock / kWave; ++i) m += sh.find.wave_mass[i];
+            __syncthreads();
+            all = static_cast<double>(m);
+        }
+        const double target = static_cast<double>(f.top_p) * all;
+        const Found p = border_key(a, x, sc, sh, 0, target);
+        if (p.bin != -1) {
+            // ties j = 0, 1, ... are kept while before_mass + j * weight < target
+            const uint32_t key = static_cast<uint32_t>(p.bin);
+            const uint64_t wt = sc.weight(value_of(key));
+            uint32_t j = p.count;
             if (wt != 0) {
-                const double q = (target - static_cast<double>(f.above_mass)) / static_cast<double>(wt);
-                uint32_t g = q < static_cast<double>(f.count) ? static_cast<uint32_t>(q) : f.count;
-                while (g > 0 && static_cast<double>(f.above_mass + (g - 1) * wt) >= target) --g;
-                while (g < f.count && static_cast<double>(f.above_mass + g * wt) < target) ++g;
-                j = g;
+                const double q = (target - static_cast<double>(p.before_mass)) / static_cast<double>(wt);
+                j = q < static_cast<double>(p.count) ? static_cast<uint32_t>(q) : p.count;
+                while (j > 0 && static_cast<double>(p.before_mass + (j - 1) * wt) >= target) --j;
+                while (j < p.count && static_cast<double>(p.before_mass + j * wt) < target) ++j;
             }
-            if (f.bin != out.border || j < ties || ties == 0) {
-                out.border = f.bin;
+            if (key != out.key || j < ties || ties == 0) {
+                out.key = key;
                 ties = j;
-                have = f.count;
+                have = p.count;
             }
         }
-        if (ties < have) out.cut = tie_index(a, x, sh, out.border, ties);
     }
-    if (threadIdx.x == 0) a.state[row] = out;
+    if (ties < have) out.cut = tie_index(a, x, sh, out.key, ties);
+    return out;
 }
 
-// ---- kept weight and count of each part ----
-// A kept logit's weight as an integer; 0 and not counted for the others.
-__device__ __forceinline__ uint64_t kept_weight(const Settings &st, const RowState &rs, uint32_t key, float x, int i,
-                                                uint32_t max_key, bool &kept) {
-    kept = false;
-    if (key == 0 || key < rs.border || (key == rs.border && static_cast<uint32_t>(i) > rs.cut)) return 0;
-    const double w = st.weight(x);
-    kept = key == max_key || w >= st.min_w;
-    return kept ? st.fixed(w) : 0;
+// Sorts the first n entries (n2 a power of two, filled up with 0) from the largest down.
+__device__ __forceinline__ void sort_list(unsigned long long *e, int n2) {
+    for (int size = 2; size <= n2; size <<= 1) {
+        for (int dist = size >> 1; dist > 0; dist >>= 1) {
+            for (int t = threadIdx.x; t < n2 / 2; t += kTokenBlock) {
+                const int i = 2 * t - (t & (dist - 1)), j = i + dist;
+                const unsigned long long u = e[i], v = e[j];
+                if ((u < v) == ((i & size) == 0)) {
+                    e[i] = v;
+                    e[j] = u;
+                }
+            }
+            __syncthreads();
+        }
+    }
 }
 
 template <class T>
-__global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
-    __shared__ unsigned long long s_mass[kPartBlock / kWave];
-    __shared__ uint32_t s_count[kPartBlock / kWave];
-    const int row = blockIdx.y, part = blockIdx.x;
-    const uint32_t max_key = row_max(a, row);
-    const Settings st(a, row, max_key);
-    const RowState rs = a.hist_count != nullptr ? a.state[row] : RowState{1u, kNoCut};
-    const T *x = row_at<T>(a, row);
-    using L = Logits<T>;
-    uint64_t mass = 0;
-    uint32_t count = 0;
-#pragma unroll
-    for (int j = 0; j < kPartItems / L::kN; ++j) {
-        const int i = part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN;
-        if (i >= a.vocab) continue;
-        L v;
-        v.load(x, i, a.vocab);
-#pragma unroll
-        for (int e = 0; e < L::kN; ++e) {
-            bool kept;
-            mass += kept_weight(st, rs, key_of(v.x[e]), v.x[e], i + e, max_key, kept);
-            count += kept ? 1u : 0u;
-        }
-    }
-    mass = wave_sum64(mass);
-    for (int off = 32; off > 0; off >>= 1) count += __shfl_xor(count, off);
-    if (lane_id() == 0) {
-        s_mass[threadIdx.x / kWave] = mass;
-        s_count[threadIdx.x / kWave] = count;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kPartBlock / kWave; ++w) {
-            mass += s_mass[w];
-            count += s_count[w];
-        }
-        a.part_mass[static_cast<int64_t>(row) * a.parts + part] = mass;
-        a.part_count[static_cast<int64_t>(row) * a.parts + part] = count;
-    }
-}
-
-// ---- the token ----
-template <class T>
-__global__ __launch_bounds__(kPartBlock) void sample_token_kernel(SampleArgs a) {
-    __shared__ unsigned long long s_wave[kPartBlock / kWave];
-    __shared__ int s_part;
-    __shared__ unsigned long long s_before, s_total;
+__global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a) {
+    __shared__ TokenShared sh;
+    constexpr int kWaves = kTokenBlock / kWave;
     const int row = blockIdx.x;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const uint32_t max_key = row_max(a, row);
-    const Settings st(a, row, max_key);
-    const RowState rs = a.hist_count != nullptr ? a.state[row] : RowState{1u, kNoCut};
+    const Filters f(a, row);
+    const float2 range = row_range(a, row);
     const int64_t base = static_cast<int64_t>(row) * a.parts;
-    if (max_key == 0) {
+    if (range.x == -__builtin_inff()) {
         if (threadIdx.x == 0) {
             a.tokens[row] = -1;
             if (a.kept != nullptr) a.kept[row] = 0;
@@ -564,88 +816,210 @@ __global__ __launch_bounds__(kPartBlock) void sample_token_kernel(SampleArgs a) 
         }
         return;
     }
-    if (w == 0) {  // the part in which the running weight passes the goal
-        uint64_t total = 0;
-        uint32_t count = 0;
-        for (int p = lane; p < a.parts; p += kWave) {
-            total += a.part_mass[base + p];
-            count += a.part_count[base + p];
+    const Scale sc(a, row, f, range);
+    const RowState st = a.state[row];
+    const T *x = row_at<T>(a, row);
+    Border border{1u, kNoCut};
+    for (int p = threadIdx.x; p < a.parts; p += kTokenBlock) sh.mass[p] = a.part_mass[base + p];
+    uint32_t count = 0;
+    for (int p = threadIdx.x; p < a.parts; p += kTokenBlock) count += a.part_count[base + p];
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    if (st.listed > kList) {
+        border = slow_border(a, x, f, sc, sh);
+        // the parts' sums again, with the border known
+        count = 0;
+        for (int p = w; p < a.parts; p += kWaves) {
+            using L = Logits<T>;
+            uint64_t mass = 0;
+            for (int i = p * kPart + lane * L::kN; i < a.vocab && i < (p + 1) * kPart; i += kWave * L::kN) {
+                L v;
+                v.load(x, i, a.vocab);
+#pragma unroll
+                for (int e = 0; e < L::kN; ++e) {
+                    bool kept;
+                    mass += border.weight(sc, v.x[e], i + e, kept);
+                    count += kept ? 1u : 0u;
+                }
+            }
+            mass = wave_sum64(mass);
+            if (lane == 0) sh.mass[p] = mass;
         }
+        __syncthreads();
+    } else if (st.lo < kBins) {
+        // the collected logits in order; those of [lo, hi] come first
+        const int n = static_cast<int>(st.listed);
+        int n2 = 2;
+        while (n2 < n) n2 <<= 1;
+        for (int i = threadIdx.x; i < n2; i += kTokenBlock)
+            sh.list.entry[i] = i < n ? a.list[static_cast<int64_t>(row) * kList + i] : 0ull;
+        __syncthreads();
+        sort_list(sh.list.entry, n2);
+        // each thread's consecutive entries, their weights and the running sum
+        constexpr int kEach = kList / kTokenBlock;
+        uint64_t we[kEach], ms = 0;
+        double full[kEach];
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int i = static_cast<int>(threadIdx.x) * kEach + q;
+            full[q] = i < n ? sc.scaled(value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32))) : 0.0;
+            we[q] = Scale::fixed(full[q]);
+            ms += we[q];
+        }
+        const uint64_t mi = wave_scan64(ms);
+        if (lane == kWave - 1) sh.find.wave_mass[w] = mi;
+        if (threadIdx.x == 0) sh.total = 0;
+        __syncthreads();
+        uint64_t run = mi - ms;
+        for (int i = 0; i < w; ++i) run += sh.find.wave_mass[i];
+        // n1 entries lie in [lo, hi]; the rest in the extra bin
+        uint32_t mine = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int i = static_cast<int>(threadIdx.x) * kEach + q;
+            if (i < n && sc.bin(value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32))) <= st.hi) ++mine;
+        }
+        mine = wave_sum32(mine);
+        if (lane == 0) sh.find.wave_count[w] = mine;
+        __syncthreads();
+        uint32_t n1 = 0;
+        for (int i = 0; i < kWaves; ++i) n1 += sh.find.wave_count[i];
+        // entries of [lo, hi] that top_k leaves, and where the weight of the
+        // first top_k ends in the list
+        uint32_t nk = n1, end = n1;
+        uint64_t from = st.mass;  // weight before the list's first entry that counts towards `end`
+        if (f.top_k > 0 && st.total == 0) {
+            if (st.extra >= 0) {
+                const uint32_t more = static_cast<uint32_t>(f.top_k) - st.extra_count;
+                end = n1 + (more < static_cast<uint32_t>(n) - n1 ? more : static_cast<uint32_t>(n) - n1);
+                from = st.extra_mass;
+            } else {
+                const uint32_t more = static_cast<uint32_t>(f.top_k) - st.count;
+                nk = more < n1 ? more : n1;
+                end = nk;
+            }
+        }
+        // sum of the entries that lie between `from` and `end`: of the extra
+        // bin's alone, where there is one
+        const uint32_t skip = st.extra >= 0 ? n1 : 0u;
+        uint64_t part = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const uint32_t i = threadIdx.x * kEach + q;
+            if (i >= skip && i < end) part += we[q];
+        }
+        part = wave_sum64(part);
+        __syncthreads();
+        if (lane == 0) sh.find.wave_mass[w] = part;
+        __syncthreads();
+        uint64_t all = from;
+        for (int i = 0; i < kWaves; ++i) all += sh.find.wave_mass[i];
+        if (st.total != 0) all = st.total;
+        const double target = f.nucleus() ? static_cast<double>(f.top_p) * static_cast<double>(all) : __builtin_inf();
+        uint32_t keep = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const uint32_t i = threadIdx.x * kEach + q;
+            if (i < nk && static_cast<double>(st.mass + run) < target) {
+                keep = i + 1;
+                if (full[q] >= sc.min_w || sh.list.entry[i] >> 32 == key_of(sc.top)) {
+                    const uint32_t index = ~static_cast<uint32_t>(sh.list.entry[i]);
+                    __hip_atomic_fetch_add(&sh.mass[index >> kPartLg], static_cast<unsigned long long>(we[q]),
+                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                    ++count;
+                }
+            }
+            run += we[q];
+        }
+        for (int off = 32; off > 0; off >>= 1) {
+            const uint32_t o = __shfl_xor(keep, off);
+            keep = keep > o ? keep : o;
+        }
+        __syncthreads();
+        if (lane == 0) sh.find.wave_count[w] = keep;
+        __syncthreads();
+        keep = 0;
+        for (int i = 0; i < kWaves; ++i) keep = keep > sh.find.wave_count[i] ? keep : sh.find.wave_count[i];
+        if (keep > 0) {
+            border.key = static_cast<uint32_t>(sh.list.entry[keep - 1] >> 32);
+            border.cut = ~static_cast<uint32_t>(sh.list.entry[keep - 1]);
+        } else {  // nothing of the list: what precedes its first entry
+            border.key = static_cast<uint32_t>(sh.list.entry[0] >> 32) + 1u;
+        }
+    }
+    // the part in which the running weight passes the goal
+    count = wave_sum32(count);
+    if (lane == 0 && count != 0)
+        __hip_atomic_fetch_add(&sh.count, count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __syncthreads();
+    if (w == 0) {
+        uint64_t total = 0;
+        for (int p = lane; p < a.parts; p += kWave) total += sh.mass[p];
         total = wave_sum64(total);
-        for (int off = 32; off > 0; off >>= 1) count += __shfl_xor(count, off);
         float u = a.u[row];
         u = u > 0.0f ? u : 0.0f;
         u = u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f;
         const uint64_t goal = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         uint64_t before = 0;
         for (int p0 = 0; p0 < a.parts; p0 += kWave) {
-            const uint64_t m = p0 + lane < a.parts ? a.part_mass[base + p0 + lane] : 0;
+            const uint64_t m = p0 + lane < a.parts ? sh.mass[p0 + lane] : 0;
             const uint64_t incl = wave_scan64(m);
             const uint64_t hit = ballot(before + incl > goal);
             if (hit != 0) {
                 const int l = __builtin_ctzll(hit);
                 if (lane == l) {
-                    s_part = p0 + l;
-                    s_before = goal - (before + incl - m);  // what is left to pass in the part
-                    s_total = total;
+                    sh.part = p0 + l;
+                    sh.goal = goal - (before + incl - m);  // what is left to pass in the part
+                    sh.total = total;
                 }
                 break;
             }
             before += __shfl(static_cast<unsigned long long>(incl), kWave - 1);
         }
-        if (lane == 0 && a.kept != nullptr) a.kept[row] = static_cast<int32_t>(count);
+        if (lane == 0 && a.kept != nullptr) a.kept[row] = static_cast<int32_t>(sh.count);
     }
     __syncthreads();
-    const uint64_t goal = s_before;
-    const T *x = row_at<T>(a, row);
     // each thread takes consecutive logits of the part
-    const int first = s_part * kPart + static_cast<int>(threadIdx.x) * kPartItems;
-    float v[kPartItems];
-    uint64_t mass = 0;
-    using L = Logits<T>;
+    constexpr int kEach = kPart / kTokenBlock;
+    const uint64_t goal = sh.goal;
+    const int first = sh.part * kPart + static_cast<int>(threadIdx.x) * kEach;
+    float v[kEach];
+    uint64_t we[kEach], ms = 0;
 #pragma unroll
-    for (int j = 0; j < kPartItems / L::kN; ++j) {
-        L l;
-        l.load(x, first + j * L::kN, a.vocab);
-#pragma unroll
-        for (int e = 0; e < L::kN; ++e) {
-            const int i = j * L::kN + e;
-            bool kept;
-            v[i] = l.x[e];
-            mass += kept_weight(st, rs, key_of(v[i]), v[i], first + i, max_key, kept);
-        }
+    for (int e = 0; e < kEach; ++e) {
+        bool kept;
+        v[e] = first + e < a.vocab ? static_cast<float>(x[first + e]) : -__builtin_inff();
+        we[e] = border.weight(sc, v[e], first + e, kept);
+        ms += we[e];
     }
-    const uint64_t incl = wave_scan64(mass);
-    if (lane == kWave - 1) s_wave[w] = incl;
+    const uint64_t incl = wave_scan64(ms);
+    if (lane == kWave - 1) sh.find.wave_mass[w] = incl;
     __syncthreads();
-    uint64_t run = incl - mass;
-    for (int i = 0; i < w; ++i) run += s_wave[i];
-    if (run <= goal && run + mass > goal) {
+    uint64_t run = incl - ms;
+    for (int i = 0; i < w; ++i) run += sh.find.wave_mass[i];
+    if (run <= goal && run + ms > goal) {
         int at = -1;
         float chosen = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPartItems; ++i) {
-            bool kept;
-            run += kept_weight(st, rs, key_of(v[i]), v[i], first + i, max_key, kept);
+        for (int e = 0; e < kEach; ++e) {
+            run += we[e];
             if (at < 0 && run > goal) {
-                at = first + i;
-                chosen = v[i];
+                at = first + e;
+                chosen = v[e];
             }
         }
         a.tokens[row] = at;
         if (a.logprobs != nullptr) {
-            const double z = st.max_inf ? 0.0 : (static_cast<double>(chosen) - st.max) * st.inv_t;
-            a.logprobs[row] = static_cast<float>(z - log(static_cast<double>(s_total) / st.scale));
+            const double z = sc.top_inf ? 0.0 : (static_cast<double>(chosen) - sc.max) * (sc.rate / 1.4426950408889634);
+            a.logprobs[row] = static_cast<float>(z - log(ldexp(static_cast<double>(sh.total), -sc.bits)));
         }
     }
 }
 
 // ============================================================ host side ---
-constexpr int64_t kVocabMax = int64_t{1} << 22;
-
 struct SamplePlan {
     int64_t parts;
-    size_t hist_mass, part_mass, hist_count, part_max, part_count, state, bytes;  // offsets
+    size_t list, hist_mass, part_mass, part_range, state, hist_count, part_count, bytes;  // offsets
 };
 
 bool sample_sizes_ok(int64_t rows, int64_t vocab) {
@@ -663,10 +1037,11 @@ SamplePlan sample_plan(int64_t rows, int64_t vocab) {
         return here;
     };
     const size_t r = static_cast<size_t>(rows), g = static_cast<size_t>(p.parts);
+    p.list = take(r * kList * 8);
     p.hist_mass = take(r * kBins * 8);
-    p.part_mass = take(r * g * 8);
     p.hist_count = take(r * kBins * 4);
-    p.part_max = take(r * g * 4);
+    p.part_mass = take(r * g * 8);
+    p.part_range = take(r * g * 8);
     p.part_count = take(r * g * 4);
     p.state = take(r * sizeof(RowState));
     p.bytes = at;
@@ -674,21 +1049,19 @@ SamplePlan sample_plan(int64_t rows, int64_t vocab) {
 }
 
 template <class T>
-int sample_launch(const SampleArgs &a, int64_t rows, bool border, hipStream_t s) {
+int sample_launch(const SampleArgs &a, int64_t rows, bool searched, hipStream_t s) {
     const unsigned r = static_cast<unsigned>(rows);
     const dim3 parts(static_cast<unsigned>(a.parts), r);
     hipLaunchKernelGGL((sample_max_kernel<T>), parts, dim3(kPartBlock), 0, s, a);
     SSC_TRY(launched());
-    if (border) {
+    if (searched) {
         hipLaunchKernelGGL((sample_hist_kernel<T>), dim3((a.vocab + kHistPart - 1) / kHistPart, r), dim3(kHistBlock),
                            0, s, a);
-        SSC_TRY(launched());
-        hipLaunchKernelGGL((sample_border_kernel<T>), dim3(r), dim3(kBorderBlock), 0, s, a);
         SSC_TRY(launched());
     }
     hipLaunchKernelGGL((sample_sum_kernel<T>), parts, dim3(kPartBlock), 0, s, a);
     SSC_TRY(launched());
-    hipLaunchKernelGGL((sample_token_kernel<T>), dim3(r), dim3(kPartBlock), 0, s, a);
+    hipLaunchKernelGGL((sample_token_kernel<T>), dim3(r), dim3(kTokenBlock), 0, s, a);
     return launched();
 }
 
@@ -729,8 +1102,6 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
             if (overlap(w.p, w.bytes, r.p, r.bytes)) return SSC_ERR_ALIAS;
     SSC_TRY(check_device());
     if (rows == 0) return SSC_OK;
-    // temperatures may be 0, which keeps one token
-    const bool border = temperature != nullptr || top_k != nullptr || top_p != nullptr;
     SampleArgs a{};
     a.logits = logits;
     a.stride = stride;
@@ -748,19 +1119,22 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
     a.kept = kept;
     a.logprobs = logprobs;
     char *base = static_cast<char *>(scratch);
-    a.part_max = reinterpret_cast<uint32_t *>(base + p.part_max);
+    a.part_range = reinterpret_cast<float2 *>(base + p.part_range);
     a.part_mass = reinterpret_cast<uint64_t *>(base + p.part_mass);
     a.part_count = reinterpret_cast<uint32_t *>(base + p.part_count);
     a.state = reinterpret_cast<RowState *>(base + p.state);
-    if (border) {
+    a.list = reinterpret_cast<uint64_t *>(base + p.list);
+    // a histogram only where a row may ask for one
+    const bool searched = top_k != nullptr || top_p != nullptr;
+    if (searched) {
         a.hist_mass = reinterpret_cast<uint64_t *>(base + p.hist_mass);
         a.hist_count = reinterpret_cast<uint32_t *>(base + p.hist_count);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (dtype) {
-    case SSC_F32: return sample_launch<float>(a, rows, border, s);
-    case SSC_BF16: return sample_launch<__bf16>(a, rows, border, s);
-    default: return sample_launch<_Float16>(a, rows, border, s);
+    case SSC_F32: return sample_launch<float>(a, rows, searched, s);
+    case SSC_BF16: return sample_launch<__bf16>(a, rows, searched, s);
+    default: return sample_launch<_Float16>(a, rows, searched, s);
     }
 }
 
