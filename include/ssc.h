@@ -474,8 +474,8 @@ size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
  * and always the first of the order. tokens[r] is the first index, in index
  * order, at which the running sum of the kept weights exceeds u[r] times their
  * sum. A temperature that is not above 0 keeps the first of the order alone.
- * A logit of NaN or -infinity is no token; +infinity shares the row's
- * weight evenly among the logits of +infinity. A row with no token gives
+ * A logit of NaN or -infinity is no token, and beside one of +infinity no
+ * other is (those of +infinity weigh the same). A row with no token gives
  * tokens[r] = -1, kept[r] = 0, logprobs[r] = -infinity. A u outside [0, 1) is
  * taken as the nearest end (NaN as 0), a top_p of NaN as 1, of 0 or less as one
  * that keeps the first only, a min_p of NaN as 0.

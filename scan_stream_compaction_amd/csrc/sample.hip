@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ssc.h"
 #include "ssc_device.h"
 #include "ssc_host.h"
@@ -33,7 +35,7 @@ constexpr int kPartLg = 12;
 constexpr int kPart = 1 << kPartLg;   // logits of a part
 constexpr int kPartBlock = 256;
 constexpr int kPartItems = kPart / kPartBlock;
-constexpr int kHistPart = 8192;       // logits a workgroup adds to its row's histogram
+constexpr int kHistPart = 8192;       // fewest logits of a workgroup of a row's histogram
 constexpr int kHistBlock = 512;
 constexpr int kBins = 2048;
 constexpr int kTokenBlock = 1024;
@@ -59,6 +61,7 @@ struct SampleArgs {
     const void *logits;
     int64_t stride;
     int vocab, parts, bits;  // bits: fractional bits of a weight
+    int splits;              // workgroups of a row's histogram
     const float *u, *temperature, *top_p, *min_p;
     const int32_t *top_k;
     int32_t *tokens, *kept;
@@ -108,66 +111,78 @@ struct Filters {
     __device__ __forceinline__ bool small_k() const { return top_k > 1 && top_k <= kListTopK; }
 };
 
-// Weights and bins of a row.
+// s * g + c with the constant in scalar registers: the compiler's own choice
+// for a polynomial, a multiply-add onto a copy of each constant, takes two more
+// instructions a step.
+__device__ __forceinline__ double fma_const(double s, double g, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(s), "v"(g), "s"(c));
+    return d;
+}
+
+// Weights and bins of a row. A row with a logit of +infinity has no other
+// tokens: with `lift`, +infinity is read as 0 and everything else as -infinity.
 struct Scale {
     double max, rate, min_w;  // rate: log2(e) / T; min_w at the weights' scale
     float top, width;         // the maximum; bins per unit of distance from it
     int bits;
-    bool top_inf;
+    bool lift;
 
     __device__ __forceinline__ Scale(const SampleArgs &a, int row, const Filters &f, float2 range) {
-        top = range.x;
-        top_inf = top == __builtin_inff();
-        max = top_inf ? 0.0 : static_cast<double>(top);
+        lift = range.x == __builtin_inff();
+        top = lift ? 0.0f : range.x;
+        max = static_cast<double>(top);
         const double t = f.t > 0.0f ? static_cast<double>(f.t) : 1.0;
         rate = 1.4426950408889634 / t;
         bits = a.bits;
         const float mp = a.min_p != nullptr ? a.min_p[row] : 0.0f;
         min_w = ldexp(mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0), bits);
-        // the bins span the row, or as far down as weights matter (a NaN from
-        // infinities gives way)
-        const float span = fminf(fminf(top - range.y, 64.0f * static_cast<float>(t)), 0x1.fffffep127f);
+        // the bins span the row, or as far down as weights matter
+        const float span = lift ? 0.0f : fminf(fminf(top - range.y, 64.0f * static_cast<float>(t)), 0x1.fffffep127f);
         width = span > 0.0f ? fminf((kBins - 1) / span, 0x1p100f) : 0.0f;
     }
     // A token's logit on the axis of the bins: bin b is [b, b + 1), the last
     // without an end; a larger logit never lies further.
-    __device__ __forceinline__ float place(float x) const {
-        if (top_inf) return x == top ? 0.0f : __builtin_inff();
-        return (top - x) * width;
-    }
+    __device__ __forceinline__ float place(float x) const { return (top - x) * width; }
     __device__ __forceinline__ int bin(float x) const {
         return static_cast<int>(fminf(place(x), static_cast<float>(kBins - 1)));
     }
     // exp((x - max) / T) * 2^bits, by 2^y = 2^round(y) * 2^(y - round(y)), the
-    // second factor by its Taylor series in fp64: terms up to the 11th leave
-    // 7e-15 of it at most, below the integers' own step for weights of
-    // 2^-3 and less of the largest.
+    // second factor by its Taylor series in fp64, ln(2)^k / k!: terms up to
+    // the 11th leave 7e-15 of it at most, below the integers' own step for
+    // weights of 2^-3 and less of the largest. 0 for -infinity and NaN.
     __device__ __forceinline__ double scaled(float x) const {
-        if (top_inf) return x == top ? ldexp(1.0, bits) : 0.0;
-        constexpr double kLn2 = 0.69314718055994530942;
+        constexpr double L1 = 0.69314718055994530942, L2 = L1 * L1, L4 = L2 * L2, L8 = L4 * L4;
         const double y = fmax((static_cast<double>(x) - max) * rate, -1000.0);
         const double n = __builtin_rint(y);
-        const double g = (y - n) * kLn2;
-        double s = 1.0 / 39916800;
-        s = __builtin_fma(s, g, 1.0 / 3628800);
-        s = __builtin_fma(s, g, 1.0 / 362880);
-        s = __builtin_fma(s, g, 1.0 / 40320);
-        s = __builtin_fma(s, g, 1.0 / 5040);
-        s = __builtin_fma(s, g, 1.0 / 720);
-        s = __builtin_fma(s, g, 1.0 / 120);
-        s = __builtin_fma(s, g, 1.0 / 24);
-        s = __builtin_fma(s, g, 1.0 / 6);
-        s = __builtin_fma(s, g, 0.5);
-        s = __builtin_fma(s, g, 1.0);
-        s = __builtin_fma(s, g, 1.0);
+        const double r = y - n;
+        double s = fma_const(r, L8 * L2 * L1 / 39916800, L8 * L2 / 3628800);
+        s = fma_const(s, r, L8 * L1 / 362880);
+        s = fma_const(s, r, L8 / 40320);
+        s = fma_const(s, r, L4 * L2 * L1 / 5040);
+        s = fma_const(s, r, L4 * L2 / 720);
+        s = fma_const(s, r, L4 * L1 / 120);
+        s = fma_const(s, r, L4 / 24);
+        s = fma_const(s, r, L2 * L1 / 6);
+        s = fma_const(s, r, L2 / 2);
+        s = fma_const(s, r, L1);
+        s = __builtin_fma(s, r, 1.0);
         return ldexp(s, static_cast<int>(n) + bits);
     }
-    // Rounded to an integer: adding 2^52 leaves it in the low bits.
-    __device__ __forceinline__ static uint64_t fixed(double w) {
-        return static_cast<uint64_t>(__double_as_longlong(w + 0x1p52)) & ((uint64_t{1} << 52) - 1);
+    // Rounded to an integer: adding 2^52 leaves it in the low bits, under the
+    // bits of 2^52 itself. A sum of n such takes those off once.
+    __device__ __forceinline__ static uint64_t raised(double w) {
+        return static_cast<uint64_t>(__double_as_longlong(w + 0x1p52));
     }
+    static constexpr uint64_t kRaise = 0x4330000000000000ull;
+    __device__ __forceinline__ static uint64_t fixed(double w) { return raised(w) - kRaise; }
     __device__ __forceinline__ uint64_t weight(float x) const { return fixed(scaled(x)); }
+    // whether min_p keeps it
+    __device__ __forceinline__ bool large(double w, float x) const { return w >= min_w || x == top; }
 };
+
+// Neither NaN nor -infinity.
+__device__ __forceinline__ bool is_token(float x) { return x >= -0x1.fffffep127f; }
 
 // 16 bytes of logits from any element address.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
@@ -189,6 +204,16 @@ struct Logits {
 #pragma unroll
             for (int e = 0; e < kN; ++e) x[e] = i + e < n ? static_cast<float>(row[i + e]) : -__builtin_inff();
         }
+    }
+    __device__ __forceinline__ void lift(bool lift) {
+        if (lift) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) x[e] = x[e] == __builtin_inff() ? 0.0f : -__builtin_inff();
+        }
+    }
+    __device__ __forceinline__ void load(const T *row, int i, int n, const Scale &sc) {
+        load(row, i, n);
+        lift(sc.lift);
     }
 };
 
@@ -240,32 +265,17 @@ __device__ __forceinline__ float2 row_range(const SampleArgs &a, int row) {
 template <class T>
 __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
     __shared__ float2 s_range[kPartBlock / kWave];
-    const int row = blockIdx.y, part = blockIdx.x;
+    const int row = blockIdx.y;
     const T *x = row_at<T>(a, row);
     using L = Logits<T>;
-    float2 r = {-__builtin_inff(), __builtin_inff()};
-#pragma unroll
-    for (int j = 0; j < kPartItems / L::kN; ++j) {
-        const int i = part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN;
-        if (i >= a.vocab) continue;
-        L v;
-        v.load(x, i, a.vocab);
-#pragma unroll
-        for (int e = 0; e < L::kN; ++e) {
-            r.x = fmaxf(r.x, v.x[e]);  // NaN gives way
-            r.y = fminf(r.y, v.x[e] > -__builtin_inff() ? v.x[e] : __builtin_inff());
-        }
-    }
-    r = wave_range(r);
-    if (lane_id() == 0) s_range[threadIdx.x / kWave] = r;
     const Filters f(a, row);
-    if (a.hist_count != nullptr && f.searched()) {
-        for (int b = part * kPartBlock + static_cast<int>(threadIdx.x); b < kBins; b += a.parts * kPartBlock) {
+    if (a.splits > 1 && f.searched()) {
+        for (int b = static_cast<int>(blockIdx.x * kPartBlock + threadIdx.x); b < kBins; b += gridDim.x * kPartBlock) {
             a.hist_mass[static_cast<int64_t>(row) * kBins + b] = 0;
             a.hist_count[static_cast<int64_t>(row) * kBins + b] = 0;
         }
     }
-    if (part == 0 && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         RowState s{};
         s.extra = -1;
         if (f.top_k == 1) {  // the first of the order is in bin 0
@@ -276,29 +286,47 @@ __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
         }
         a.state[row] = s;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kPartBlock / kWave; ++w) {
-            r.x = fmaxf(r.x, s_range[w].x);
-            r.y = fminf(r.y, s_range[w].y);
+    for (int part = blockIdx.x; part < a.parts; part += gridDim.x) {
+        float2 r = {-__builtin_inff(), __builtin_inff()};
+        L v[kPartItems / L::kN];
+#pragma unroll
+        for (int j = 0; j < kPartItems / L::kN; ++j)
+            v[j].load(x, part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN, a.vocab);
+#pragma unroll
+        for (int j = 0; j < kPartItems / L::kN; ++j) {
+#pragma unroll
+            for (int e = 0; e < L::kN; ++e) {
+                // NaN gives way in both; x * 0 is one for the infinities
+                r.x = fmaxf(r.x, v[j].x[e]);
+                r.y = fminf(r.y, __builtin_fmaf(v[j].x[e], 0.0f, v[j].x[e]));
+            }
         }
-        a.part_range[static_cast<int64_t>(row) * a.parts + part] = r;
+        r = wave_range(r);
+        __syncthreads();
+        if (lane_id() == 0) s_range[threadIdx.x / kWave] = r;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kPartBlock / kWave; ++w) {
+                r.x = fmaxf(r.x, s_range[w].x);
+                r.y = fminf(r.y, s_range[w].y);
+            }
+            a.part_range[static_cast<int64_t>(row) * a.parts + part] = r;
+        }
     }
 }
 
 // ---- counts and weights by bin, and the border bins ----
 struct Hist {
-    unsigned long long mass[kBins];
-    uint32_t count[kBins];
+    unsigned long long mass[kBins + 1];  // the last for what is no token
+    uint32_t count[kBins + 1];
 };
 
 __device__ __forceinline__ void hist_count(Hist &h, int bin) {
     __hip_atomic_fetch_add(&h.count[bin], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 __device__ __forceinline__ void hist_mass(Hist &h, int bin, uint64_t w) {
-    if (w != 0)
-        __hip_atomic_fetch_add(&h.mass[bin], static_cast<unsigned long long>(w), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_WORKGROUP);
+    __hip_atomic_fetch_add(&h.mass[bin], static_cast<unsigned long long>(w), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
 // Where a running sum over the bins reaches a goal.
@@ -379,49 +407,65 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     __syncthreads();
     const T *x = row_at<T>(a, row);
     using L = Logits<T>;
-    const int begin = blockIdx.x * kHistPart;
     const bool counts = f.top_k > 0, masses = f.nucleus() && !f.small_k();
+    const auto each = [&](auto counted, auto weighed) {
+        constexpr int kStep = kHistBlock * L::kN, kDeep = 2;
+        for (int i0 = (blockIdx.x * kHistBlock + static_cast<int>(threadIdx.x)) * L::kN; i0 < a.vocab;
+             i0 += kDeep * a.splits * kStep) {
+            L v[kDeep];
 #pragma unroll
-    for (int j = 0; j < kHistPart / (kHistBlock * L::kN); ++j) {
-        const int i = begin + (j * kHistBlock + static_cast<int>(threadIdx.x)) * L::kN;
-        if (i >= a.vocab) continue;
-        L v;
-        v.load(x, i, a.vocab);
+            for (int j = 0; j < kDeep; ++j) v[j].load(x, i0 + j * a.splits * kStep, a.vocab, sc);
 #pragma unroll
-        for (int e = 0; e < L::kN; ++e) {
-            if (!(v.x[e] > -__builtin_inff())) continue;
-            const int b = sc.bin(v.x[e]);
-            if (counts) hist_count(h, b);
-            if (masses) hist_mass(h, b, sc.weight(v.x[e]));
+            for (int j = 0; j < kDeep; ++j) {
+#pragma unroll
+                for (int e = 0; e < L::kN; ++e) {
+                    const float xe = v[j].x[e];
+                    const int b = is_token(xe) ? sc.bin(xe) : kBins;
+                    if (decltype(counted)::value) hist_count(h, b);
+                    if (decltype(weighed)::value) hist_mass(h, b, sc.weight(xe));
+                }
+            }
         }
+    };
+    if (counts && masses)
+        each(std::true_type{}, std::true_type{});
+    else if (counts)
+        each(std::true_type{}, std::false_type{});
+    else
+        each(std::false_type{}, std::true_type{});
+    __syncthreads();
+    if (a.splits > 1) {
+        unsigned long long *gm =
+            reinterpret_cast<unsigned long long *>(a.hist_mass) + static_cast<int64_t>(row) * kBins;
+        uint32_t *gc = a.hist_count + static_cast<int64_t>(row) * kBins;
+        for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
+            if (h.count[b] != 0)
+                __hip_atomic_fetch_add(gc + b, h.count[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (h.mass[b] != 0)
+                __hip_atomic_fetch_add(gm + b, h.mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        // The workgroup that adds last finds the border bins. Everything it
+        // reads was written by agent-scope atomics, which take effect beyond
+        // the XCDs' own L2 caches: once each wavefront has waited for its own
+        // to be acknowledged, agent-scope loads see them, and no cache has to
+        // be written back (with release fences instead, 256 rows of 131,072
+        // logits in 16 workgroups each took 641 us against 47).
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0)
+            s_last = __hip_atomic_fetch_add(&a.state[row].done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                     gridDim.x - 1;
+        __syncthreads();
+        if (!s_last) return;
+        for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
+            h.count[b] = __hip_atomic_load(gc + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            h.mass[b] = __hip_atomic_load(gm + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    unsigned long long *gm = reinterpret_cast<unsigned long long *>(a.hist_mass) + static_cast<int64_t>(row) * kBins;
-    uint32_t *gc = a.hist_count + static_cast<int64_t>(row) * kBins;
-    for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
-        if (h.count[b] != 0)
-            __hip_atomic_fetch_add(gc + b, h.count[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (h.mass[b] != 0)
-            __hip_atomic_fetch_add(gm + b, h.mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    // The workgroup that adds last finds the border bins. Everything it reads
-    // was written by agent-scope atomics, which take effect beyond the XCDs'
-    // own L2 caches: once each wavefront has waited for its own to be
-    // acknowledged, agent-scope loads see them, and no cache has to be written
-    // back (with release fences instead, this kernel took 641 us for 256 rows
-    // of 131,072).
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0)
-        s_last = __hip_atomic_fetch_add(&a.state[row].done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                 gridDim.x - 1;
-    __syncthreads();
-    if (!s_last) return;
     uint32_t n = 0;
     uint64_t total = 0;
     for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
-        h.count[b] = __hip_atomic_load(gc + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        h.mass[b] = __hip_atomic_load(gm + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         n += h.count[b];
         total += h.mass[b];
     }
@@ -497,99 +541,111 @@ template <class T>
 __global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
     constexpr int kWaves = kPartBlock / kWave;
     __shared__ float s_x[kWaves][kPart / kWaves];
+    __shared__ uint16_t s_i[kWaves][kPart / kWaves];
     __shared__ unsigned long long s_mass[kWaves];
     __shared__ uint32_t s_count[kWaves];
-    const int row = blockIdx.y, part = blockIdx.x;
+    const int row = blockIdx.y;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const T *x = row_at<T>(a, row);
     using L = Logits<T>;
     constexpr int kEach = kPartItems / L::kN;
-    L v[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j)
-        v[j].load(x, part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN, a.vocab);
     const Filters f(a, row);
     const Scale sc(a, row, f, row_range(a, row));
     RowState *st = a.state + row;
     const int lo = st->lo, hi = st->hi, extra = st->extra;
-    uint64_t mass = 0;
-    uint32_t count = 0;
-    const auto add = [&](float xe) {
-        const double we = sc.scaled(xe);
-        if (we >= sc.min_w || xe == sc.top) {
-            mass += Scale::fixed(we);
-            ++count;
-        }
-    };
-    if (lo >= kBins) {
+    // No logit below `least` is kept or collected: those that are lie above
+    // top - (deepest + 1) / width but for some roundings, which the added 2
+    // covers; rounding the difference to fp32 keeps its order among logits.
+    const int deepest = extra > hi ? extra : hi;
+    constexpr float kLowest = -0x1.fffffep127f;
+    const float least = lo >= kBins || deepest >= kBins - 1 || sc.width == 0.0f
+                            ? kLowest
+                            : fmaxf(sc.top - (static_cast<float>(deepest) + 2.0f) / sc.width, kLowest);
+    for (int part = blockIdx.x; part < a.parts; part += gridDim.x) {
+        L v[kEach];
+        const int first = part * kPart + static_cast<int>(threadIdx.x) * L::kN;
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-#pragma unroll
-            for (int e = 0; e < L::kN; ++e)
-                if (v[j].x[e] > -__builtin_inff()) add(v[j].x[e]);
-        }
-    } else {
-        // places in [0, kept) are kept, those in [kept, end) and [far, far_end)
-        // collected; the last bin's end is a NaN, which nothing reaches
-        const float kept = static_cast<float>(lo);
-        const float end = hi >= kBins - 1 ? __builtin_nanf("") : static_cast<float>(hi + 1);
-        const float far = extra < 0 ? __builtin_nanf("") : static_cast<float>(extra);
-        const float far_end = extra >= kBins - 1 ? __builtin_nanf("") : far + 1.0f;
-        uint32_t packed = 0, listed = 0;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-#pragma unroll
-            for (int e = 0; e < L::kN; ++e) {
-                const float xe = v[j].x[e];
-                const bool token = xe > -__builtin_inff();
-                const float pl = sc.place(xe);
-                if (lo > 0) {  // packed first, so that the exponentials run on full wavefronts
-                    const bool keep = token && pl < kept;
-                    const uint64_t mask = ballot(keep);
-                    if (keep) s_x[w][packed + mbcnt64(mask)] = xe;
-                    packed += static_cast<uint32_t>(__builtin_popcountll(mask));
-                }
-                const bool list = token && ((pl >= kept && !(pl >= end)) || (pl >= far && !(pl >= far_end)));
-                listed |= list ? 1u << (j * L::kN + e) : 0u;
-            }
-        }
-        if (ballot(listed != 0) != 0) {
-            const uint32_t mine = static_cast<uint32_t>(__builtin_popcount(listed));
-            const uint32_t incl = wave_inclusive_scan<SumU32>(mine);
-            uint32_t at = 0;
-            if (lane == kWave - 1)
-                at = __hip_atomic_fetch_add(&st->listed, incl, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            at = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(at), kWave - 1)) + incl - mine;
-            uint64_t *list = a.list + static_cast<int64_t>(row) * kList;
+        for (int j = 0; j < kEach; ++j) v[j].load(x, first + j * kPartBlock * L::kN, a.vocab, sc);
+        uint64_t mass = 0;
+        uint32_t count = 0;  // of the wavefront
+        if (lo >= kBins) {
 #pragma unroll
             for (int j = 0; j < kEach; ++j) {
-                const int i = part * kPart + (j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN;
 #pragma unroll
                 for (int e = 0; e < L::kN; ++e) {
-                    if ((listed >> (j * L::kN + e)) & 1u) {
-                        if (at < kList) list[at] = entry_of(key_of(v[j].x[e]), i + e);
-                        ++at;
+                    const float xe = v[j].x[e];
+                    const double we = sc.scaled(xe);
+                    const uint64_t keep = ballot(sc.large(we, xe)) & ballot(is_token(xe));
+                    count += static_cast<uint32_t>(__builtin_popcountll(keep));
+                    mass += (keep >> lane) & 1 ? Scale::fixed(we) : 0;
+                }
+            }
+        } else {
+            // what may be kept or collected is packed first, so that the rest
+            // of the work runs on full wavefronts
+            uint32_t packed = 0;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+#pragma unroll
+                for (int e = 0; e < L::kN; ++e) {
+                    const float xe = v[j].x[e];
+                    const bool near = xe >= least;
+                    const uint64_t mask = ballot(near);
+                    if (mask == 0) continue;
+                    if (near) {
+                        const uint32_t at = packed + mbcnt64(mask);
+                        s_x[w][at] = xe;
+                        s_i[w][at] = static_cast<uint16_t>((j * kPartBlock + static_cast<int>(threadIdx.x)) * L::kN + e);
                     }
+                    packed += static_cast<uint32_t>(__builtin_popcountll(mask));
+                }
+            }
+            // places in [0, kept) are kept, those in [kept, end) and [far, far_end)
+            // collected; the last bin's end is a NaN, which nothing reaches
+            const float kept = static_cast<float>(lo);
+            const float end = hi >= kBins - 1 ? __builtin_nanf("") : static_cast<float>(hi + 1);
+            const float far = extra < 0 ? __builtin_nanf("") : static_cast<float>(extra);
+            const float far_end = extra >= kBins - 1 ? __builtin_nanf("") : far + 1.0f;
+            for (uint32_t i0 = 0; i0 < packed; i0 += kWave) {
+                const uint32_t i = i0 + lane;
+                const bool here = i < packed;
+                const float xe = here ? s_x[w][i] : -__builtin_inff();
+                const float pl = sc.place(xe);
+                if (lo > 0) {
+                    const double we = sc.scaled(xe);
+                    const bool keep = here && pl < kept && sc.large(we, xe);
+                    mass += keep ? Scale::fixed(we) : 0;
+                    count += static_cast<uint32_t>(__builtin_popcountll(ballot(keep)));
+                }
+                const bool list = here && ((pl >= kept && !(pl >= end)) || (pl >= far && !(pl >= far_end)));
+                const uint64_t mask = ballot(list);
+                if (mask != 0) {
+                    uint32_t at = 0;
+                    if (lane == 0)
+                        at = __hip_atomic_fetch_add(&st->listed, static_cast<uint32_t>(__builtin_popcountll(mask)),
+                                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    at = uniform(at) + mbcnt64(mask);
+                    if (list && at < kList)
+                        a.list[static_cast<int64_t>(row) * kList + at] = entry_of(key_of(xe), part * kPart + s_i[w][i]);
                 }
             }
         }
-        for (uint32_t i = lane; i < packed; i += kWave) add(s_x[w][i]);
-    }
-    mass = wave_sum64(mass);
-    count = wave_sum32(count);
-    if (lane == 0) {
-        s_mass[w] = mass;
-        s_count[w] = count;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kWaves; ++i) {
-            mass += s_mass[i];
-            count += s_count[i];
+        mass = wave_sum64(mass);
+        __syncthreads();
+        if (lane == 0) {
+            s_mass[w] = mass;
+            s_count[w] = count;
         }
-        a.part_mass[static_cast<int64_t>(row) * a.parts + part] = mass;
-        a.part_count[static_cast<int64_t>(row) * a.parts + part] = count;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kWaves; ++i) {
+                mass += s_mass[i];
+                count += s_count[i];
+            }
+            a.part_mass[static_cast<int64_t>(row) * a.parts + part] = mass;
+            a.part_count[static_cast<int64_t>(row) * a.parts + part] = count;
+        }
     }
 }
 
@@ -623,7 +679,7 @@ __device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Sc
     using L = Logits<T>;
     for (int i = static_cast<int>(threadIdx.x) * L::kN; i < a.vocab; i += kTokenBlock * L::kN) {
         L v;
-        v.load(x, i, a.vocab);
+        v.load(x, i, a.vocab, sc);
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) {
             const uint32_t k = key_of(v.x[e]);
@@ -662,8 +718,8 @@ __device__ __forceinline__ Found border_key(const SampleArgs &a, const T *x, con
 
 // The index of the `need`-th logit, in index order, with this key.
 template <class T>
-__device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, TokenShared &sh, uint32_t key,
-                                              uint32_t need) {
+__device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, const Scale &sc, TokenShared &sh,
+                                              uint32_t key, uint32_t need) {
     using L = Logits<T>;
     constexpr int kWaves = kTokenBlock / kWave;
     constexpr int kStep = kWave * L::kN;
@@ -675,7 +731,7 @@ __device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, T
     uint32_t count = 0;
     for (int s = first; s < last; ++s) {
         L v;
-        v.load(x, s * kStep + lane * L::kN, a.vocab);
+        v.load(x, s * kStep + lane * L::kN, a.vocab, sc);
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) count += key_of(v.x[e]) == key ? 1u : 0u;
     }
@@ -689,7 +745,7 @@ __device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, T
         for (int s = first; s < last; ++s) {
             const int i = s * kStep + lane * L::kN;
             L v;
-            v.load(x, i, a.vocab);
+            v.load(x, i, a.vocab, sc);
             uint32_t mine = 0;
 #pragma unroll
             for (int e = 0; e < L::kN; ++e) mine += key_of(v.x[e]) == key ? 1u : 0u;
@@ -719,7 +775,7 @@ struct Border {
         kept = false;
         if (k == 0 || k < key || (k == key && static_cast<uint32_t>(i) > cut)) return 0;
         const double w = sc.scaled(x);
-        kept = w >= sc.min_w || x == sc.top;
+        kept = sc.large(w, x);
         return kept ? Scale::fixed(w) : 0;
     }
 };
@@ -732,7 +788,7 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
     double all = -1.0;  // weight that top_k leaves
     if (f.top_k == 1) {
         out.key = key_of(sc.top);
-        out.cut = tie_index(a, x, sh, out.key, 1);
+        out.cut = tie_index(a, x, sc, sh, out.key, 1);
         return out;
     }
     if (f.top_k > 0) {
@@ -777,11 +833,13 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
             }
         }
     }
-    if (ties < have) out.cut = tie_index(a, x, sh, out.key, ties);
+    if (ties < have) out.cut = tie_index(a, x, sc, sh, out.key, ties);
     return out;
 }
 
-// Sorts the first n entries (n2 a power of two, filled up with 0) from the largest down.
+// Sorts n2 entries (a power of two) from the largest down: bitonic merges. A
+// wavefront's 64 pairs lie in 128 entries of its own while they are at most 64
+// apart, so only the longer distances need the workgroup's barriers.
 __device__ __forceinline__ void sort_list(unsigned long long *e, int n2) {
     for (int size = 2; size <= n2; size <<= 1) {
         for (int dist = size >> 1; dist > 0; dist >>= 1) {
@@ -793,7 +851,14 @@ __device__ __forceinline__ void sort_list(unsigned long long *e, int n2) {
                     e[j] = u;
                 }
             }
-            __syncthreads();
+            // the next distance, or the next size's first
+            const int next = dist > 1 ? dist >> 1 : size;
+            if (dist > kWave || next > kWave || (dist == 1 && size == n2)) {
+                __syncthreads();
+            } else {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
         }
     }
 }
@@ -834,7 +899,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             uint64_t mass = 0;
             for (int i = p * kPart + lane * L::kN; i < a.vocab && i < (p + 1) * kPart; i += kWave * L::kN) {
                 L v;
-                v.load(x, i, a.vocab);
+                v.load(x, i, a.vocab, sc);
 #pragma unroll
                 for (int e = 0; e < L::kN; ++e) {
                     bool kept;
@@ -922,7 +987,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             const uint32_t i = threadIdx.x * kEach + q;
             if (i < nk && static_cast<double>(st.mass + run) < target) {
                 keep = i + 1;
-                if (full[q] >= sc.min_w || sh.list.entry[i] >> 32 == key_of(sc.top)) {
+                if (sc.large(full[q], value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32)))) {
                     const uint32_t index = ~static_cast<uint32_t>(sh.list.entry[i]);
                     __hip_atomic_fetch_add(&sh.mass[index >> kPartLg], static_cast<unsigned long long>(we[q]),
                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
@@ -989,6 +1054,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
     for (int e = 0; e < kEach; ++e) {
         bool kept;
         v[e] = first + e < a.vocab ? static_cast<float>(x[first + e]) : -__builtin_inff();
+        if (sc.lift) v[e] = v[e] == __builtin_inff() ? 0.0f : -__builtin_inff();
         we[e] = border.weight(sc, v[e], first + e, kept);
         ms += we[e];
     }
@@ -1010,7 +1076,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         }
         a.tokens[row] = at;
         if (a.logprobs != nullptr) {
-            const double z = sc.top_inf ? 0.0 : (static_cast<double>(chosen) - sc.max) * (sc.rate / 1.4426950408889634);
+            const double z = (static_cast<double>(chosen) - sc.max) * (sc.rate / 1.4426950408889634);
             a.logprobs[row] = static_cast<float>(z - log(ldexp(static_cast<double>(sh.total), -sc.bits)));
         }
     }
@@ -1051,12 +1117,13 @@ SamplePlan sample_plan(int64_t rows, int64_t vocab) {
 template <class T>
 int sample_launch(const SampleArgs &a, int64_t rows, bool searched, hipStream_t s) {
     const unsigned r = static_cast<unsigned>(rows);
-    const dim3 parts(static_cast<unsigned>(a.parts), r);
+    // up to 4096 workgroups, each with several parts of a row where there are more
+    const int64_t each = (static_cast<int64_t>(a.parts) * rows + 4095) / 4096;
+    const dim3 parts(static_cast<unsigned>((a.parts + each - 1) / each), r);
     hipLaunchKernelGGL((sample_max_kernel<T>), parts, dim3(kPartBlock), 0, s, a);
     SSC_TRY(launched());
     if (searched) {
-        hipLaunchKernelGGL((sample_hist_kernel<T>), dim3((a.vocab + kHistPart - 1) / kHistPart, r), dim3(kHistBlock),
-                           0, s, a);
+        hipLaunchKernelGGL((sample_hist_kernel<T>), dim3(a.splits, r), dim3(kHistBlock), 0, s, a);
         SSC_TRY(launched());
     }
     hipLaunchKernelGGL((sample_sum_kernel<T>), parts, dim3(kPartBlock), 0, s, a);
@@ -1124,9 +1191,14 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
     a.part_count = reinterpret_cast<uint32_t *>(base + p.part_count);
     a.state = reinterpret_cast<RowState *>(base + p.state);
     a.list = reinterpret_cast<uint64_t *>(base + p.list);
-    // a histogram only where a row may ask for one
+    // A histogram only where a row may ask for one, its rows split until
+    // there are eight workgroups to a compute unit: rows differ in work (256
+    // rows of 131,072: 2, 4, 8, 16 workgroups a row 62, 39, 33, 43 us).
     const bool searched = top_k != nullptr || top_p != nullptr;
+    a.splits = 1;
     if (searched) {
+        const int64_t most = (vocab + kHistPart - 1) / kHistPart;
+        while (a.splits < most && a.splits * rows < 2048) ++a.splits;
         a.hist_mass = reinterpret_cast<uint64_t *>(base + p.hist_mass);
         a.hist_count = reinterpret_cast<uint32_t *>(base + p.hist_count);
     }

@@ -8,6 +8,8 @@ import numpy as np
 def sample_row(x, u, t=1.0, k=0, p=1.0, m=0.0):
     """(token, kept, logprob) of one row of logits (float64 values)."""
     x = np.where(np.isnan(x), -np.inf, x)
+    if np.any(x == np.inf):  # no token beside +infinity
+        x = np.where(x == np.inf, 0.0, -np.inf)
     order = np.argsort(-x, kind="stable")
     order = order[x[order] > -np.inf]
     if order.size == 0:
@@ -16,10 +18,7 @@ def sample_row(x, u, t=1.0, k=0, p=1.0, m=0.0):
     p = 1.0 if np.isnan(p) else p
     m = 0.0 if np.isnan(m) else min(max(m, 0.0), 1.0)
     top = x[order[0]]
-    if np.isinf(top):
-        w = (x[order] == np.inf).astype(np.float64)
-    else:
-        w = np.exp((x[order] - top) / (1.0 if greedy else t))
+    w = np.exp((x[order] - top) / (1.0 if greedy else t))
     n = order.size
     if greedy:
         n = 1
