@@ -391,7 +391,7 @@ typedef enum ssc_dtype {
  *     depends on the sizes and the ranks only, so a call repeats bit for bit.
  */
 
-/* Scratch bytes of a grouping of n keys (0 for up to 4096 keys of at most 511
+/* Scratch bytes of a grouping of n keys (0 for up to 8192 keys of at most 511
  * groups). */
 size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
 
@@ -404,7 +404,7 @@ size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
  *   order[s]   = the i with ranks[i] = s, for s < offsets[groups]; the
  *                entries past that are not written               (nullable)
  * The many-way form of ssc_partition_i32: one counting and one scattering
- * step per 9 bits of group number (a single launch for up to 4096 keys of at
+ * step per 9 bits of group number (a single launch for up to 8192 keys of at
  * most 511 groups). */
 int ssc_group_by_key_i32(const int32_t *keys, int64_t n, int64_t groups, int32_t *order,
                          int32_t *ranks, int32_t *offsets, void *scratch, size_t scratch_bytes,

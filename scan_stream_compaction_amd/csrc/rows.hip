@@ -39,7 +39,7 @@ constexpr int kGroupBlock = 1024;
 constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kGroupSmall = 4 * kGroupBlock;    // keys one workgroup sorts alone
+constexpr int kGroupSmall = 8 * kGroupBlock;    // keys one workgroup sorts alone
 constexpr int kGroupTiles = 256;                // most workgroups of a tiled pass
 
 template <class K>
@@ -47,22 +47,43 @@ __device__ __forceinline__ uint32_t key_of(K k, uint32_t groups) {
     return k >= 0 && static_cast<uint64_t>(k) < groups ? static_cast<uint32_t>(k) : groups;
 }
 
-// Rank of each lane's digit among the keys this wavefront has seen, in
-// order; cnt holds the wavefront's counts.
-__device__ __forceinline__ uint32_t digit_rank(uint32_t d, bool valid, int bits, uint32_t *cnt) {
-    uint64_t m = ballot(valid);
-    for (int b = 0; b < bits; ++b) {
-        const uint64_t bb = ballot(valid && ((d >> b) & 1u));
-        m &= ((d >> b) & 1u) ? bb : ~bb;
+// Ranks of `items` (at most ITEMS) consecutive sets of 64 keys among the keys this wavefront has
+// seen, in order; cnt holds the wavefront's counts. The lanes' masks do not
+// depend on one another and come first; the counts then follow key order.
+template <int ITEMS>
+__device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bool (&valid)[ITEMS], int items,
+                                            int bits, uint32_t *cnt, uint32_t (&rk)[ITEMS]) {
+    uint32_t lo[ITEMS], hi[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint64_t all = ballot(valid[j]);
+        lo[j] = static_cast<uint32_t>(all);
+        hi[j] = static_cast<uint32_t>(all >> 32);
     }
-    const uint32_t below = mbcnt64(m);
-    const uint32_t same = static_cast<uint32_t>(__builtin_popcountll(m));
-    uint32_t run = 0;
-    if (valid) {
-        run = cnt[d];
-        if (below + 1u == same) cnt[d] = run + same;
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+        if (b >= bits) continue;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            if (j >= items) continue;
+            const uint32_t bit = static_cast<uint32_t>(static_cast<int32_t>(d[j] << (31 - b)) >> 31);  // 0 or all ones
+            const uint64_t bb = ballot(bit != 0);
+            lo[j] &= ~(static_cast<uint32_t>(bb) ^ bit);
+            hi[j] &= ~(static_cast<uint32_t>(bb >> 32) ^ bit);
+        }
     }
-    return run + below;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        if (j >= items) continue;
+        const uint32_t below = __builtin_amdgcn_mbcnt_hi(hi[j], __builtin_amdgcn_mbcnt_lo(lo[j], 0u));
+        const uint32_t same = static_cast<uint32_t>(__builtin_popcount(lo[j]) + __builtin_popcount(hi[j]));
+        uint32_t run = 0;
+        if (valid[j]) {
+            run = cnt[d[j]];
+            if (below + 1u == same) cnt[d[j]] = run + same;
+        }
+        rk[j] = run + below;
+    }
 }
 
 // Exclusive prefix of v over the workgroup's threads.
@@ -72,9 +93,9 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *s_wave
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     if (lane == kWave - 1) s_wave[w] = incl;
     __syncthreads();
-    uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += s_wave[i];
-    __syncthreads();
+    const uint32_t totals = wave_inclusive_scan<SumU32>(lane < kGroupWaves ? s_wave[lane] : 0u);
+    const uint32_t before =
+        w == 0 ? 0u : static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(totals), w - 1));
     return before + incl - v;
 }
 
@@ -83,17 +104,19 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *s_wave
 __device__ __forceinline__ uint32_t counts_before(uint32_t (*cnt)[kDigits], uint32_t digits) {
     uint32_t total = 0;
     if (threadIdx.x < digits) {
+        uint32_t c[kGroupWaves];
+#pragma unroll
+        for (int w = 0; w < kGroupWaves; ++w) c[w] = cnt[w][threadIdx.x];
 #pragma unroll
         for (int w = 0; w < kGroupWaves; ++w) {
-            const uint32_t c = cnt[w][threadIdx.x];
             cnt[w][threadIdx.x] = total;
-            total += c;
+            total += c[w];
         }
     }
     return total;
 }
 
-// Up to 4096 keys: one workgroup holds (key, position) in registers and
+// Up to 8192 keys: one workgroup holds (key, position) in registers and
 // exchanges them through LDS between passes.
 template <class K, int ITEMS>
 __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
@@ -108,53 +131,76 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t digits = 1u << bits;
-    const uint32_t first = static_cast<uint32_t>(w) * kWave * ITEMS + lane;
+    // as few keys to a wavefront as all sixteen leave it
+    const int items = static_cast<int>((n + kGroupBlock - 1) / kGroupBlock);
+    const uint32_t first = static_cast<uint32_t>(w * kWave * items + lane);
     uint32_t key[ITEMS], pos[ITEMS], rk[ITEMS];
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         const uint32_t i = first + j * kWave;
         pos[j] = i;
-        key[j] = i < n ? key_of(keys[i], groups) : 0u;
+        key[j] = j < items && i < n ? key_of(keys[i], groups) : 0u;
     }
     for (int p = 0; p < passes; ++p) {
         const int shift = p * bits;
         for (uint32_t d = threadIdx.x; d < digits * kGroupWaves; d += kGroupBlock)
             s_cnt[d >> bits][d & (digits - 1)] = 0;
         __syncthreads();
+        uint32_t dig[ITEMS];
+        bool valid[ITEMS];
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j)
-            rk[j] = digit_rank((key[j] >> shift) & (digits - 1), first + j * kWave < n, bits, s_cnt[w]);
+        for (int j = 0; j < ITEMS; ++j) {
+            dig[j] = (key[j] >> shift) & (digits - 1);
+            valid[j] = j < items && first + j * kWave < n;
+        }
+        digit_ranks<ITEMS>(dig, valid, items, bits, s_cnt[w], rk);
         __syncthreads();
         const uint32_t total = counts_before(s_cnt, digits);
         const uint32_t start = block_exclusive(total, s_wave);
         if (threadIdx.x < digits) s_start[threadIdx.x] = start;
         __syncthreads();
-        const bool last = p == passes - 1;
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            if (first + j * kWave >= n) continue;
-            const uint32_t d = (key[j] >> shift) & (digits - 1);
-            const uint32_t at = s_start[d] + s_cnt[w][d] + rk[j];
-            if (!last) {
-                s_key[at] = key[j];
-                s_pos[at] = static_cast<uint16_t>(pos[j]);
-            } else {
-                if (passes > 1) sorted_out[at] = key[j];
-                const bool kept = key[j] < groups;
-                if (order != nullptr && kept) order[at] = static_cast<int32_t>(pos[j]);
-                if (ranks != nullptr) ranks[pos[j]] = kept ? static_cast<int32_t>(at) : -1;
-            }
+            if (!valid[j]) continue;
+            const uint32_t at = s_start[dig[j]] + s_cnt[w][dig[j]] + rk[j];
+            s_key[at] = key[j];
+            s_pos[at] = static_cast<uint16_t>(pos[j]);
         }
         __syncthreads();
-        if (!last) {
+        if (p < passes - 1) {
 #pragma unroll
             for (int j = 0; j < ITEMS; ++j) {
                 const uint32_t i = first + j * kWave;
-                if (i < n) {
+                if (valid[j]) {
                     key[j] = s_key[i];
                     pos[j] = s_pos[i];
                 }
             }
+        }
+    }
+    // the outputs leave from LDS in order
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = threadIdx.x + j * kGroupBlock;
+        if (i < n) {
+            key[j] = s_key[i];
+            pos[j] = s_pos[i];
+            if (passes > 1) sorted_out[i] = key[j];
+            if (order != nullptr && key[j] < groups) order[i] = static_cast<int32_t>(pos[j]);
+        }
+    }
+    if (ranks != nullptr) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t i = threadIdx.x + j * kGroupBlock;
+            if (i < n) s_key[pos[j]] = key[j] < groups ? i : ~0u;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t i = threadIdx.x + j * kGroupBlock;
+            if (i < n) ranks[i] = static_cast<int32_t>(s_key[i]);
         }
     }
     // the digit starts of a single pass are the offsets
@@ -206,7 +252,7 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
     {
         const uint32_t d = (4 * threadIdx.x) & (digits - 1), parts = (4 * kGroupBlock) >> bits;
         u32x4 before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
-#pragma unroll 16
+#pragma unroll 8
         for (uint32_t t = (4 * threadIdx.x) >> bits; t < gridDim.x; t += parts) {
             const u32x4 c = *reinterpret_cast<const u32x4 *>(table + t * digits + d);
             all += c;
@@ -235,34 +281,37 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
         for (uint32_t d = threadIdx.x; d < digits * kGroupWaves; d += kGroupBlock)
             s_cnt[d >> bits][d & (digits - 1)] = 0;
         const uint32_t first = step + static_cast<uint32_t>(w) * kWave * ITEMS + lane;
-        uint32_t key[ITEMS], rk[ITEMS];
+        uint32_t key[ITEMS], pos[ITEMS], rk[ITEMS];
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
             const uint32_t i = first + j * kWave;
             key[j] = i < end ? pass_key(keys, sorted, i, groups) : 0u;
+            pos[j] = positions != nullptr && i < end ? positions[i] : i;
         }
         __syncthreads();
+        uint32_t dig[ITEMS];
+        bool valid[ITEMS];
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j)
-            rk[j] = digit_rank((key[j] >> shift) & (digits - 1), first + j * kWave < end, bits, s_cnt[w]);
+        for (int j = 0; j < ITEMS; ++j) {
+            dig[j] = (key[j] >> shift) & (digits - 1);
+            valid[j] = first + j * kWave < end;
+        }
+        digit_ranks<ITEMS>(dig, valid, ITEMS, bits, s_cnt[w], rk);
         __syncthreads();
         const uint32_t count = counts_before(s_cnt, digits);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            const uint32_t i = first + j * kWave;
-            if (i >= end) continue;
-            const uint32_t d = (key[j] >> shift) & (digits - 1);
-            const uint32_t at = s_base[d] + s_cnt[w][d] + rk[j];
+            if (!valid[j]) continue;
+            const uint32_t at = s_base[dig[j]] + s_cnt[w][dig[j]] + rk[j];
             if (at >= n) continue;  // only a table changed under the call
-            const uint32_t pos = positions != nullptr ? positions[i] : i;
             if (sorted_out != nullptr) sorted_out[at] = key[j];
             if (positions_out != nullptr) {
-                positions_out[at] = pos;
+                positions_out[at] = pos[j];
             } else {
                 const bool kept = key[j] < groups;
-                if (order != nullptr && kept) order[at] = static_cast<int32_t>(pos);
-                if (ranks != nullptr) ranks[pos] = kept ? static_cast<int32_t>(at) : -1;
+                if (order != nullptr && kept) order[at] = static_cast<int32_t>(pos[j]);
+                if (ranks != nullptr) ranks[pos[j]] = kept ? static_cast<int32_t>(at) : -1;
             }
         }
         __syncthreads();
@@ -698,34 +747,59 @@ __global__ __launch_bounds__(kRowBlock) void embed_grad_kernel(
                 const uint32_t left = kSumRows - ((s >> lg) & (kSumRows - 1u));
                 count = count < left ? count : left;
             }
-            if (l == 0) {
-#pragma unroll 2
-                for (uint32_t j = 0; j < count; ++j) {
-                    const uint32_t i = static_cast<uint32_t>(order[s + j]);
-                    if (i >= n) continue;
-                    const T *src = dout + static_cast<int64_t>(i) * m.width;
-                    typename C::Raw r[CH];
+            // kRows rows in flight, then the rest one by one
+            const auto add_rows = [&](uint32_t first, auto rows) {
+                constexpr uint32_t R = decltype(rows)::value;
+                typename C::Raw r[R][CH];
+                bool ok[R];
 #pragma unroll
-                    for (int q = 0; q < CH; ++q) r[q] = C::load_stream(src + at[q]);
+                for (uint32_t j = 0; j < R; ++j) {
+                    const uint32_t i = static_cast<uint32_t>(order[first + j]);
+                    ok[j] = i < n;
+                    const T *src = dout + static_cast<int64_t>(ok[j] ? i : 0) * m.width;
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) r[j][q] = C::load_stream(src + at[q]);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < R; ++j) {
+                    if (!ok[j]) continue;
 #pragma unroll
                     for (int q = 0; q < CH; ++q) {
                         float x[N];
-                        C::unpack(r[q], x);
+                        C::unpack(r[j][q], x);
 #pragma unroll
                         for (int e = 0; e < N; ++e) acc[q][e] += x[e];
                     }
                 }
+            };
+            const auto add_sums = [&](const float *p, auto rows) {
+                constexpr uint32_t R = decltype(rows)::value;
+                float x[R][CH][N];
+#pragma unroll
+                for (uint32_t j = 0; j < R; ++j) {
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) load_values<float, N>(p + static_cast<int64_t>(j) * m.width + at[q], x[j][q]);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < R; ++j) {
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[q][e] += x[j][q][e];
+                    }
+                }
+            };
+            constexpr uint32_t kRows = CH == 1 ? 4 : 2;
+            using Many = std::integral_constant<uint32_t, kRows>;
+            using One = std::integral_constant<uint32_t, 1>;
+            uint32_t j = 0;
+            if (l == 0) {
+                for (; j + kRows <= count; j += kRows) add_rows(s + j, Many{});
+                for (; j < count; ++j) add_rows(s + j, One{});
             } else {
                 const float *p = sums.level[l - 1] + static_cast<int64_t>(s >> lg) * m.width;
-                for (uint32_t j = 0; j < count; ++j, p += m.width) {
-#pragma unroll
-                    for (int q = 0; q < CH; ++q) {
-                        float x[N];
-                        load_values<float, N>(p + at[q], x);
-#pragma unroll
-                        for (int e = 0; e < N; ++e) acc[q][e] += x[e];
-                    }
-                }
+                for (; j + kRows <= count; j += kRows) add_sums(p + static_cast<int64_t>(j) * m.width, Many{});
+                for (; j < count; ++j) add_sums(p + static_cast<int64_t>(j) * m.width, One{});
             }
             s += count << lg;
         }
@@ -807,8 +881,10 @@ int launch_small(const K *keys, uint32_t n, uint32_t groups, const GroupPlan &p,
     };
     if (n <= kGroupBlock)
         SSC_TRY(launch(std::integral_constant<int, 1>{}));
-    else
+    else if (n <= 4 * kGroupBlock)
         SSC_TRY(launch(std::integral_constant<int, 4>{}));
+    else
+        SSC_TRY(launch(std::integral_constant<int, 8>{}));
     return p.passes > 1 ? launch_offsets(sorted, n, groups, offsets, s) : SSC_OK;
 }
 
@@ -956,9 +1032,12 @@ int embed_impl(const void *table, int dtype, int64_t vocab, int64_t width, const
     });
 }
 
+// A level is made where the batch holds at least 16 of its blocks, the third
+// where it holds 64: a launch more for every batch, against at most 1024
+// blocks of 256 that a row with nearly all of the tokens has to add.
 int sum_levels(int64_t n) {
     int l = 0;
-    while (l < kSumLevels && n >> (kSumLg * (l + 2)) > 0) ++l;
+    while (l < kSumLevels && n >> (kSumLg * (l + 2) + (l == 2 ? 2 : 0)) > 0) ++l;
     return l;
 }
 

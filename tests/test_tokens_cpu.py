@@ -41,7 +41,7 @@ def test_group_refusals(name):
 
 
 def test_scratch_sizes():
-    assert ssc.group_scratch_bytes(4096, 511) == 0
+    assert ssc.group_scratch_bytes(8192, 511) == 0
     assert ssc.group_scratch_bytes(1000, 512) == 4000  # two passes leave their sorted keys
     # 17 spans of 1024 keys x 128 digits of 7 bits (100 groups and one more)
     assert ssc.group_scratch_bytes(16_385, 100) == 17 * 128 * 4
@@ -54,7 +54,8 @@ def test_scratch_sizes():
     assert L.ssc_embed_grad_scratch_bytes(255, 64) == 0
     assert L.ssc_embed_grad_scratch_bytes(256, 64) == 16 * 64 * 4
     assert L.ssc_embed_grad_scratch_bytes(4096, 64) == (256 + 16) * 64 * 4
-    assert L.ssc_embed_grad_scratch_bytes(65_536, 64) == (4096 + 256 + 16) * 64 * 4
+    assert L.ssc_embed_grad_scratch_bytes(65_536, 64) == (4096 + 256) * 64 * 4
+    assert L.ssc_embed_grad_scratch_bytes(2 ** 18, 64) == (16_384 + 1024 + 64) * 64 * 4
     assert ssc.sample_scratch_bytes(0, 100) == 0 and ssc.sample_scratch_bytes(4, 0) == 0
     assert ssc.sample_scratch_bytes(4, 100_000) > 0
 
