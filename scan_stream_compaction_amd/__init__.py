@@ -683,13 +683,13 @@ def _numel(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.numel()
 
 
-def _optional(t, name: str, like: torch.Tensor, n: int) -> torch.Tensor | None:
+def _optional(t, name: str, like: torch.Tensor, shape) -> torch.Tensor | None:
     """An int32 output that is wanted (True, or the tensor to write) or not."""
     if t is True:
-        return torch.empty(n, dtype=torch.int32, device=like.device)
+        return like.new_empty(shape, dtype=torch.int32)
     if t is None or t is False:
         return None
-    return _need(t, name, like, (torch.int32,), n)
+    return _need(t, name, like, (torch.int32,), like.numel())
 
 
 def group_scratch_bytes(n: int, groups: int) -> int:
@@ -711,11 +711,8 @@ def group_by_key(keys: torch.Tensor, groups: int, *, order=True, ranks=True,
     if not 1 <= groups < 2**31 - 1:
         raise ValueError(f"groups must be in [1, 2^31 - 2], not {groups}")
     order = _optional(order, "order", keys, n)
-    made = ranks is True
-    ranks = _optional(ranks, "ranks", keys, n)
-    if made and keys.dim() != 1:
-        ranks = ranks.view(keys.shape)
-    offsets = (torch.empty(groups + 1, dtype=torch.int32, device=keys.device) if offsets is None
+    ranks = _optional(ranks, "ranks", keys, keys.shape)
+    offsets = (keys.new_empty(groups + 1, dtype=torch.int32) if offsets is None
                else _need(offsets, "offsets", keys, (torch.int32,), groups + 1))
     scratch = _work_bytes(scratch, keys, group_scratch_bytes(n, groups))
     _row_call(name, keys, keys, n, groups, order, ranks, offsets, scratch, _numel(scratch))

@@ -35,7 +35,7 @@ constexpr int kPartLg = 12;
 constexpr int kPart = 1 << kPartLg;   // logits of a part
 constexpr int kPartBlock = 256;
 constexpr int kPartItems = kPart / kPartBlock;
-constexpr int kHistPart = 8192;       // fewest logits of a workgroup of a row's histogram
+constexpr int kHistPart = 4096;       // fewest logits of a workgroup of a row's histogram
 constexpr int kHistBlock = 512;
 constexpr int kBins = 2048;
 constexpr int kTokenBlock = 1024;
@@ -43,6 +43,7 @@ constexpr int kList = 4096;           // collected logits a row has room for
 constexpr int kListTopK = kList / 2;  // up to this top_k, all its logits are collected
 constexpr int64_t kVocabMax = int64_t{1} << 22;
 constexpr int kPartsMax = static_cast<int>(kVocabMax / kPart);
+static_assert(kPartsMax <= kTokenBlock, "a part to a thread");
 constexpr uint32_t kNoCut = 0xffffffffu;
 
 // What is known of a row's border. Bins are numbered from the maximum down:
@@ -650,20 +651,32 @@ __global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
 }
 
 // ---- border and token ----
+// A kept logit's weight; 0 and not counted for the others.
+struct Border {
+    uint32_t key, cut;  // smallest kept key, last index at which it is kept
+    __device__ __forceinline__ uint64_t weight(const Scale &sc, float x, int i, bool &kept) const {
+        const uint32_t k = key_of(x);
+        kept = false;
+        if (k == 0 || k < key || (k == key && static_cast<uint32_t>(i) > cut)) return 0;
+        const double w = sc.scaled(x);
+        kept = sc.large(w, x);
+        return kept ? Scale::fixed(w) : 0;
+    }
+};
+
 struct TokenShared {
     union {
         struct {
-            unsigned long long entry[kList];
+            __attribute__((aligned(16))) unsigned long long entry[kList];
         } list;
         Hist h;
     };
     FindShared<kTokenBlock> find;
     unsigned long long mass[kPartsMax];
-    uint32_t count;
-    uint32_t cut;
-    uint32_t border_key, border_cut;
+    unsigned long long at_skip, at_end, goal, total;
+    uint32_t count, cut;
+    Border border;
     int part;
-    unsigned long long goal, total;
 };
 
 // The slow way, for a row whose border bins hold more logits than the list
@@ -767,19 +780,6 @@ __device__ __forceinline__ uint32_t tie_index(const SampleArgs &a, const T *x, c
     return cut;
 }
 
-// A kept logit's weight; 0 and not counted for the others.
-struct Border {
-    uint32_t key, cut;  // smallest kept key, last index at which it is kept
-    __device__ __forceinline__ uint64_t weight(const Scale &sc, float x, int i, bool &kept) const {
-        const uint32_t k = key_of(x);
-        kept = false;
-        if (k == 0 || k < key || (k == key && static_cast<uint32_t>(i) > cut)) return 0;
-        const double w = sc.scaled(x);
-        kept = sc.large(w, x);
-        return kept ? Scale::fixed(w) : 0;
-    }
-};
-
 template <class T>
 __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, const Filters &f, const Scale &sc,
                                               TokenShared &sh) {
@@ -837,23 +837,74 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
     return out;
 }
 
-// Sorts n2 entries (a power of two) from the largest down: bitonic merges. A
-// wavefront's 64 pairs lie in 128 entries of its own while they are at most 64
-// apart, so only the longer distances need the workgroup's barriers.
+// Entries [0, n) of e from the largest down into out, for n2 <= 512: each
+// entry's place is the number of larger ones, counted by kTokenBlock / n2
+// threads together, two entries a read (n2 is a power of two of 32 at least, e
+// filled up with 0).
+__device__ __forceinline__ void rank_list(const unsigned long long *e, unsigned long long *out, int n, int n2) {
+    typedef unsigned long long Pair __attribute__((ext_vector_type(2)));
+    const Pair *pairs = reinterpret_cast<const Pair *>(e);
+    const int lg = __builtin_ctz(kTokenBlock / n2);
+    const int i = static_cast<int>(threadIdx.x) >> lg, part = static_cast<int>(threadIdx.x) & ((1 << lg) - 1);
+    const unsigned long long mine = e[i];
+    uint32_t place = 0;
+#pragma unroll 4
+    for (int j = part; j < (n + 1) / 2; j += 1 << lg) {
+        const Pair v = pairs[j];
+        place += (v[0] > mine ? 1u : 0u) + (v[1] > mine ? 1u : 0u);
+    }
+    for (int off = 1 << lg; off > 1; off >>= 1) place += __shfl_xor(place, off >> 1);
+    if (part == 0 && i < n) out[place] = mine;
+    __syncthreads();
+}
+
+// Sorts n2 entries (a power of two, 4 at least) from the largest down: bitonic
+// merges, two distances d and d / 2 at a time on four entries in registers.
+// A wavefront's entries are 256 of its own while d is at most 128, so only
+// the longer distances need the workgroup's barriers.
+__device__ __forceinline__ void order_pair(unsigned long long &u, unsigned long long &v, bool down) {
+    if ((u < v) == down) {
+        const unsigned long long x = u;
+        u = v;
+        v = x;
+    }
+}
 __device__ __forceinline__ void sort_list(unsigned long long *e, int n2) {
+    const int quads = n2 / 4;
     for (int size = 2; size <= n2; size <<= 1) {
-        for (int dist = size >> 1; dist > 0; dist >>= 1) {
-            for (int t = threadIdx.x; t < n2 / 2; t += kTokenBlock) {
-                const int i = 2 * t - (t & (dist - 1)), j = i + dist;
-                const unsigned long long u = e[i], v = e[j];
-                if ((u < v) == ((i & size) == 0)) {
-                    e[i] = v;
-                    e[j] = u;
+        int d = size >> 1;
+        // an odd number of distances: the first alone
+        const bool odd = (__builtin_ctz(static_cast<unsigned>(size)) & 1) != 0;
+        for (bool single = odd; d > 0; d >>= single ? 1 : 2, single = false) {
+            const int h = single ? d : d >> 1;
+            for (int t = threadIdx.x; t < quads; t += kTokenBlock) {
+                if (single) {  // pairs 2t and 2t + 1 of the distance
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int p = 2 * t + s, i = 2 * p - (p & (d - 1));
+                        unsigned long long u = e[i], v = e[i + d];
+                        order_pair(u, v, (i & size) == 0);
+                        e[i] = u;
+                        e[i + d] = v;
+                    }
+                } else {
+                    const int i = 4 * t - 3 * (t & (h - 1));
+                    const bool down = (i & size) == 0;
+                    unsigned long long q0 = e[i], q1 = e[i + h], q2 = e[i + d], q3 = e[i + d + h];
+                    order_pair(q0, q2, down);
+                    order_pair(q1, q3, down);
+                    order_pair(q0, q1, down);
+                    order_pair(q2, q3, down);
+                    e[i] = q0;
+                    e[i + h] = q1;
+                    e[i + d] = q2;
+                    e[i + d + h] = q3;
                 }
             }
-            // the next distance, or the next size's first
-            const int next = dist > 1 ? dist >> 1 : size;
-            if (dist > kWave || next > kWave || (dist == 1 && size == n2)) {
+            // the next step's first distance
+            const int left = single ? d >> 1 : d >> 2;
+            const int next = left > 0 ? left : size;
+            if (d > 2 * kWave || next > 2 * kWave || (left == 0 && size == n2)) {
                 __syncthreads();
             } else {
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -870,9 +921,16 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
     const int row = blockIdx.x;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const int64_t base = static_cast<int64_t>(row) * a.parts;
+    // all first loads before anything waits for one; a part to a thread
+    const RowState st = a.state[row];
+    const bool has_part = static_cast<int>(threadIdx.x) < a.parts;
+    const uint64_t part_mass = has_part ? a.part_mass[base + threadIdx.x] : 0;
+    uint32_t count = has_part ? a.part_count[base + threadIdx.x] : 0;
+    const uint64_t *list = a.list + static_cast<int64_t>(row) * kList;
+    const uint64_t first_entry = list[threadIdx.x];  // used where it has been written
     const Filters f(a, row);
     const float2 range = row_range(a, row);
-    const int64_t base = static_cast<int64_t>(row) * a.parts;
     if (range.x == -__builtin_inff()) {
         if (threadIdx.x == 0) {
             a.tokens[row] = -1;
@@ -882,12 +940,9 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         return;
     }
     const Scale sc(a, row, f, range);
-    const RowState st = a.state[row];
     const T *x = row_at<T>(a, row);
     Border border{1u, kNoCut};
-    for (int p = threadIdx.x; p < a.parts; p += kTokenBlock) sh.mass[p] = a.part_mass[base + p];
-    uint32_t count = 0;
-    for (int p = threadIdx.x; p < a.parts; p += kTokenBlock) count += a.part_count[base + p];
+    if (has_part) sh.mass[threadIdx.x] = part_mass;
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
     if (st.listed > kList) {
@@ -914,49 +969,63 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
     } else if (st.lo < kBins) {
         // the collected logits in order; those of [lo, hi] come first
         const int n = static_cast<int>(st.listed);
-        int n2 = 2;
+        int n2 = 32;
         while (n2 < n) n2 <<= 1;
-        for (int i = threadIdx.x; i < n2; i += kTokenBlock)
-            sh.list.entry[i] = i < n ? a.list[static_cast<int64_t>(row) * kList + i] : 0ull;
+        unsigned long long *sorted = sh.list.entry;
+        sorted[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? first_entry : 0ull;
+        for (int i = threadIdx.x + kTokenBlock; i < n2; i += kTokenBlock) sorted[i] = i < n ? list[i] : 0ull;
         __syncthreads();
-        sort_list(sh.list.entry, n2);
-        // each thread's consecutive entries, their weights and the running sum
+        if (n2 <= 512) {  // by the squares of n: 200 entries 1.2 us against 6 by merges, 512 as long
+            sorted += kList / 2;
+            rank_list(sh.list.entry, sorted, n, n2);
+        } else {
+            sort_list(sorted, n2);
+        }
+        // each thread's consecutive entries, their weights and the running
+        // sum; n1 of all entries lie in [lo, hi], the rest in the extra bin
         constexpr int kEach = kList / kTokenBlock;
+        unsigned long long entry[kEach];
         uint64_t we[kEach], ms = 0;
         double full[kEach];
-#pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const int i = static_cast<int>(threadIdx.x) * kEach + q;
-            full[q] = i < n ? sc.scaled(value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32))) : 0.0;
-            we[q] = Scale::fixed(full[q]);
-            ms += we[q];
-        }
-        const uint64_t mi = wave_scan64(ms);
-        if (lane == kWave - 1) sh.find.wave_mass[w] = mi;
-        if (threadIdx.x == 0) sh.total = 0;
-        __syncthreads();
-        uint64_t run = mi - ms;
-        for (int i = 0; i < w; ++i) run += sh.find.wave_mass[i];
-        // n1 entries lie in [lo, hi]; the rest in the extra bin
         uint32_t mine = 0;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
             const int i = static_cast<int>(threadIdx.x) * kEach + q;
-            if (i < n && sc.bin(value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32))) <= st.hi) ++mine;
+            entry[q] = 0;
+            full[q] = 0.0;
+            we[q] = 0;
+            if (i < n) {
+                entry[q] = sorted[i];
+                const float xe = value_of(static_cast<uint32_t>(entry[q] >> 32));
+                full[q] = sc.scaled(xe);
+                we[q] = Scale::fixed(full[q]);
+                ms += we[q];
+                mine += sc.bin(xe) <= st.hi ? 1u : 0u;
+            }
         }
+        const uint64_t mi = wave_scan64(ms);
         mine = wave_sum32(mine);
-        if (lane == 0) sh.find.wave_count[w] = mine;
+        if (lane == kWave - 1) {
+            sh.find.wave_mass[w] = mi;
+            sh.find.wave_count[w] = mine;
+        }
         __syncthreads();
+        uint64_t run = mi - ms;
         uint32_t n1 = 0;
-        for (int i = 0; i < kWaves; ++i) n1 += sh.find.wave_count[i];
-        // entries of [lo, hi] that top_k leaves, and where the weight of the
-        // first top_k ends in the list
-        uint32_t nk = n1, end = n1;
-        uint64_t from = st.mass;  // weight before the list's first entry that counts towards `end`
+        for (int i = 0; i < kWaves; ++i) {
+            run += i < w ? sh.find.wave_mass[i] : 0;
+            n1 += sh.find.wave_count[i];
+        }
+        // nk: the entries of [lo, hi] that top_k leaves; the first top_k end
+        // before entry `end`, and their weight is `from` and that of the
+        // entries from `skip` on
+        uint32_t nk = n1, skip = 0, end = n1;
+        uint64_t from = st.mass;
         if (f.top_k > 0 && st.total == 0) {
             if (st.extra >= 0) {
                 const uint32_t more = static_cast<uint32_t>(f.top_k) - st.extra_count;
-                end = n1 + (more < static_cast<uint32_t>(n) - n1 ? more : static_cast<uint32_t>(n) - n1);
+                skip = n1;
+                end = n1 + more < static_cast<uint32_t>(n) ? n1 + more : static_cast<uint32_t>(n);
                 from = st.extra_mass;
             } else {
                 const uint32_t more = static_cast<uint32_t>(f.top_k) - st.count;
@@ -964,53 +1033,41 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
                 end = nk;
             }
         }
-        // sum of the entries that lie between `from` and `end`: of the extra
-        // bin's alone, where there is one
-        const uint32_t skip = st.extra >= 0 ? n1 : 0u;
-        uint64_t part = 0;
+        // running sums at skip and end, by the threads that hold the entries before them
+        uint64_t at = run;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
-            const uint32_t i = threadIdx.x * kEach + q;
-            if (i >= skip && i < end) part += we[q];
+            const uint32_t i = threadIdx.x * kEach + q + 1;
+            at += we[q];
+            if (i == skip) sh.at_skip = at;
+            if (i == end) sh.at_end = at;
         }
-        part = wave_sum64(part);
+        if (threadIdx.x == 0) {
+            if (skip == 0) sh.at_skip = 0;
+            if (end == 0) sh.at_end = 0;
+            sh.border = Border{n > 0 ? static_cast<uint32_t>(sorted[0] >> 32) + 1u : 1u, kNoCut};  // nothing of the list
+        }
         __syncthreads();
-        if (lane == 0) sh.find.wave_mass[w] = part;
-        __syncthreads();
-        uint64_t all = from;
-        for (int i = 0; i < kWaves; ++i) all += sh.find.wave_mass[i];
-        if (st.total != 0) all = st.total;
+        const uint64_t all = st.total != 0 ? st.total : from + (sh.at_end - sh.at_skip);
         const double target = f.nucleus() ? static_cast<double>(f.top_p) * static_cast<double>(all) : __builtin_inf();
-        uint32_t keep = 0;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
             const uint32_t i = threadIdx.x * kEach + q;
-            if (i < nk && static_cast<double>(st.mass + run) < target) {
-                keep = i + 1;
-                if (sc.large(full[q], value_of(static_cast<uint32_t>(sh.list.entry[i] >> 32)))) {
-                    const uint32_t index = ~static_cast<uint32_t>(sh.list.entry[i]);
-                    __hip_atomic_fetch_add(&sh.mass[index >> kPartLg], static_cast<unsigned long long>(we[q]),
-                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                    ++count;
-                }
-            }
+            const bool keep = i < nk && static_cast<double>(st.mass + run) < target;
             run += we[q];
-        }
-        for (int off = 32; off > 0; off >>= 1) {
-            const uint32_t o = __shfl_xor(keep, off);
-            keep = keep > o ? keep : o;
+            if (!keep) continue;
+            const uint32_t index = ~static_cast<uint32_t>(entry[q]);
+            if (sc.large(full[q], value_of(static_cast<uint32_t>(entry[q] >> 32)))) {
+                __hip_atomic_fetch_add(&sh.mass[index >> kPartLg], static_cast<unsigned long long>(we[q]),
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                ++count;
+            }
+            // the last kept entry is the border
+            if (!(i + 1 < nk && static_cast<double>(st.mass + run) < target))
+                sh.border = Border{static_cast<uint32_t>(entry[q] >> 32), index};
         }
         __syncthreads();
-        if (lane == 0) sh.find.wave_count[w] = keep;
-        __syncthreads();
-        keep = 0;
-        for (int i = 0; i < kWaves; ++i) keep = keep > sh.find.wave_count[i] ? keep : sh.find.wave_count[i];
-        if (keep > 0) {
-            border.key = static_cast<uint32_t>(sh.list.entry[keep - 1] >> 32);
-            border.cut = ~static_cast<uint32_t>(sh.list.entry[keep - 1]);
-        } else {  // nothing of the list: what precedes its first entry
-            border.key = static_cast<uint32_t>(sh.list.entry[0] >> 32) + 1u;
-        }
+        border = sh.border;
     }
     // the part in which the running weight passes the goal
     count = wave_sum32(count);
