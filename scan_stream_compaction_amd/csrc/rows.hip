@@ -246,6 +246,20 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t digits = 1u << bits;
+    const uint32_t begin = blockIdx.x * span;
+    const uint32_t end = n - begin < span ? n : begin + span;
+    // a step's keys: the first step's are on their way while the table is read
+    uint32_t first = begin + static_cast<uint32_t>(w) * kWave * ITEMS + lane;
+    uint32_t key[ITEMS], pos[ITEMS];
+    const auto load = [&]() {
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t i = first + j * kWave;
+            key[j] = i < end ? pass_key(keys, sorted, i, groups) : 0u;
+            pos[j] = positions != nullptr && i < end ? positions[i] : i;
+        }
+    };
+    load();
     // where this span's first key of each digit goes: the keys of smaller
     // digits, then those of the same digit in earlier spans; a thread sums
     // four digits over every parts-th row of the table
@@ -275,21 +289,15 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
         if (offsets != nullptr && blockIdx.x == 0 && threadIdx.x <= groups)
             offsets[threadIdx.x] = static_cast<int32_t>(start);
     }
-    const uint32_t begin = blockIdx.x * span;
-    const uint32_t end = n - begin < span ? n : begin + span;
     for (uint32_t step = begin; step < end; step += ITEMS * kGroupBlock) {
+        if (step != begin) {
+            first += ITEMS * kGroupBlock;
+            load();
+        }
         for (uint32_t d = threadIdx.x; d < digits * kGroupWaves; d += kGroupBlock)
             s_cnt[d >> bits][d & (digits - 1)] = 0;
-        const uint32_t first = step + static_cast<uint32_t>(w) * kWave * ITEMS + lane;
-        uint32_t key[ITEMS], pos[ITEMS], rk[ITEMS];
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            const uint32_t i = first + j * kWave;
-            key[j] = i < end ? pass_key(keys, sorted, i, groups) : 0u;
-            pos[j] = positions != nullptr && i < end ? positions[i] : i;
-        }
         __syncthreads();
-        uint32_t dig[ITEMS];
+        uint32_t dig[ITEMS], rk[ITEMS];
         bool valid[ITEMS];
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
@@ -438,7 +446,8 @@ __device__ __forceinline__ void store_values(G *p, const float *f) {
 }
 
 // Which row and which of its chunks a thread works on: 2^lg threads to a
-// row, the column blocks in gridDim.y. WAVE: whole wavefronts to a row (lg >=
+// row, the column blocks in gridDim.y, further rows in gridDim.z (a
+// dimension of a launch holds at most 2^32 - 1 threads). WAVE: whole wavefronts to a row (lg >=
 // 6), whose ids, ranks and weights then come through scalar loads. CH: chunks
 // that a thread has in flight at a time.
 struct RowMap {
@@ -451,7 +460,8 @@ constexpr int kRowBlock = 256;
 template <bool WAVE>
 __device__ __forceinline__ int64_t row_of(const RowMap &m) {
     const uint32_t sub = threadIdx.x >> m.lg;
-    return (static_cast<int64_t>(blockIdx.x) << (8 - m.lg)) + (WAVE ? uniform(sub) : sub);
+    const int64_t block = static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x;
+    return (block << (8 - m.lg)) + (WAVE ? uniform(sub) : sub);
 }
 __device__ __forceinline__ int col_of(const RowMap &m) {
     return static_cast<int>((blockIdx.y << m.lg) + (threadIdx.x & ((1u << m.lg) - 1u)));
@@ -1003,7 +1013,9 @@ RowLaunch row_launch(int64_t rows, int64_t width, int per_chunk, bool split) {
     int64_t cols = 1;
     const int64_t parts = (r.map.chunks + (1 << lg) - 1) >> lg;
     while (split && cols < parts && cols < 64 && blocks * cols < enough) ++cols;
-    r.grid = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cols));
+    constexpr int64_t kMostBlocks = int64_t{1} << 22;
+    const int64_t x = blocks < kMostBlocks ? blocks : kMostBlocks;
+    r.grid = dim3(static_cast<unsigned>(x), static_cast<unsigned>(cols), static_cast<unsigned>((blocks + x - 1) / x));
     r.wave = lg >= 6;
     const int64_t each = (parts + cols - 1) / cols;
     r.deep = !r.wave || each == 1 ? 1 : (each == 2 ? 2 : 4);

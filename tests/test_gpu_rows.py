@@ -169,6 +169,27 @@ def test_embed_unaligned_rows_and_nonfinite():
     assert bool((ssc.embed_rows(table[:0], ids) == 0).all())
 
 
+def test_many_wide_rows():
+    """More workgroups than one dimension of a launch holds, and elements past
+    2^32: 17,000,003 rows of 1030 bf16 (35 GB)."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of device memory")
+    n, width, vocab = 17_000_003, 1030, 1000
+    table = _randn(_gen(31), vocab, width, dtype=torch.bfloat16)
+    ids = (torch.arange(n, device=DEV) * 7919) % vocab
+    out = ssc.embed_rows(table, ids, 1.0)
+    for first in range(0, n, 1_000_000):
+        assert torch.equal(out[first:first + 1_000_000:997], table[ids[first:first + 1_000_000:997]])
+    assert torch.equal(out[-5000:], table[ids[-5000:]])
+    # back as one row a token, from the same buffer: ranks in reverse
+    ranks = torch.arange(n - 1, -1, -1, device=DEV, dtype=torch.int32)
+    back = ssc.combine_rows(out, ranks)
+    del out
+    for first in range(0, n, 1_000_000):
+        assert torch.equal(back[first:first + 1_000_000:991], table[ids[ranks[first:first + 1_000_000:991].long()]])
+    assert torch.equal(back[-5000:], table[ids[ranks[-5000:].long()]])
+
+
 def _grad_case(ids, vocab, width, dtype, scale, gdtype, seed):
     g = _gen(seed)
     n = ids.numel()
