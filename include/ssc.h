@@ -391,8 +391,8 @@ typedef enum ssc_dtype {
  *     depends on the sizes and the ranks only, so a call repeats bit for bit.
  */
 
-/* Scratch bytes of a grouping of n keys (0 for up to 8192 keys of at most 511
- * groups). */
+/* Scratch bytes of a grouping of n keys (0 for up to 8192 keys of at most
+ * 4096 groups). */
 size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
 
 /* Stable partition into `groups` groups: key k belongs to group k, and one
@@ -405,7 +405,7 @@ size_t ssc_group_scratch_bytes(int64_t n, int64_t groups);
  *                entries past that are not written               (nullable)
  * The many-way form of ssc_partition_i32: one counting and one scattering
  * step per 9 bits of group number (a single launch for up to 8192 keys of at
- * most 511 groups). */
+ * most 4096 groups). */
 int ssc_group_by_key_i32(const int32_t *keys, int64_t n, int64_t groups, int32_t *order,
                          int32_t *ranks, int32_t *offsets, void *scratch, size_t scratch_bytes,
                          void *stream);

@@ -676,7 +676,7 @@ def _work_bytes(scratch, like: torch.Tensor, nbytes: int) -> torch.Tensor | None
     """The caller's scratch, or a new one that needs no zeros (None for none)."""
     if scratch is not None:
         return _scratch(scratch, like, nbytes)
-    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _numel(t: torch.Tensor | None) -> int:
@@ -759,7 +759,7 @@ def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, 
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to a given out")
-        out = torch.empty(vocab, width, dtype=dout.dtype if dtype is None else dtype, device=dout.device)
+        out = dout.new_empty((vocab, width), dtype=dtype)
     else:
         _need(out, "out", dout, None, vocab * width)
         if dtype is not None and out.dtype != dtype:
@@ -889,7 +889,7 @@ def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor
             raise ValueError(f"{name} holds one value a row")
         settings.append(t)
     tokens, kept, logprobs = (
-        torch.empty(rows, dtype=dt, device=logits.device) if t is None else _need(t, name, logits, (dt,), rows)
+        logits.new_empty(rows, dtype=dt) if t is None else _need(t, name, logits, (dt,), rows)
         for t, name, dt in ((tokens, "tokens", torch.int32), (kept, "kept", torch.int32),
                             (logprobs, "logprobs", torch.float32)))
     scratch = _work_bytes(scratch, logits, sample_scratch_bytes(rows, vocab))

@@ -40,6 +40,7 @@ constexpr int kGroupWaves = kGroupBlock / kWave;
 constexpr int kDigitBits = 9;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kGroupSmall = 8 * kGroupBlock;    // keys one workgroup sorts alone
+constexpr int kGroupFew = 4096;                 // groups whose offsets it then finds itself
 constexpr int kGroupTiles = 256;                // most workgroups of a tiled pass
 
 template <class K>
@@ -116,6 +117,18 @@ __device__ __forceinline__ uint32_t counts_before(uint32_t (*cnt)[kDigits], uint
     return total;
 }
 
+// Number of sorted keys below v, known to lie in [lo, hi].
+__device__ __forceinline__ uint32_t keys_below(const uint32_t *sorted, uint32_t lo, uint32_t hi, uint32_t v) {
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (sorted[mid] < v)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
 // Up to 8192 keys: one workgroup holds (key, position) in registers and
 // exchanges them through LDS between passes.
 template <class K, int ITEMS>
@@ -185,9 +198,15 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
         if (i < n) {
             key[j] = s_key[i];
             pos[j] = s_pos[i];
-            if (passes > 1) sorted_out[i] = key[j];
+            if (sorted_out != nullptr) sorted_out[i] = key[j];
             if (order != nullptr && key[j] < groups) order[i] = static_cast<int32_t>(pos[j]);
         }
+    }
+    if (passes == 1) {  // the digit starts are the offsets
+        if (threadIdx.x <= groups) offsets[threadIdx.x] = static_cast<int32_t>(s_start[threadIdx.x]);
+    } else if (sorted_out == nullptr) {  // 0.9 us for each 1024 groups, against a launch of 4 us for any number
+        for (uint32_t v = threadIdx.x; v <= groups; v += kGroupBlock)
+            offsets[v] = static_cast<int32_t>(keys_below(s_key, 0, n, v));
     }
     if (ranks != nullptr) {
         __syncthreads();
@@ -203,8 +222,6 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
             if (i < n) ranks[i] = static_cast<int32_t>(s_key[i]);
         }
     }
-    // the digit starts of a single pass are the offsets
-    if (passes == 1 && threadIdx.x <= groups) offsets[threadIdx.x] = static_cast<int32_t>(s_start[threadIdx.x]);
 }
 
 // The tiled form: a pass is a counting launch and a scattering launch, each
@@ -341,24 +358,8 @@ __global__ __launch_bounds__(kGroupBlock) void group_offsets_kernel(const uint32
     __syncthreads();
     const uint32_t v = blockIdx.x * kGroupBlock + threadIdx.x;
     if (v > groups) return;
-    uint32_t lo = 0, hi = samples;  // strides that end below v
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (s_key[mid] < v)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    hi = lo < samples ? (lo + 1) * stride - 1 : n;
-    lo *= stride;
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (sorted[mid] < v)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    offsets[v] = static_cast<int32_t>(lo);
+    const uint32_t s = keys_below(s_key, 0, samples, v);  // strides that end below v
+    offsets[v] = static_cast<int32_t>(keys_below(sorted, s * stride, s < samples ? (s + 1) * stride - 1 : n, v));
 }
 
 __global__ __launch_bounds__(256) void fill_zero_kernel(uint32_t *__restrict__ p, int64_t words) {
@@ -878,7 +879,8 @@ GroupPlan group_plan(int64_t n, int64_t groups) {
     p.bits = (all + p.passes - 1) / p.passes;
     if (p.bits < 2) p.bits = 2;  // the table is read four digits at a time
     if (n <= kGroupSmall) {
-        p.bytes = p.passes > 1 ? static_cast<size_t>(n) * 4 : 0;  // the sorted keys
+        // the sorted keys, for a launch that finds the offsets of many groups
+        p.bytes = p.passes > 1 && groups > kGroupFew ? static_cast<size_t>(n) * 4 : 0;
         return p;
     }
     int64_t tiles = (n + kGroupBlock - 1) / kGroupBlock;
@@ -918,7 +920,7 @@ int launch_small(const K *keys, uint32_t n, uint32_t groups, const GroupPlan &p,
         SSC_TRY(launch(std::integral_constant<int, 4>{}));
     else
         SSC_TRY(launch(std::integral_constant<int, 8>{}));
-    return p.passes > 1 ? launch_offsets(sorted, n, groups, offsets, s) : SSC_OK;
+    return sorted != nullptr ? launch_offsets(sorted, n, groups, offsets, s) : SSC_OK;
 }
 
 template <class K>
@@ -949,7 +951,7 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
         return launched();
     }
     const uint32_t un = static_cast<uint32_t>(n), ug = static_cast<uint32_t>(groups);
-    if (n <= kGroupSmall) return launch_small(keys, un, ug, p, order, ranks, offsets, static_cast<uint32_t *>(scratch), s);
+    if (n <= kGroupSmall) return launch_small(keys, un, ug, p, order, ranks, offsets, p.bytes > 0 ? static_cast<uint32_t *>(scratch) : nullptr, s);
     uint32_t *table = static_cast<uint32_t *>(scratch);
     uint32_t *buf[2][2];  // keys and positions of the two sides
     uint32_t *at = table + p.table_bytes / 4;

@@ -82,7 +82,7 @@ def _check_group(keys, groups, **kw):
 GROUP_SIZES = [1, 2, 63, 64, 65, 1023, 1024, 1025, 4095, 4097, 8191, 8192, 8193, 17408, 40961, 300_001]
 
 
-@pytest.mark.parametrize("groups", [1, 2, 8, 511, 512, 1000, 131_072])
+@pytest.mark.parametrize("groups", [1, 2, 8, 511, 512, 1000, 4096, 4097, 131_072])
 @pytest.mark.parametrize("n", GROUP_SIZES)
 def test_group_by_key(n, groups):
     r = np.random.RandomState(n * 7 + groups)

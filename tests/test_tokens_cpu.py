@@ -41,8 +41,8 @@ def test_group_refusals(name):
 
 
 def test_scratch_sizes():
-    assert ssc.group_scratch_bytes(8192, 511) == 0
-    assert ssc.group_scratch_bytes(1000, 512) == 4000  # two passes leave their sorted keys
+    assert ssc.group_scratch_bytes(8192, 4096) == 0
+    assert ssc.group_scratch_bytes(1000, 4097) == 4000  # the sorted keys, to find many offsets in
     # 17 spans of 1024 keys x 128 digits of 7 bits (100 groups and one more)
     assert ssc.group_scratch_bytes(16_385, 100) == 17 * 128 * 4
     # two passes of 9 bits: the table, (key, position) once, sorted keys
