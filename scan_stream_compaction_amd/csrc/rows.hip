@@ -48,9 +48,10 @@ __device__ __forceinline__ uint32_t key_of(K k, uint32_t groups) {
     return k >= 0 && static_cast<uint64_t>(k) < groups ? static_cast<uint32_t>(k) : groups;
 }
 
-// Ranks of `items` (at most ITEMS) consecutive sets of 64 keys among the keys this wavefront has
-// seen, in order; cnt holds the wavefront's counts. The lanes' masks do not
-// depend on one another and come first; the counts then follow key order.
+// Ranks of `items` (at most ITEMS) consecutive sets of 64 keys among the keys
+// this wavefront has seen, in order; cnt holds the wavefront's counts. The
+// lanes' masks do not depend on one another and come first; the counts then
+// follow key order.
 template <int ITEMS>
 __device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bool (&valid)[ITEMS], int items,
                                             int bits, uint32_t *cnt, uint32_t (&rk)[ITEMS]) {
@@ -374,6 +375,7 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(uint32_t *__restrict__ p
 // no alignment beyond their element's: gfx950 takes unaligned 16-byte
 // global accesses.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
+
 template <class T, bool VEC>
 struct Chunk {
     static constexpr int kN = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
@@ -448,9 +450,9 @@ __device__ __forceinline__ void store_values(G *p, const float *f) {
 
 // Which row and which of its chunks a thread works on: 2^lg threads to a
 // row, the column blocks in gridDim.y, further rows in gridDim.z (a
-// dimension of a launch holds at most 2^32 - 1 threads). WAVE: whole wavefronts to a row (lg >=
-// 6), whose ids, ranks and weights then come through scalar loads. CH: chunks
-// that a thread has in flight at a time.
+// dimension of a launch holds at most 2^32 - 1 threads). WAVE: whole
+// wavefronts to a row (lg >= 6), whose ids, ranks and weights then come through
+// scalar loads. CH: chunks that a thread has in flight at a time.
 struct RowMap {
     int lg;          // log2 of the threads of a row (0 .. 8)
     int chunks;      // chunks of a row
@@ -951,7 +953,9 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
         return launched();
     }
     const uint32_t un = static_cast<uint32_t>(n), ug = static_cast<uint32_t>(groups);
-    if (n <= kGroupSmall) return launch_small(keys, un, ug, p, order, ranks, offsets, p.bytes > 0 ? static_cast<uint32_t *>(scratch) : nullptr, s);
+    if (n <= kGroupSmall)
+        return launch_small(keys, un, ug, p, order, ranks, offsets,
+                            p.bytes > 0 ? static_cast<uint32_t *>(scratch) : nullptr, s);
     uint32_t *table = static_cast<uint32_t *>(scratch);
     uint32_t *buf[2][2];  // keys and positions of the two sides
     uint32_t *at = table + p.table_bytes / 4;

@@ -317,9 +317,11 @@ __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
 }
 
 // ---- counts and weights by bin, and the border bins ----
+// The last 64, one a lane, take what needs no place: masked logits are many,
+// and a wavefront's adds to one bin go one after another.
 struct Hist {
-    unsigned long long mass[kBins + 1];  // the last for what is no token
-    uint32_t count[kBins + 1];
+    unsigned long long mass[kBins + kWave];
+    uint32_t count[kBins + kWave];
 };
 
 __device__ __forceinline__ void hist_count(Hist &h, int bin) {
@@ -411,6 +413,8 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     const bool counts = f.top_k > 0, masses = f.nucleus() && !f.small_k();
     const auto each = [&](auto counted, auto weighed) {
         constexpr int kStep = kHistBlock * L::kN, kDeep = 2;
+        const int nowhere = kBins + lane_id();
+        uint32_t deepest = 0;
         for (int i0 = (blockIdx.x * kHistBlock + static_cast<int>(threadIdx.x)) * L::kN; i0 < a.vocab;
              i0 += kDeep * a.splits * kStep) {
             L v[kDeep];
@@ -421,11 +425,23 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
 #pragma unroll
                 for (int e = 0; e < L::kN; ++e) {
                     const float xe = v[j].x[e];
-                    const int b = is_token(xe) ? sc.bin(xe) : kBins;
-                    if (decltype(counted)::value) hist_count(h, b);
-                    if (decltype(weighed)::value) hist_mass(h, b, sc.weight(xe));
+                    const int b = is_token(xe) ? sc.bin(xe) : nowhere;
+                    if (decltype(counted)::value) {  // the last bin's in a register
+                        const bool last = b == kBins - 1;
+                        deepest += last ? 1u : 0u;
+                        hist_count(h, last ? nowhere : b);
+                    }
+                    if (decltype(weighed)::value) {
+                        const uint64_t w = sc.weight(xe);
+                        hist_mass(h, w != 0 ? b : nowhere, w);
+                    }
                 }
             }
+        }
+        if (decltype(counted)::value) {
+            deepest = wave_sum32(deepest);
+            if (lane_id() == 0 && deepest != 0)
+                __hip_atomic_fetch_add(&h.count[kBins - 1], deepest, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
     };
     if (counts && masses)
@@ -683,7 +699,7 @@ struct TokenShared {
 // (equal or nearly equal logits in numbers): the border key digit by digit.
 template <class T>
 __device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Scale &sc, TokenShared &sh,
-                                       uint32_t prefix, int shift, int width) {
+                                       bool weigh, uint32_t prefix, int shift, int width) {
     for (int b = threadIdx.x; b < kBins; b += kTokenBlock) {
         sh.h.mass[b] = 0;
         sh.h.count[b] = 0;
@@ -696,10 +712,20 @@ __device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Sc
 #pragma unroll
         for (int e = 0; e < L::kN; ++e) {
             const uint32_t k = key_of(v.x[e]);
-            if (k == 0 || (shift + width < 32 && k >> (shift + width) != prefix)) continue;
+            const bool mine = k != 0 && (shift + width >= 32 || k >> (shift + width) == prefix);
+            const uint64_t all = ballot(mine);
+            if (all == 0) continue;
+            // the logits equal to the first lane's go in one add: this way is
+            // taken for rows with many of the same
+            const uint32_t k0 = static_cast<uint32_t>(
+                __builtin_amdgcn_readlane(static_cast<int>(k), __builtin_ctzll(all)));
+            const uint64_t same = ballot(mine && k == k0);
+            const bool first = lane_id() == __builtin_ctzll(all);
+            if (!mine || (k == k0 && !first)) continue;
+            const uint32_t n = first ? static_cast<uint32_t>(__builtin_popcountll(same)) : 1u;
             const int b = static_cast<int>((k >> shift) & ((1u << width) - 1u));
-            hist_count(sh.h, b);
-            hist_mass(sh.h, b, sc.weight(v.x[e]));
+            __hip_atomic_fetch_add(&sh.h.count[b], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (weigh) hist_mass(sh.h, b, n * sc.weight(v.x[e]));
         }
     }
     __syncthreads();
@@ -709,14 +735,14 @@ __device__ __forceinline__ void refine(const SampleArgs &a, const T *x, const Sc
 // key; -1 where neither is reached).
 template <class T>
 __device__ __forceinline__ Found border_key(const SampleArgs &a, const T *x, const Scale &sc, TokenShared &sh,
-                                            uint32_t need, double target) {
+                                            bool weigh, uint32_t need, double target) {
     const int which = need > 0 ? 0 : 1;
     uint32_t key = 0, before = 0;
     uint64_t before_mass = 0;
     Found f{};
-    for (int level = 0; level < 3; ++level) {
+    for (int level = 0; level < (sizeof(T) == 2 ? 2 : 3); ++level) {
         const int shift = level == 0 ? 21 : (level == 1 ? 10 : 0), width = level == 2 ? 10 : 11;
-        refine(a, x, sc, sh, key, shift, width);
+        refine(a, x, sc, sh, weigh, key, shift, width);
         find_bins<kTokenBlock, true>(sh.h, sh.find, need, target, -1.0, before, before_mass);
         f = sh.find.found[which];
         __syncthreads();
@@ -725,6 +751,7 @@ __device__ __forceinline__ Found border_key(const SampleArgs &a, const T *x, con
         before = f.before;
         before_mass = f.before_mass;
     }
+    if (sizeof(T) == 2) key = key << 10 | ((key >> 21) != 0 ? 0u : 0x3ffu);  // the sign gives the rest
     f.bin = static_cast<int>(key);
     return f;
 }
@@ -792,7 +819,7 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
         return out;
     }
     if (f.top_k > 0) {
-        const Found k = border_key(a, x, sc, sh, static_cast<uint32_t>(f.top_k), -1.0);
+        const Found k = border_key(a, x, sc, sh, f.nucleus(), static_cast<uint32_t>(f.top_k), -1.0);
         if (k.bin != -1) {
             out.key = static_cast<uint32_t>(k.bin);
             ties = static_cast<uint32_t>(f.top_k) - k.before;
@@ -802,7 +829,7 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
     }
     if (f.nucleus()) {
         if (all < 0.0) {  // all of the row's
-            refine(a, x, sc, sh, 0, 21, 11);
+            refine(a, x, sc, sh, true, 0, 21, 11);
             uint64_t m = 0;
             for (int b = threadIdx.x; b < kBins; b += kTokenBlock) m += sh.h.mass[b];
             m = wave_sum64(m);
@@ -814,7 +841,7 @@ __device__ __forceinline__ Border slow_border(const SampleArgs &a, const T *x, c
             all = static_cast<double>(m);
         }
         const double target = static_cast<double>(f.top_p) * all;
-        const Found p = border_key(a, x, sc, sh, 0, target);
+        const Found p = border_key(a, x, sc, sh, true, 0, target);
         if (p.bin != -1) {
             // ties j = 0, 1, ... are kept while before_mass + j * weight < target
             const uint32_t key = static_cast<uint32_t>(p.bin);

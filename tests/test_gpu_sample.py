@@ -241,3 +241,18 @@ def test_refusals_on_the_gpu():
     with pytest.raises(ssc.SSCError):
         ssc.sample_rows(torch.zeros(1, 2 ** 22 + 1, device=DEV), u[:1])
     assert ssc.sample_rows(x[:0], u[:0])[0].numel() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("seed", range(4))
+def test_rows_of_few_values(dtype, seed):
+    """More equal logits at the border than are collected, beside settings that cut them."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    rows, vocab = 5, (9000, 20_001, 60_000)[seed % 3]
+    logits = (torch.randint(-4, 3, (rows, vocab), device=DEV, generator=g) * (1.0, 0.37, 3.1)[seed % 3]).to(dtype)
+    u, t, p = (torch.rand(rows, device=DEV, generator=g) for _ in range(3))
+    k = torch.randint(0, vocab, (rows,), device=DEV, generator=g).int()
+    _check(logits, u, top_k=k)
+    _check(logits, u, top_p=p)
+    _check(logits, u, 0.3 + t, k, p)
