@@ -19,6 +19,10 @@
 // Launches, each over parts of rows except the last: maxima; histograms (only
 // where a filter is given; a row's last workgroup finds the border bins); sums
 // of the better bins with the border bins' logits collected; border and token.
+// 256 rows of 131,072 bf16 under mixed settings take 13 + 33 + 29 + 14 us, the
+// first bound by HBM, the second by LDS adds (29 clocks a wavefront) and the
+// border search at its end, the third by exponentials, the last by latency;
+// one such row of fp32 takes 3.4 + 9.3 + 4.8 + 10 us, latency throughout.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1201,7 +1205,8 @@ SamplePlan sample_plan(int64_t rows, int64_t vocab) {
 template <class T>
 int sample_launch(const SampleArgs &a, int64_t rows, bool searched, hipStream_t s) {
     const unsigned r = static_cast<unsigned>(rows);
-    // up to 4096 workgroups, each with several parts of a row where there are more
+    // up to 4096 workgroups, each with several parts of a row where there are
+    // more (sums of 256 rows of 131,072: 2048, 4096, 8192 workgroups 35, 30, 32 us)
     const int64_t each = (static_cast<int64_t>(a.parts) * rows + 4095) / 4096;
     const dim3 parts(static_cast<unsigned>((a.parts + each - 1) / each), r);
     hipLaunchKernelGGL((sample_max_kernel<T>), parts, dim3(kPartBlock), 0, s, a);
