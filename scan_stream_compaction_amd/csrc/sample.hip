@@ -39,7 +39,8 @@ constexpr int kPartLg = 12;
 constexpr int kPart = 1 << kPartLg;   // logits of a part
 constexpr int kPartBlock = 256;
 constexpr int kPartItems = kPart / kPartBlock;
-constexpr int kHistPart = 4096;       // fewest logits of a workgroup of a row's histogram
+constexpr int kHistPart = 8192;       // fewest logits of a workgroup of a row's histogram
+constexpr int kHistMost = 32768;      // and most, where the row is split
 constexpr int kHistBlock = 512;
 constexpr int kBins = 2048;
 constexpr int kTokenBlock = 1024;
@@ -1280,14 +1281,21 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
     a.part_count = reinterpret_cast<uint32_t *>(base + p.part_count);
     a.state = reinterpret_cast<RowState *>(base + p.state);
     a.list = reinterpret_cast<uint64_t *>(base + p.list);
-    // A histogram only where a row may ask for one, its rows split until
-    // there are eight workgroups to a compute unit: rows differ in work (256
-    // rows of 131,072: 2, 4, 8, 16 workgroups a row 62, 39, 33, 43 us).
+    // A histogram only where a row may ask for one. A workgroup adds its 2048
+    // bins to the row's by atomics, so a split costs as much as some thousand
+    // logits: rows are split until there are two workgroups to a compute unit
+    // or parts are of 8192 logits, and into parts of at most 32,768 in any
+    // case, since rows differ in work. bf16, top_k of 50, top_p of 0.9, us:
+    //   part                1 x 131,072   64 x 131,072   256 x 131,072   1 x 4,194,304
+    //   4096                10.3, 12.2    26.8, 40.9     104, 139        34, 40
+    //   8192                10.3, 12.0    18.6, 31.1     55, 76          23, 26
+    //   16,384              11.8, 13.6    13.8, 20.2     36, 55          19, 23
+    //   32,768              12.1, 17.3    13.9, 21.0     28, 48          18, 23
     const bool searched = top_k != nullptr || top_p != nullptr;
     a.splits = 1;
     if (searched) {
         const int64_t most = (vocab + kHistPart - 1) / kHistPart;
-        while (a.splits < most && a.splits * rows < 2048) ++a.splits;
+        while (a.splits < most && (a.splits * rows < 512 || vocab > int64_t{kHistMost} * a.splits)) ++a.splits;
         a.hist_mass = reinterpret_cast<uint64_t *>(base + p.hist_mass);
         a.hist_count = reinterpret_cast<uint32_t *>(base + p.hist_count);
     }
