@@ -692,7 +692,7 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
 // largest blocks that fit into its range, at most 30 of a level: the work
 // per row stays even when one id takes the whole batch, with no atomics, in
 // an order that the offsets fix. Bound by HBM: 65,536 tokens over 131,072 rows
-// of 2048 bf16, frequencies falling as 1/rank, in 24 us of block sums and 122
+// of 2048 bf16, frequencies falling as 1/rank, in 24 us of block sums and 121
 // us of rows (707 MB; writing zeros alone takes 78).
 constexpr int kSumLevels = 3;
 constexpr int kSumLg = 4;  // 16 positions to a block, 16 blocks to a block of the next level
@@ -1010,11 +1010,24 @@ int with_type(int dtype, int64_t width, F f) {
     }
 }
 
-// One chunk to a thread, up to a workgroup to a row (a wavefront to a row, with
-// several chunks to a thread, was slower: embed 63.6 us against 61.3, combine's
-// gradient 271 against 222, dispatch 101 against 97.7); where the rows are too few
-// to fill the chip (fewer than two workgroups a compute unit), columns over
-// several workgroups (split).
+// Up to a workgroup to a row (a wavefront to a row, with four or eight chunks
+// to a thread, was slower: embed 63.6 us against 61.3, combine's gradient 271
+// against 222, dispatch 101 against 97.7). Up to 256 chunks a row gets a
+// thread a chunk, or half the threads with two chunks each, all of a row's
+// loads in flight: where the chunks fill at most `halve` eighths of the
+// threads. 40,000 rows of bf16, a table of 60,000, one chunk against two, us:
+//   chunks               65           138          192          256
+//   threads           128   64     256   128    256   128    256   128
+//   embed            17.5  14.4   28.6  27.0   39.7  36.0   49.3  47.7
+//   embed's gradient 30.7  27.5   48.3  49.0   54.8  42.8   76.1  57.8
+//   combine          28.3  23.0   49.5  45.6   61.5  58.4   79.0  79.2
+//   its gradient     60.0  43.9    116  86.5    121  97.2    144   124
+//   dispatch         26.0  27.8   50.9  55.8
+// so all rows for 8, combine up to 5/8 (9,973 x 6 rows of 182 chunks 35.5
+// against 38.7) and dispatch none. A small table's gradient stays at one (10,007
+// rows of 65 chunks 10.1 against 11.5). Where the rows are too few to fill the
+// chip (fewer than two workgroups a compute unit), columns go over several
+// workgroups (split).
 struct RowLaunch {
     RowMap map;
     dim3 grid;
@@ -1022,13 +1035,14 @@ struct RowLaunch {
     int deep;    // chunks to a thread, as 1, 2 or 4
 };
 
-RowLaunch row_launch(int64_t rows, int64_t width, int per_chunk, bool split) {
+RowLaunch row_launch(int64_t rows, int64_t width, int per_chunk, bool split, int halve) {
     RowLaunch r{};
     r.map.width = static_cast<int>(width);
     r.map.chunks = static_cast<int>((width + per_chunk - 1) / per_chunk);
     const int64_t enough = 512;
     int lg = 0;
     while (lg < 8 && (1 << lg) < r.map.chunks) ++lg;
+    if (lg > 6 && r.map.chunks <= halve << (lg - 3)) --lg;
     r.map.lg = lg;
     const int64_t blocks = (rows + (256 >> lg) - 1) >> (8 - lg);
     int64_t cols = 1;
@@ -1078,7 +1092,7 @@ int embed_impl(const void *table, int dtype, int64_t vocab, int64_t width, const
     return with_type(dtype, width, [&](auto t, auto vec) {
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
-        const RowLaunch r = row_launch(n, width, Chunk<T, V>::kN, true);
+        const RowLaunch r = row_launch(n, width, Chunk<T, V>::kN, true, 8);
         return with_shape(r, [&](auto wave, auto ch) {
             hipLaunchKernelGGL((embed_kernel<T, V, decltype(wave)::value, decltype(ch)::value, I>), r.grid,
                                dim3(kRowBlock), 0, static_cast<hipStream_t>(stream), static_cast<const T *>(table),
@@ -1144,7 +1158,7 @@ int embed_grad_impl(const void *dout, int dtype, int64_t n, int64_t width, const
             at += blocks * width;
         }
         for (int l = 0; l < sums.levels; ++l) {
-            const RowLaunch r = row_launch(n >> (kSumLg * (l + 1)), width, Chunk<T, V>::kN, true);
+            const RowLaunch r = row_launch(n >> (kSumLg * (l + 1)), width, Chunk<T, V>::kN, true, 0);
             if (r.wave)
                 hipLaunchKernelGGL((grad_blocks_kernel<T, V, true, I>), r.grid, dim3(kRowBlock), 0, s,
                                    static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
@@ -1153,7 +1167,7 @@ int embed_grad_impl(const void *dout, int dtype, int64_t n, int64_t width, const
                                    static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
             SSC_TRY(launched());
         }
-        const RowLaunch r = row_launch(vocab, width, Chunk<T, V>::kN, true);
+        const RowLaunch r = row_launch(vocab, width, Chunk<T, V>::kN, true, vocab >= 16384 ? 8 : 0);
         const auto launch = [&](auto *g) {
             using G = std::remove_pointer_t<decltype(g)>;
             return with_shape(r, [&](auto wave, auto ch) {
@@ -1239,7 +1253,7 @@ int ssc_dispatch_rows(const void *x, int dtype, int64_t tokens, int64_t per, int
     return with_type(dtype, width, [&](auto t, auto vec) {
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
-        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true);
+        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true, 0);
         return with_shape(r, [&](auto wave, auto ch) {
             hipLaunchKernelGGL((dispatch_kernel<T, V, decltype(wave)::value, decltype(ch)::value>), r.grid,
                                dim3(kRowBlock), 0, static_cast<hipStream_t>(stream), static_cast<const T *>(x),
@@ -1264,7 +1278,7 @@ int ssc_combine_rows(const void *y, int dtype, int64_t rows, int64_t width, cons
     return with_type(dtype, width, [&](auto t, auto vec) {
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
-        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true);
+        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, true, 5);
         const auto launch = [&](auto weighted) {
             return with_shape(r, [&](auto wave, auto ch) {
                 constexpr int kCh = decltype(ch)::value > 1 ? 2 : 1;
@@ -1304,7 +1318,7 @@ int ssc_combine_rows_grad(const void *dout, const void *y, int dtype, int64_t ro
     return with_type(dtype, width, [&](auto t, auto vec) {
         using T = decltype(t);
         constexpr bool V = decltype(vec)::value;
-        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, false);
+        const RowLaunch r = row_launch(tokens, width, Chunk<T, V>::kN, false, 8);
         return with_shape(r, [&](auto wave, auto ch) {
             constexpr int kCh = decltype(ch)::value > 1 ? 2 : 1;
             hipLaunchKernelGGL((combine_grad_kernel<T, V, decltype(wave)::value, kCh>), r.grid, dim3(kRowBlock), 0,
