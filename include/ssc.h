@@ -483,9 +483,10 @@ size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
  * no top_k, no top_p, no min_p. kept[r] (nullable) is the number of kept
  * tokens, logprobs[r] (nullable) the logarithm of the chosen weight over the
  * kept ones' sum. Weights are computed in fp64 and summed as fixed-point
- * integers of at least 40 fractional bits, so that neither the order of
- * a sum nor the split of a row changes a result. 1 <= vocab <= 2^22 and at
- * most 65,535 rows. */
+ * integers, so that neither the order of a sum nor the split of a row changes
+ * a result: of 62 - ceil(log2(vocab + 1)) fractional bits, at most 50, each
+ * off by half the last one, where the largest weight is 1.
+ * 1 <= vocab <= 2^22 and at most 65,535 rows. */
 int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                     const float *u, const float *temperature, const int32_t *top_k,
                     const float *top_p, const float *min_p, int32_t *tokens, int32_t *kept,

@@ -19,10 +19,11 @@
 // Launches, each over parts of rows except the last: maxima; histograms (only
 // where a filter is given; a row's last workgroup finds the border bins); sums
 // of the better bins with the border bins' logits collected; border and token.
-// 256 rows of 131,072 bf16 under mixed settings take 13 + 33 + 29 + 14 us, the
-// first bound by HBM, the second by LDS adds (29 clocks a wavefront) and the
-// border search at its end, the third by exponentials, the last by latency;
-// one such row of fp32 takes 3.4 + 9.3 + 4.8 + 10 us, latency throughout.
+// 256 rows of 131,072 bf16 under mixed settings take 13 + 35 + 29 + 14 us, the
+// first bound by HBM, the second by exponentials and 64-bit LDS adds in the rows
+// that top_p alone cuts (256 such rows 46 us, 256 of top_k 27) and the latency of
+// its steps, the third by exponentials, the last by latency; one such row of
+// fp32 takes 3.4 + 10 + 4.8 + 10 us, latency throughout.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -1,7 +1,11 @@
 """ssc_sample_rows on the GPU against the definition in 64 bits. Tokens and
-kept counts are equal; logprobs, computed in fp64, are off by the rounding to
-fp32 and by the weights' 2^-40 (the sum's relative error is below that, and
-the logarithm's absolute one with it)."""
+kept counts are equal. Logprobs are off by the rounding to fp32, half a step,
+and by the sum of the weights. A weight is at most 1 and its fp64 value off by
+7e-15 (the series' last term) and some steps of 2^-53 of itself, together
+under 2^-46; it is rounded to an integer multiple of 2^-bits, half of that off.
+The sum over V logits is 1 at least, so it is off by at most V * 2^-(bits + 1)
++ 2^-46 of itself, equal weights all the same way, and its logarithm by as
+much. The chosen weight's own logarithm is taken from the logit."""
 from __future__ import annotations
 
 import numpy as np
@@ -29,7 +33,9 @@ def _check(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
     lp = got[2].double().cpu().numpy()
     none = tokens < 0
     assert np.all(lp[none] == -np.inf)
-    tol = 2.0 ** -24 * np.abs(logprobs[~none]) + 2.0 ** -38
+    vocab = logits.shape[1]
+    bits = min(62 - vocab.bit_length(), 50)
+    tol = 2.0 ** -24 * np.abs(logprobs[~none]) + vocab * 2.0 ** -(bits + 1) + 2.0 ** -45
     assert np.all(np.abs(lp[~none] - logprobs[~none]) <= tol)
     return got
 
@@ -204,6 +210,19 @@ def test_graph_replays_and_streams():
         torch.cuda.synchronize()
         eager = _check(logits, u, t, k, p, m)
         assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_equal_small_weights(dtype):
+    """Thousands of weights that are all rounded alike, beside one of 1: the
+    logprob of the large one is as small as their sum."""
+    for vocab, low in ((131_072, -25.0), (36_917, -20.0), (4097, -30.0)):
+        logits = torch.full((2, vocab), low, device=DEV, dtype=dtype)
+        logits[0, 7] = 0.0
+        logits[1, vocab - 1] = 0.0
+        u = torch.tensor([0.5, 0.5], device=DEV)
+        _check(logits, u)
+        _check(logits, u, top_p=torch.tensor([1.0, 0.999], device=DEV))
 
 
 def test_sampled_tokens_feed_the_lookup():
