@@ -732,7 +732,7 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
     n = _need(ids, "ids", table, None, 0).numel()
     out = (table.new_empty((n, width) if ids.dim() == 1 else (*ids.shape, width)) if out is None
            else _need(out, "out", table, (table.dtype,), n * width))
-    _row_call(name, table, table, DTYPE[table.dtype], vocab, width, ids, n, scale, out)
+    _row_call(name, table, table, DTYPE[table.dtype], vocab, width, ids, n, float(scale), out)
     return out
 
 
@@ -769,7 +769,7 @@ def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, 
     if out.dtype not in (dout.dtype, torch.float32):
         raise TypeError("the gradient is of dout's dtype or float32")
     scratch = _work_bytes(scratch, dout, int(lib().ssc_embed_grad_scratch_bytes(n, width)))
-    _row_call(name, dout, dout, DTYPE[dout.dtype], n, width, ids, order, offsets, vocab, scale, out,
+    _row_call(name, dout, dout, DTYPE[dout.dtype], n, width, ids, order, offsets, vocab, float(scale), out,
               DTYPE[out.dtype], int(accumulate), scratch, _numel(scratch))
     return out
 

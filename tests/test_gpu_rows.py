@@ -409,6 +409,36 @@ def test_the_token_path_in_a_graph_and_on_a_side_stream():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("chunks,extra", [(65, 0), (80, 1), (81, 3), (128, 0), (129, 0), (160, 1), (200, 0), (256, 0), (257, 1)])
+def test_rows_by_half_the_threads(dtype, chunks, extra):
+    """Widths around those at which a row's threads take two chunks each, with
+    a last chunk that starts early; a table large enough for it too."""
+    each = 16 // torch.empty(0, dtype=dtype).element_size()
+    width = chunks * each - extra
+    g = _gen(width)
+    vocab, n = 16_400, 900
+    ids = (torch.rand(n, device=DEV, generator=g) ** 6 * (vocab + 1)).long() - 1
+    _grad_case(ids, vocab, width, dtype, 0.5, dtype, width)
+    table = _randn(g, 301, width, dtype=dtype)
+    few = ids % 300 - (ids < 0).long()
+    inside = few >= 0
+    want = torch.where(inside[:, None], table[few.clamp(min=0)], torch.zeros((), dtype=dtype, device=DEV))
+    assert torch.equal(ssc.embed_rows(table, few), want)
+    test_dispatch_combine_and_gradients(dtype, 130, 3, 5, width, 0.2)
+
+
+def test_scale_of_other_number_types():
+    table = torch.randn(9, 16, device=DEV)
+    ids = torch.tensor([3, 8, -1, 0], device=DEV)
+    want = ssc.embed_rows(table, ids, 0.5)
+    order, _, offsets = ssc.group_by_key(ids, 9)
+    dtable = ssc.embed_rows_grad(want, ids, order, offsets, 0.5)
+    for scale in (np.float32(0.5), torch.tensor(0.5), torch.tensor(0.5, device=DEV)):
+        assert torch.equal(ssc.embed_rows(table, ids, scale), want)
+        assert torch.equal(ssc.embed_rows_grad(want, ids, order, offsets, scale), dtable)
+
+
 def test_two_groupings_at_once():
     """Calls in flight on two streams, each with a scratch of its own."""
     r = np.random.RandomState(9)

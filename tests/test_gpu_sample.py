@@ -225,6 +225,27 @@ def test_equal_small_weights(dtype):
         _check(logits, u, top_p=torch.tensor([1.0, 0.999], device=DEV))
 
 
+def test_two_calls_at_once():
+    """Calls in flight on two streams, each with a scratch of its own."""
+    inputs, want = [], []
+    for i in range(2):
+        logits, u, rand = _inputs(40 + i, 24, 70_001, torch.bfloat16)
+        inputs.append((logits, u, 0.5 + rand(24), (rand(24) * 90).int(), 0.5 + 0.6 * rand(24)))
+        want.append([x.clone() for x in _check(*inputs[i])])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    scratch = [torch.empty(ssc.sample_scratch_bytes(24, 70_001), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ssc.sample_rows(*inputs[i], scratch=scratch[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
 def test_sampled_tokens_feed_the_lookup():
     """A decoding step: the sampled ids, -1 for a row without tokens, go
     straight into the embedding lookup."""
