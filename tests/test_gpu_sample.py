@@ -225,6 +225,29 @@ def test_equal_small_weights(dtype):
         _check(logits, u, top_p=torch.tensor([1.0, 0.999], device=DEV))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_largest_vocabulary(dtype):
+    vocab = 2 ** 22
+    logits, u, rand = _inputs(22, 2, vocab, dtype, 1.5)
+    _check(logits, u)
+    _check(logits, u, top_k=torch.tensor([100, 3_000_000], dtype=torch.int32, device=DEV))
+    _check(logits, u, 0.5 + rand(2), None, torch.tensor([0.3, 0.95], device=DEV), torch.tensor([0.0, 1e-4], device=DEV))
+
+
+def test_most_rows():
+    """65,535 rows, more than 2^32 logits in all, against some of the rows alone."""
+    rows, vocab = 65_535, 66_001
+    if torch.cuda.mem_get_info()[0] < 40 * 2 ** 30:
+        pytest.skip("needs 40 GB of device memory")
+    logits, u, rand = _inputs(23, rows, vocab, torch.bfloat16)
+    t, k, p = 0.5 + rand(rows), (rand(rows) * 100).int(), 0.5 + 0.6 * rand(rows)
+    tokens, kept, logprobs = ssc.sample_rows(logits, u, t, k, p)
+    some = torch.tensor([0, 1, 32_767, 65_074, 65_075, 65_533, 65_534], device=DEV)
+    got = _check(logits[some], u[some], t[some], k[some], p[some])
+    assert torch.equal(got[0], tokens[some]) and torch.equal(got[1], kept[some]) and torch.equal(got[2], logprobs[some])
+    assert bool(((tokens >= 0) & (tokens < vocab)).all())
+
+
 def test_two_calls_at_once():
     """Calls in flight on two streams, each with a scratch of its own."""
     inputs, want = [], []
