@@ -99,14 +99,24 @@ struct Filters {
     float t;        // temperature; 0: the first of the order alone
     float top_p;    // 2: off
     int32_t top_k;  // 0: off
+    float min_p, u;
 
+    // u stands in for a setting that is not given, so that no load waits
+    // behind a branch and all are in flight together
     __device__ __forceinline__ Filters(const SampleArgs &a, int row) {
-        t = a.temperature != nullptr ? a.temperature[row] : 1.0f;
+        const auto at = [&](const void *p) {
+            return reinterpret_cast<const uint32_t *>(p != nullptr ? p : a.u)[row];
+        };
+        const uint32_t bits_t = at(a.temperature), bits_k = at(a.top_k), bits_p = at(a.top_p), bits_m = at(a.min_p),
+                       bits_u = at(a.u);
+        t = a.temperature != nullptr ? __uint_as_float(bits_t) : 1.0f;
+        min_p = a.min_p != nullptr ? __uint_as_float(bits_m) : 0.0f;
+        u = __uint_as_float(bits_u);
         const bool greedy = !(t > 0.0f);
         if (greedy) t = 0.0f;
-        const int32_t k = a.top_k != nullptr ? a.top_k[row] : 0;
+        const int32_t k = a.top_k != nullptr ? static_cast<int32_t>(bits_k) : 0;
         top_k = greedy ? 1 : (k < 1 || k >= a.vocab ? 0 : k);
-        const float p = a.top_p != nullptr ? a.top_p[row] : 2.0f;
+        const float p = a.top_p != nullptr ? __uint_as_float(bits_p) : 2.0f;
         top_p = greedy || !(p < 1.0f) ? 2.0f : p;
         if (top_p <= 0.0f) top_k = 1;
         if (top_k == 1) top_p = 2.0f;
@@ -135,14 +145,14 @@ struct Scale {
     int bits;
     bool lift;
 
-    __device__ __forceinline__ Scale(const SampleArgs &a, int row, const Filters &f, float2 range) {
+    __device__ __forceinline__ Scale(const SampleArgs &a, const Filters &f, float2 range) {
         lift = range.x == __builtin_inff();
         top = lift ? 0.0f : range.x;
         max = static_cast<double>(top);
         const double t = f.t > 0.0f ? static_cast<double>(f.t) : 1.0;
         rate = 1.4426950408889634 / t;
         bits = a.bits;
-        const float mp = a.min_p != nullptr ? a.min_p[row] : 0.0f;
+        const float mp = f.min_p;
         min_w = ldexp(mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0), bits);
         // the bins span the row, or as far down as weights matter
         const float span = lift ? 0.0f : fminf(fminf(top - range.y, 64.0f * static_cast<float>(t)), 0x1.fffffep127f);
@@ -229,28 +239,47 @@ __device__ __forceinline__ const T *row_at(const SampleArgs &a, int row) {
     return static_cast<const T *>(a.logits) + static_cast<int64_t>(row) * a.stride;
 }
 
-__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(static_cast<unsigned long long>(v), off);
-    return v;
-}
-__device__ __forceinline__ uint32_t wave_sum32(uint32_t v) {
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
-__device__ __forceinline__ float2 wave_range(float2 r) {
-    for (int off = 32; off > 0; off >>= 1) {
-        r.x = fmaxf(r.x, __shfl_xor(r.x, off));
-        r.y = fminf(r.y, __shfl_xor(r.y, off));
-    }
-    return r;
+// Across a wavefront, all of whose lanes are active, by DPP as
+// wave_inclusive_scan does it: shuffles through LDS took four times as long.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ uint64_t dpp_move64(uint64_t v) {
+    return static_cast<uint64_t>(dpp_move<CTRL, ROW_MASK>(static_cast<uint32_t>(v >> 32))) << 32 |
+           dpp_move<CTRL, ROW_MASK>(static_cast<uint32_t>(v));
 }
 __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
-    const int lane = lane_id();
-    for (int off = 1; off < kWave; off <<= 1) {
-        const uint64_t o = __shfl_up(static_cast<unsigned long long>(v), off);
-        v += lane >= off ? o : 0;
-    }
+    v += dpp_move64<0x111, 0xf>(v);
+    v += dpp_move64<0x112, 0xf>(v);
+    v += dpp_move64<0x114, 0xf>(v);
+    v += dpp_move64<0x118, 0xf>(v);
+    v += dpp_move64<0x142, 0xa>(v);
+    v += dpp_move64<0x143, 0xc>(v);
     return v;
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), kWave - 1));
+}
+__device__ __forceinline__ uint64_t last_lane64(uint64_t v) {
+    return static_cast<uint64_t>(last_lane(static_cast<uint32_t>(v >> 32))) << 32 | last_lane(static_cast<uint32_t>(v));
+}
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) { return last_lane64(wave_scan64(v)); }
+__device__ __forceinline__ uint32_t wave_sum32(uint32_t v) { return last_lane(wave_inclusive_scan<SumU32>(v)); }
+// a lane without a source keeps its own
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float2 range_step(float2 r) {
+    const auto from = [](float v) {
+        const int own = __float_as_int(v);
+        return __int_as_float(__builtin_amdgcn_update_dpp(own, own, CTRL, ROW_MASK, 0xf, false));
+    };
+    return {fmaxf(r.x, from(r.x)), fminf(r.y, from(r.y))};
+}
+__device__ __forceinline__ float2 wave_range(float2 r) {
+    r = range_step<0x111, 0xf>(r);
+    r = range_step<0x112, 0xf>(r);
+    r = range_step<0x114, 0xf>(r);
+    r = range_step<0x118, 0xf>(r);
+    r = range_step<0x142, 0xa>(r);
+    r = range_step<0x143, 0xc>(r);
+    return {__uint_as_float(last_lane(__float_as_uint(r.x))), __uint_as_float(last_lane(__float_as_uint(r.y)))};
 }
 
 // Largest and smallest token logit of a row, by every wavefront for itself;
@@ -262,10 +291,7 @@ __device__ __forceinline__ float2 row_range(const SampleArgs &a, int row) {
         r.x = fmaxf(r.x, v.x);
         r.y = fminf(r.y, v.y);
     }
-    r = wave_range(r);
-    r.x = __uint_as_float(uniform(__float_as_uint(r.x)));
-    r.y = __uint_as_float(uniform(__float_as_uint(r.y)));
-    return r;
+    return wave_range(r);
 }
 
 // ---- range of each part; clears the rows' histograms and sets their state ----
@@ -408,7 +434,7 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     const int row = blockIdx.y;
     const Filters f(a, row);
     if (!f.searched()) return;
-    const Scale sc(a, row, f, row_range(a, row));
+    const Scale sc(a, f, row_range(a, row));
     for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
         h.mass[b] = 0;
         h.count[b] = 0;
@@ -462,9 +488,9 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
             reinterpret_cast<unsigned long long *>(a.hist_mass) + static_cast<int64_t>(row) * kBins;
         uint32_t *gc = a.hist_count + static_cast<int64_t>(row) * kBins;
         for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
-            if (h.count[b] != 0)
+            if (counts && h.count[b] != 0)
                 __hip_atomic_fetch_add(gc + b, h.count[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (h.mass[b] != 0)
+            if (masses && h.mass[b] != 0)
                 __hip_atomic_fetch_add(gm + b, h.mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         // The workgroup that adds last finds the border bins. Everything it
@@ -480,9 +506,22 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
                      gridDim.x - 1;
         __syncthreads();
         if (!s_last) return;
-        for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
-            h.count[b] = __hip_atomic_load(gc + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            h.mass[b] = __hip_atomic_load(gm + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // all loads in flight before the first is used: one after another
+        // they took 2 us
+        constexpr int kEach = kBins / kHistBlock;
+        uint32_t c[kEach];
+        unsigned long long m[kEach];
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) {
+            const int b = s * kHistBlock + static_cast<int>(threadIdx.x);
+            c[s] = counts ? __hip_atomic_load(gc + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+            m[s] = masses ? __hip_atomic_load(gm + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+        }
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) {
+            const int b = s * kHistBlock + static_cast<int>(threadIdx.x);
+            h.count[b] = c[s];
+            h.mass[b] = m[s];
         }
         __syncthreads();
     }
@@ -574,7 +613,7 @@ __global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
     using L = Logits<T>;
     constexpr int kEach = kPartItems / L::kN;
     const Filters f(a, row);
-    const Scale sc(a, row, f, row_range(a, row));
+    const Scale sc(a, f, row_range(a, row));
     RowState *st = a.state + row;
     const int lo = st->lo, hi = st->hi, extra = st->extra;
     // No logit below `least` is kept or collected: those that are lie above
@@ -972,7 +1011,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         }
         return;
     }
-    const Scale sc(a, row, f, range);
+    const Scale sc(a, f, range);
     const T *x = row_at<T>(a, row);
     Border border{1u, kNoCut};
     if (has_part) sh.mass[threadIdx.x] = part_mass;
@@ -1036,8 +1075,13 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
                 mine += sc.bin(xe) <= st.hi ? 1u : 0u;
             }
         }
-        const uint64_t mi = wave_scan64(ms);
-        mine = wave_sum32(mine);
+        // wavefronts without entries leave the work to the others
+        const bool busy = w * kWave * kEach < n;
+        uint64_t mi = 0;
+        if (busy) {
+            mi = wave_scan64(ms);
+            mine = wave_sum32(mine);
+        }
         if (lane == kWave - 1) {
             sh.find.wave_mass[w] = mi;
             sh.find.wave_count[w] = mine;
@@ -1067,13 +1111,15 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             }
         }
         // running sums at skip and end, by the threads that hold the entries before them
-        uint64_t at = run;
+        if (busy) {
+            uint64_t at = run;
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const uint32_t i = threadIdx.x * kEach + q + 1;
-            at += we[q];
-            if (i == skip) sh.at_skip = at;
-            if (i == end) sh.at_end = at;
+            for (int q = 0; q < kEach; ++q) {
+                const uint32_t i = threadIdx.x * kEach + q + 1;
+                at += we[q];
+                if (i == skip) sh.at_skip = at;
+                if (i == end) sh.at_end = at;
+            }
         }
         if (threadIdx.x == 0) {
             if (skip == 0) sh.at_skip = 0;
@@ -1084,7 +1130,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         const uint64_t all = st.total != 0 ? st.total : from + (sh.at_end - sh.at_skip);
         const double target = f.nucleus() ? static_cast<double>(f.top_p) * static_cast<double>(all) : __builtin_inf();
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
+        for (int q = 0; busy && q < kEach; ++q) {
             const uint32_t i = threadIdx.x * kEach + q;
             const bool keep = i < nk && static_cast<double>(st.mass + run) < target;
             run += we[q];
@@ -1103,16 +1149,16 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         border = sh.border;
     }
     // the part in which the running weight passes the goal
-    count = wave_sum32(count);
-    if (lane == 0 && count != 0)
-        __hip_atomic_fetch_add(&sh.count, count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    if (ballot(count != 0) != 0) {
+        count = wave_sum32(count);
+        if (lane == 0) __hip_atomic_fetch_add(&sh.count, count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
     __syncthreads();
     if (w == 0) {
         uint64_t total = 0;
         for (int p = lane; p < a.parts; p += kWave) total += sh.mass[p];
         total = wave_sum64(total);
-        float u = a.u[row];
-        u = u > 0.0f ? u : 0.0f;
+        float u = f.u > 0.0f ? f.u : 0.0f;
         u = u < 0x1.fffffep-1f ? u : 0x1.fffffep-1f;
         const uint64_t goal = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         uint64_t before = 0;
@@ -1129,7 +1175,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
                 }
                 break;
             }
-            before += __shfl(static_cast<unsigned long long>(incl), kWave - 1);
+            before += last_lane64(incl);
         }
         if (lane == 0 && a.kept != nullptr) a.kept[row] = static_cast<int32_t>(sh.count);
     }
