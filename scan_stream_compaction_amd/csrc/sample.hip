@@ -58,6 +58,7 @@ struct RowState {
     uint64_t mass;        // weight of the bins below lo ...
     uint64_t extra_mass;  // ... and below extra
     uint64_t total;       // of the row, where top_p alone cuts it; else 0
+    double rate;          // log2(e) / temperature, divided once
     uint32_t count, extra_count;  // their logits
     int32_t lo, hi, extra;        // extra: top_k's border bin, where top_p's lies before it (-1: none)
     uint32_t listed;      // logits collected so far (may pass kList: the list is then not used)
@@ -145,17 +146,16 @@ struct Scale {
     int bits;
     bool lift;
 
-    __device__ __forceinline__ Scale(const SampleArgs &a, const Filters &f, float2 range) {
+    __device__ __forceinline__ Scale(const SampleArgs &a, const Filters &f, double rate, float2 range) : rate(rate) {
         lift = range.x == __builtin_inff();
         top = lift ? 0.0f : range.x;
         max = static_cast<double>(top);
-        const double t = f.t > 0.0f ? static_cast<double>(f.t) : 1.0;
-        rate = 1.4426950408889634 / t;
+        const float t = f.t > 0.0f ? f.t : 1.0f;
         bits = a.bits;
         const float mp = f.min_p;
         min_w = ldexp(mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0), bits);
         // the bins span the row, or as far down as weights matter
-        const float span = lift ? 0.0f : fminf(fminf(top - range.y, 64.0f * static_cast<float>(t)), 0x1.fffffep127f);
+        const float span = lift ? 0.0f : fminf(fminf(top - range.y, 64.0f * t), 0x1.fffffep127f);
         width = span > 0.0f ? fminf((kBins - 1) / span, 0x1p100f) : 0.0f;
     }
     // A token's logit on the axis of the bins: bin b is [b, b + 1), the last
@@ -263,6 +263,32 @@ __device__ __forceinline__ uint64_t last_lane64(uint64_t v) {
 }
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) { return last_lane64(wave_scan64(v)); }
 __device__ __forceinline__ uint32_t wave_sum32(uint32_t v) { return last_lane(wave_inclusive_scan<SumU32>(v)); }
+// Of a workgroup's wavefront totals (up to 16, in LDS): the sum of those before
+// wavefront w, and of all. A lane a total, for a loop over them would be read
+// by every wavefront, one after another (1 us with sixteen).
+template <int WAVES>
+__device__ __forceinline__ uint64_t sum_before64(const unsigned long long *totals, int w, uint64_t &all) {
+    const int lane = lane_id();
+    uint64_t v = lane < WAVES ? totals[lane] : 0;
+    v += dpp_move64<0x111, 0xf>(v);
+    v += dpp_move64<0x112, 0xf>(v);
+    v += dpp_move64<0x114, 0xf>(v);
+    v += dpp_move64<0x118, 0xf>(v);
+    const auto at = [&](int l) {
+        return static_cast<uint64_t>(static_cast<uint32_t>(
+                   __builtin_amdgcn_readlane(static_cast<int>(v >> 32), l))) << 32 |
+               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
+    };
+    all = at(WAVES - 1);
+    return w == 0 ? 0 : at(w - 1);
+}
+template <int WAVES>
+__device__ __forceinline__ uint32_t sum_before32(const uint32_t *totals, int w, uint32_t &all) {
+    const int lane = lane_id();
+    const uint32_t v = wave_inclusive_scan<SumU32>(lane < WAVES ? totals[lane] : 0u);
+    all = last_lane(v);
+    return w == 0 ? 0 : static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), w - 1));
+}
 // a lane without a source keeps its own
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ float2 range_step(float2 r) {
@@ -311,6 +337,7 @@ __global__ __launch_bounds__(kPartBlock) void sample_max_kernel(SampleArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         RowState s{};
         s.extra = -1;
+        s.rate = 1.4426950408889634 / (f.t > 0.0f ? static_cast<double>(f.t) : 1.0);
         if (f.top_k == 1) {  // the first of the order is in bin 0
             s.lo = s.hi = 0;
         } else {             // everything is kept, unless the histogram says otherwise
@@ -407,10 +434,11 @@ __device__ __forceinline__ void find_bins(const Hist &h, FindShared<BLOCK> &sh, 
     __syncthreads();
     uint32_t cr = before + ci - cs;
     uint64_t mr = before_mass + mi - ms;
-    for (int i = 0; i < w; ++i) {
-        cr += sh.wave_count[i];
-        mr += sh.wave_mass[i];
-    }
+    constexpr int kWaves = BLOCK / kWave;
+    uint32_t all_count;
+    uint64_t all_mass;
+    cr += sum_before32<kWaves>(sh.wave_count, w, all_count);
+    mr += sum_before64<kWaves>(sh.wave_mass, w, all_mass);
 #pragma unroll
     for (int s = 0; s < kEach; ++s) {
         const int b = static_cast<int>(threadIdx.x) * kEach + s;
@@ -434,7 +462,7 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
     const int row = blockIdx.y;
     const Filters f(a, row);
     if (!f.searched()) return;
-    const Scale sc(a, f, row_range(a, row));
+    const Scale sc(a, f, a.state[row].rate, row_range(a, row));
     for (int b = threadIdx.x; b < kBins; b += kHistBlock) {
         h.mass[b] = 0;
         h.count[b] = 0;
@@ -538,12 +566,8 @@ __global__ __launch_bounds__(kHistBlock) void sample_hist_kernel(SampleArgs a) {
         sh.wave_mass[threadIdx.x / kWave] = total;
     }
     __syncthreads();
-    n = 0;
-    total = 0;
-    for (int i = 0; i < kHistBlock / kWave; ++i) {
-        n += sh.wave_count[i];
-        total += sh.wave_mass[i];
-    }
+    sum_before32<kHistBlock / kWave>(sh.wave_count, 0, n);
+    sum_before64<kHistBlock / kWave>(sh.wave_mass, 0, total);
     __syncthreads();
     RowState *s = a.state + row;
     const uint32_t k = static_cast<uint32_t>(f.top_k);
@@ -613,7 +637,7 @@ __global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
     using L = Logits<T>;
     constexpr int kEach = kPartItems / L::kN;
     const Filters f(a, row);
-    const Scale sc(a, f, row_range(a, row));
+    const Scale sc(a, f, a.state[row].rate, row_range(a, row));
     RowState *st = a.state + row;
     const int lo = st->lo, hi = st->hi, extra = st->extra;
     // No logit below `least` is kept or collected: those that are lie above
@@ -1011,7 +1035,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         }
         return;
     }
-    const Scale sc(a, f, range);
+    const Scale sc(a, f, st.rate, range);
     const T *x = row_at<T>(a, row);
     Border border{1u, kNoCut};
     if (has_part) sh.mass[threadIdx.x] = part_mass;
@@ -1056,17 +1080,18 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         // each thread's consecutive entries, their weights and the running
         // sum; n1 of all entries lie in [lo, hi], the rest in the extra bin
         constexpr int kEach = kList / kTokenBlock;
+        const int each = n <= kTokenBlock ? 1 : kEach;
         unsigned long long entry[kEach];
         uint64_t we[kEach], ms = 0;
         double full[kEach];
         uint32_t mine = 0;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
-            const int i = static_cast<int>(threadIdx.x) * kEach + q;
+            const int i = static_cast<int>(threadIdx.x) * each + q;
             entry[q] = 0;
             full[q] = 0.0;
             we[q] = 0;
-            if (i < n) {
+            if (q < each && i < n) {
                 entry[q] = sorted[i];
                 const float xe = value_of(static_cast<uint32_t>(entry[q] >> 32));
                 full[q] = sc.scaled(xe);
@@ -1076,7 +1101,7 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             }
         }
         // wavefronts without entries leave the work to the others
-        const bool busy = w * kWave * kEach < n;
+        const bool busy = w * kWave * each < n;
         uint64_t mi = 0;
         if (busy) {
             mi = wave_scan64(ms);
@@ -1087,12 +1112,10 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             sh.find.wave_count[w] = mine;
         }
         __syncthreads();
-        uint64_t run = mi - ms;
-        uint32_t n1 = 0;
-        for (int i = 0; i < kWaves; ++i) {
-            run += i < w ? sh.find.wave_mass[i] : 0;
-            n1 += sh.find.wave_count[i];
-        }
+        uint64_t run = mi - ms, all_mass;
+        uint32_t n1;
+        run += sum_before64<kWaves>(sh.find.wave_mass, w, all_mass);
+        sum_before32<kWaves>(sh.find.wave_count, 0, n1);
         // nk: the entries of [lo, hi] that top_k leaves; the first top_k end
         // before entry `end`, and their weight is `from` and that of the
         // entries from `skip` on
@@ -1115,10 +1138,10 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
             uint64_t at = run;
 #pragma unroll
             for (int q = 0; q < kEach; ++q) {
-                const uint32_t i = threadIdx.x * kEach + q + 1;
+                const uint32_t i = threadIdx.x * each + q + 1;
                 at += we[q];
-                if (i == skip) sh.at_skip = at;
-                if (i == end) sh.at_end = at;
+                if (q < each && i == skip) sh.at_skip = at;
+                if (q < each && i == end) sh.at_end = at;
             }
         }
         if (threadIdx.x == 0) {
@@ -1130,8 +1153,9 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
         const uint64_t all = st.total != 0 ? st.total : from + (sh.at_end - sh.at_skip);
         const double target = f.nucleus() ? static_cast<double>(f.top_p) * static_cast<double>(all) : __builtin_inf();
 #pragma unroll
-        for (int q = 0; busy && q < kEach; ++q) {
-            const uint32_t i = threadIdx.x * kEach + q;
+        for (int q = 0; q < kEach; ++q) {
+            if (!busy || q >= each) continue;
+            const uint32_t i = threadIdx.x * each + q;
             const bool keep = i < nk && static_cast<double>(st.mass + run) < target;
             run += we[q];
             if (!keep) continue;
@@ -1197,8 +1221,9 @@ __global__ __launch_bounds__(kTokenBlock) void sample_token_kernel(SampleArgs a)
     const uint64_t incl = wave_scan64(ms);
     if (lane == kWave - 1) sh.find.wave_mass[w] = incl;
     __syncthreads();
-    uint64_t run = incl - ms;
-    for (int i = 0; i < w; ++i) run += sh.find.wave_mass[i];
+    uint64_t all_mass;
+    const uint64_t before = sum_before64<kWaves>(sh.find.wave_mass, w, all_mass);
+    uint64_t run = before + incl - ms;
     if (run <= goal && run + ms > goal) {
         int at = -1;
         float chosen = 0.0f;
