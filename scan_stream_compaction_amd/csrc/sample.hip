@@ -19,11 +19,13 @@
 // Launches, each over parts of rows except the last: maxima; histograms (only
 // where a filter is given; a row's last workgroup finds the border bins); sums
 // of the better bins with the border bins' logits collected; border and token.
-// 256 rows of 131,072 bf16 under mixed settings take 13 + 35 + 29 + 14 us, the
+// 256 rows of 131,072 bf16 under mixed settings take 12 + 32 + 28 + 11 us, the
 // first bound by HBM, the second by exponentials and 64-bit LDS adds in the rows
-// that top_p alone cuts (256 such rows 46 us, 256 of top_k 27) and the latency of
+// that top_p alone cuts (256 such rows 43 us, 256 of top_k 23) and the latency of
 // its steps, the third by exponentials, the last by latency; one such row of
-// fp32 takes 3.4 + 10 + 4.8 + 10 us, latency throughout.
+// fp32 takes 3.0 + 7.6 + 4.4 + 7.6 us, latency throughout: as one compute unit
+// runs a row's histogram end and its token, an instruction of every wavefront
+// counts there, and a load that waits for another counts twice.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1359,10 +1361,10 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
     // or parts are of 8192 logits, and into parts of at most 32,768 in any
     // case, since rows differ in work. bf16, top_k of 50, top_p of 0.9, us:
     //   part                1 x 131,072   64 x 131,072   256 x 131,072   1 x 4,194,304
-    //   4096                10.3, 12.2    26.8, 40.9     104, 139        34, 40
-    //   8192                10.3, 12.0    18.6, 31.1     55, 76          23, 26
-    //   16,384              11.8, 13.6    13.8, 20.2     36, 55          19, 23
-    //   32,768              12.1, 17.3    13.9, 21.0     28, 48          18, 23
+    //   4096                7.7, 9.2      21.1, 34.6     75, 119         33, 38
+    //   8192                7.7, 9.2      15.3, 23.2     41, 65          21, 25
+    //   16,384              8.5, 11.2     11.9, 18.0     28, 49          17, 21
+    //   32,768              9.1, 14.7     11.0, 18.8     23, 44          16, 22
     const bool searched = top_k != nullptr || top_p != nullptr;
     a.splits = 1;
     if (searched) {
