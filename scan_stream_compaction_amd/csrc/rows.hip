@@ -48,13 +48,13 @@ __device__ __forceinline__ uint32_t key_of(K k, uint32_t groups) {
     return k >= 0 && static_cast<uint64_t>(k) < groups ? static_cast<uint32_t>(k) : groups;
 }
 
-// Ranks of `items` (at most ITEMS) consecutive sets of 64 keys among the keys
+// Ranks of ITEMS consecutive sets of 64 keys among the keys
 // this wavefront has seen, in order; cnt holds the wavefront's counts. The
 // lanes' masks do not depend on one another and come first; the counts then
 // follow key order.
 template <int ITEMS>
-__device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bool (&valid)[ITEMS], int items,
-                                            int bits, uint32_t *cnt, uint32_t (&rk)[ITEMS]) {
+__device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bool (&valid)[ITEMS], int bits,
+                                            uint32_t *cnt, uint32_t (&rk)[ITEMS]) {
     uint32_t lo[ITEMS], hi[ITEMS];
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
@@ -67,7 +67,6 @@ __device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bo
         if (b >= bits) continue;
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            if (j >= items) continue;
             const uint32_t bit = static_cast<uint32_t>(static_cast<int32_t>(d[j] << (31 - b)) >> 31);  // 0 or all ones
             const uint64_t bb = ballot(bit != 0);
             lo[j] &= ~(static_cast<uint32_t>(bb) ^ bit);
@@ -76,7 +75,6 @@ __device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bo
     }
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
-        if (j >= items) continue;
         const uint32_t below = __builtin_amdgcn_mbcnt_hi(hi[j], __builtin_amdgcn_mbcnt_lo(lo[j], 0u));
         const uint32_t same = static_cast<uint32_t>(__builtin_popcount(lo[j]) + __builtin_popcount(hi[j]));
         uint32_t run = 0;
@@ -131,10 +129,12 @@ __device__ __forceinline__ uint32_t keys_below(const uint32_t *sorted, uint32_t 
 }
 
 // Up to 8192 keys: one workgroup holds (key, position) in registers and
-// exchanges them through LDS between passes. Bound by the latency of its LDS
-// steps: 128 keys of 128 groups 3.1 us, 5000 keys in two passes 11. One launch
-// beats the tiled form's two (four) up to here: 8000 keys of 64 groups 10.4 us
-// a call against 15.3, of 10,007 groups 23 against 27.
+// exchanges them through LDS between passes. Bound by the instructions of its
+// ranks (half of a pass) and the latency of its LDS steps: 128 keys of 128
+// groups 2.7 us, 5000 keys in two passes 9.5 (11.4 with the number of sets
+// known at run time only). One launch beats the tiled form's two (four) up to
+// here: 8000 keys of 64 groups 10.4 us a call against 15.3, of 10,007 groups 23
+// against 27.
 template <class K, int ITEMS>
 __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
     const K *__restrict__ keys, uint32_t n, uint32_t groups, int passes, int bits,
@@ -148,15 +148,13 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t digits = 1u << bits;
-    // as few keys to a wavefront as all sixteen leave it
-    const int items = static_cast<int>((n + kGroupBlock - 1) / kGroupBlock);
-    const uint32_t first = static_cast<uint32_t>(w * kWave * items + lane);
+    const uint32_t first = static_cast<uint32_t>(w * kWave * ITEMS + lane);
     uint32_t key[ITEMS], pos[ITEMS], rk[ITEMS];
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         const uint32_t i = first + j * kWave;
         pos[j] = i;
-        key[j] = j < items && i < n ? key_of(keys[i], groups) : 0u;
+        key[j] = i < n ? key_of(keys[i], groups) : 0u;
     }
     for (int p = 0; p < passes; ++p) {
         const int shift = p * bits;
@@ -168,9 +166,9 @@ __global__ __launch_bounds__(kGroupBlock) void group_small_kernel(
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
             dig[j] = (key[j] >> shift) & (digits - 1);
-            valid[j] = j < items && first + j * kWave < n;
+            valid[j] = first + j * kWave < n;
         }
-        digit_ranks<ITEMS>(dig, valid, items, bits, s_cnt[w], rk);
+        digit_ranks<ITEMS>(dig, valid, bits, s_cnt[w], rk);
         __syncthreads();
         const uint32_t total = counts_before(s_cnt, digits);
         const uint32_t start = block_exclusive(total, s_wave);
@@ -329,7 +327,7 @@ __global__ __launch_bounds__(kGroupBlock) void group_scatter_kernel(
             dig[j] = (key[j] >> shift) & (digits - 1);
             valid[j] = first + j * kWave < end;
         }
-        digit_ranks<ITEMS>(dig, valid, ITEMS, bits, s_cnt[w], rk);
+        digit_ranks<ITEMS>(dig, valid, bits, s_cnt[w], rk);
         __syncthreads();
         const uint32_t count = counts_before(s_cnt, digits);
         __syncthreads();
@@ -929,12 +927,17 @@ int launch_small(const K *keys, uint32_t n, uint32_t groups, const GroupPlan &p,
                            groups, p.passes, p.bits, order, ranks, offsets, sorted);
         return launched();
     };
-    if (n <= kGroupBlock)
-        SSC_TRY(launch(std::integral_constant<int, 1>{}));
-    else if (n <= 4 * kGroupBlock)
-        SSC_TRY(launch(std::integral_constant<int, 4>{}));
-    else
-        SSC_TRY(launch(std::integral_constant<int, 8>{}));
+    // as few keys to a wavefront as all sixteen leave it, known to the compiler
+    switch ((n + kGroupBlock - 1) / kGroupBlock) {
+    case 1: SSC_TRY(launch(std::integral_constant<int, 1>{})); break;
+    case 2: SSC_TRY(launch(std::integral_constant<int, 2>{})); break;
+    case 3: SSC_TRY(launch(std::integral_constant<int, 3>{})); break;
+    case 4: SSC_TRY(launch(std::integral_constant<int, 4>{})); break;
+    case 5: SSC_TRY(launch(std::integral_constant<int, 5>{})); break;
+    case 6: SSC_TRY(launch(std::integral_constant<int, 6>{})); break;
+    case 7: SSC_TRY(launch(std::integral_constant<int, 7>{})); break;
+    default: SSC_TRY(launch(std::integral_constant<int, 8>{})); break;
+    }
     return sorted != nullptr ? launch_offsets(sorted, n, groups, offsets, s) : SSC_OK;
 }
 

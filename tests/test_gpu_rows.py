@@ -92,6 +92,14 @@ def test_group_by_key(n, groups):
     _check_group(keys, groups)
 
 
+@pytest.mark.parametrize("groups", [37, 5000])
+@pytest.mark.parametrize("n", [1500, 2048, 2049, 2900, 3500, 4999, 5121, 6144, 6145, 7168, 7169])
+def test_group_one_workgroup(n, groups):
+    """Each number of sets of 64 keys that a wavefront of the one workgroup holds."""
+    r = np.random.RandomState(n + groups)
+    _check_group(r.randint(-1, groups + 1, n).astype(np.int64), groups)
+
+
 @pytest.mark.parametrize("n", [70, 1500, 9000, 50_000])
 @pytest.mark.parametrize("groups", [3, 600, 300_000, 5_000_000, 2 ** 27 + 5])
 def test_group_many_passes_and_odd_keys(n, groups):
