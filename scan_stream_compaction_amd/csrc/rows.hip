@@ -21,6 +21,7 @@
 #include "ssc.h"
 #include "ssc_device.h"
 #include "ssc_host.h"
+#include "ssc_sets.h"
 
 namespace ssc {
 namespace {
@@ -563,23 +564,23 @@ __global__ __launch_bounds__(kRowBlock) void combine_kernel(const T *__restrict_
 #pragma unroll
             for (int e = 0; e < C::kN; ++e) acc[q][e] = 0.0f;
         }
-        for (int k0 = 0; rows > 0 && k0 < per; k0 += K) {
+        for (Sets<K> k(rows > 0 ? per : 0); k.more(); k.next()) {
             typename C::Raw r[K][CH];
             float w[K];
             bool ok[K];
 #pragma unroll
             for (int j = 0; j < K; ++j) {
-                if (k0 + j >= per) continue;
-                const int64_t slot = rk[k0 + j];
+                if (!k.has(j)) continue;
+                const int64_t slot = rk[k.at(j)];
                 ok[j] = slot >= 0 && slot < rows;
-                w[j] = WEIGHTED ? wt[k0 + j] : 1.0f;
+                w[j] = WEIGHTED ? wt[k.at(j)] : 1.0f;
                 const T *src = y + (ok[j] ? slot : 0) * m.width;
 #pragma unroll
                 for (int q = 0; q < CH; ++q) r[j][q] = C::load_stream(src + chunk_start<C::kN>(c0 + q * step, m));
             }
 #pragma unroll
             for (int j = 0; j < K; ++j) {
-                if (k0 + j >= per || !ok[j]) continue;
+                if (!k.has(j) || !ok[j]) continue;
 #pragma unroll
                 for (int q = 0; q < CH; ++q) {
                     float v[C::kN];
@@ -628,7 +629,7 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
     const float *wt = weights + t * per;
     const T *src = dout + t * m.width;
     const int step = col_step(m);
-    for (int k0 = 0; k0 < per; k0 += K) {
+    for (Sets<K> k(per); k.more(); k.next()) {
         float dot[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) dot[j] = 0.0f;
@@ -639,8 +640,8 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
                 for (int q = 0; q < CH; ++q) dr[q] = C::load(src + chunk_start<N>(c0 + q * step, m));
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
-                    if (k0 + j >= per) continue;
-                    const int64_t slot = rk[k0 + j];
+                    if (!k.has(j)) continue;
+                    const int64_t slot = rk[k.at(j)];
                     const T *from = y + (slot >= 0 && slot < rows ? slot : 0) * m.width;
 #pragma unroll
                     for (int q = 0; q < CH; ++q) r[j][q] = C::load_stream(from + chunk_start<N>(c0 + q * step, m));
@@ -657,10 +658,10 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
                     for (int e = 0; e < N; ++e) own[e] = e >= skip ? d[e] : 0.0f;
 #pragma unroll
                     for (int j = 0; j < K; ++j) {
-                        if (k0 + j >= per) continue;
-                        const int64_t slot = rk[k0 + j];
+                        if (!k.has(j)) continue;
+                        const int64_t slot = rk[k.at(j)];
                         if (slot < 0 || slot >= rows) continue;
-                        const float w = wt[k0 + j];
+                        const float w = wt[k.at(j)];
                         float v[N], g[N];
                         C::unpack(r[j][q], v);
 #pragma unroll
@@ -675,9 +676,9 @@ __global__ __launch_bounds__(kRowBlock) void combine_grad_kernel(
         }
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            if (k0 + j >= per) continue;  // the same in every thread
+            if (!k.has(j)) continue;  // the same in every thread
             const float s = row_sum(dot[j], m.lg, s_wave);
-            if (row < tokens && (threadIdx.x & ((1u << m.lg) - 1u)) == 0) dweights[t * per + k0 + j] = s;
+            if (row < tokens && (threadIdx.x & ((1u << m.lg) - 1u)) == 0) dweights[t * per + k.at(j)] = s;
         }
     }
 }
