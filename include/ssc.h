@@ -478,7 +478,8 @@ size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
  * other is (those of +infinity weigh the same). A row with no token gives
  * tokens[r] = -1, kept[r] = 0, logprobs[r] = -infinity. A u outside [0, 1) is
  * taken as the nearest end (NaN as 0), a top_p of NaN as 1, of 0 or less as one
- * that keeps the first only, a min_p of NaN as 0.
+ * that keeps the first only, a min_p of NaN as 0. No weight reaches a min_p
+ * above 1, which so keeps the first only, too.
  * The settings are arrays of one value a row, each nullable: temperature 1,
  * no top_k, no top_p, no min_p. kept[r] (nullable) is the number of kept
  * tokens, logprobs[r] (nullable) the logarithm of the chosen weight over the

@@ -118,7 +118,8 @@ struct Filters {
         const bool greedy = !(t > 0.0f);
         if (greedy) t = 0.0f;
         const int32_t k = a.top_k != nullptr ? static_cast<int32_t>(bits_k) : 0;
-        top_k = greedy ? 1 : (k < 1 || k >= a.vocab ? 0 : k);
+        // no weight reaches a min_p above 1: the first of the order alone
+        top_k = greedy || min_p > 1.0f ? 1 : (k < 1 || k >= a.vocab ? 0 : k);
         const float p = a.top_p != nullptr ? __uint_as_float(bits_p) : 2.0f;
         top_p = greedy || !(p < 1.0f) ? 2.0f : p;
         if (top_p <= 0.0f) top_k = 1;
@@ -154,8 +155,7 @@ struct Scale {
         max = static_cast<double>(top);
         const float t = f.t > 0.0f ? f.t : 1.0f;
         bits = a.bits;
-        const float mp = f.min_p;
-        min_w = ldexp(mp > 1.0f ? 1.0 : (mp > 0.0f ? static_cast<double>(mp) : 0.0), bits);
+        min_w = ldexp(f.min_p > 0.0f ? static_cast<double>(f.min_p) : 0.0, bits);
         // the bins span the row, or as far down as weights matter
         const float span = lift ? 0.0f : fminf(fminf(top - range.y, 64.0f * t), 0x1.fffffep127f);
         width = span > 0.0f ? fminf((kBins - 1) / span, 0x1p100f) : 0.0f;
