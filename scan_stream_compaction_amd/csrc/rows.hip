@@ -78,11 +78,12 @@ __device__ __forceinline__ void digit_ranks(const uint32_t (&d)[ITEMS], const bo
     for (int j = 0; j < ITEMS; ++j) {
         const uint32_t below = __builtin_amdgcn_mbcnt_hi(hi[j], __builtin_amdgcn_mbcnt_lo(lo[j], 0u));
         const uint32_t same = static_cast<uint32_t>(__builtin_popcount(lo[j]) + __builtin_popcount(hi[j]));
-        uint32_t run = 0;
-        if (valid[j]) {
-            run = cnt[d[j]];
-            if (below + 1u == same) cnt[d[j]] = run + same;
-        }
+        // every lane reads its digit's count before the last lane of the digit
+        // raises it, and the next set's lanes read after that
+        const uint32_t run = valid[j] ? cnt[d[j]] : 0u;
+        wave_lds_order();
+        if (valid[j] && below + 1u == same) cnt[d[j]] = run + same;
+        wave_lds_order();
         rk[j] = run + below;
     }
 }

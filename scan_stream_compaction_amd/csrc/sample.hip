@@ -689,6 +689,7 @@ __global__ __launch_bounds__(kPartBlock) void sample_sum_kernel(SampleArgs a) {
                     packed += static_cast<uint32_t>(__builtin_popcountll(mask));
                 }
             }
+            wave_lds_order();  // written by one lane, read by another
             // places in [0, kept) are kept, those in [kept, end) and [far, far_end)
             // collected; the last bin's end is a NaN, which nothing reaches
             const float kept = static_cast<float>(lo);
@@ -1005,8 +1006,7 @@ __device__ __forceinline__ void sort_list(unsigned long long *e, int n2) {
             if (d > 2 * kWave || next > 2 * kWave || (left == 0 && size == n2)) {
                 __syncthreads();
             } else {
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
+                wave_lds_order();
             }
         }
     }

@@ -28,6 +28,14 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) {
     return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(x)));
 }
 
+// Between LDS accesses of a wavefront's lanes to words that other lanes of it
+// access: the hardware takes a wavefront's LDS operations in order, and this
+// keeps the compiler from moving one past another.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ------------------------------------------------------------ value ops ---
 // Sum over uint32 (wraps modulo 2^32, which also serves int32 scans) and
 // over fp32. `bits`/`from_bits` move values through 32-bit descriptors.
