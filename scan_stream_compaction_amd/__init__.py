@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -685,13 +686,20 @@ def _numel(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.numel()
 
 
-def _optional(t, name: str, like: torch.Tensor, shape) -> torch.Tensor | None:
+def _shaped(t: torch.Tensor, *shape) -> torch.Tensor:
+    """A caller's buffer as the call documents its result: itself if it is of
+    that shape, else a view of its first elements, so that a larger buffer's
+    tail, which no call writes, does not go on into the next one."""
+    return t if t.shape == shape else t.view(-1)[:math.prod(shape)].view(shape)
+
+
+def _optional(t, name: str, like: torch.Tensor, *shape) -> torch.Tensor | None:
     """An int32 output that is wanted (True, or the tensor to write) or not."""
     if t is True:
         return like.new_empty(shape, dtype=torch.int32)
     if t is None or t is False:
         return None
-    return _need(t, name, like, (torch.int32,), like.numel())
+    return _shaped(_need(t, name, like, (torch.int32,), like.numel()), *shape)
 
 
 def group_scratch_bytes(n: int, groups: int) -> int:
@@ -706,16 +714,17 @@ def group_by_key(keys: torch.Tensor, groups: int, *, order=True, ranks=True,
     the key in slot s, its entries past offsets[groups] not written;
     offsets[g] is the first slot of group g, offsets[groups] the number of
     slots taken. order and ranks are True (a new tensor), False (None is
-    returned) or the int32 tensor to write."""
+    returned) or the int32 tensor to write. Of a larger tensor than needed, the
+    part that holds the result is returned."""
     _dev(keys)
     n = keys.numel()
     name = "ssc_group_by_key_" + _ids(keys, "keys")
     if not 1 <= groups < 2**31 - 1:
         raise ValueError(f"groups must be in [1, 2^31 - 2], not {groups}")
     order = _optional(order, "order", keys, n)
-    ranks = _optional(ranks, "ranks", keys, n if keys.dim() == 1 else keys.shape)
+    ranks = _optional(ranks, "ranks", keys, *keys.shape)
     offsets = (keys.new_empty(groups + 1, dtype=torch.int32) if offsets is None
-               else _need(offsets, "offsets", keys, (torch.int32,), groups + 1))
+               else _shaped(_need(offsets, "offsets", keys, (torch.int32,), groups + 1), groups + 1))
     scratch = _work_bytes(scratch, keys, group_scratch_bytes(n, groups))
     _row_call(name, keys, keys, n, groups, order, ranks, offsets, scratch, _numel(scratch))
     return order, ranks, offsets
@@ -737,13 +746,14 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
 
 
 def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, offsets: torch.Tensor,
-                    scale: float = 1.0, *, dtype: torch.dtype | None = None,
+                    scale: float = 1.0, *, vocab: int | None = None, dtype: torch.dtype | None = None,
                     out: torch.Tensor | None = None, accumulate: bool = False,
                     scratch: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of embed_rows with respect to the table: out[v] = scale *
     (sum of dout[i] over ids[i] = v), given order and offsets of
-    group_by_key(ids, vocab). dout is (*ids.shape, width); the gradient is
-    (vocab, width), of dout's type or float32 (`dtype`, or that of `out`).
+    group_by_key(ids, vocab). offsets holds vocab + 1 entries, unless vocab is
+    given: it may then be a larger buffer. dout is (*ids.shape, width); the
+    gradient is (vocab, width), of dout's type or float32 (`dtype`, or that of `out`).
     accumulate=True adds to `out` and leaves its rows without tokens as they are."""
     _dev(dout)
     if dout.dtype not in DTYPE:
@@ -756,8 +766,11 @@ def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, 
     if dout.numel() != n * width:
         raise ValueError("dout holds one row per id")
     _need(order, "order", dout, (torch.int32,), n)
-    _need(offsets, "offsets", dout, (torch.int32,), 2)
-    vocab = offsets.numel() - 1
+    if vocab is not None and vocab < 1:
+        raise ValueError(f"vocab must be at least 1, not {vocab}")
+    _need(offsets, "offsets", dout, (torch.int32,), 2 if vocab is None else vocab + 1)
+    if vocab is None:
+        vocab = offsets.numel() - 1
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to a given out")

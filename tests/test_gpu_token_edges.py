@@ -37,3 +37,49 @@ def test_min_p_above_one_keeps_the_first_alone(dtype, vocab):
             assert torch.equal(tokens.long(), first) and bool((kept == 1).all()) and bool((logprobs == 0).all())
     tokens, kept, logprobs = ssc.sample_rows(logits, u, min_p=row(1.0))
     assert torch.equal(kept.long(), equal)
+
+
+def _small_integers(g, *shape, dtype=torch.float32):
+    """Whole numbers of [-3, 3], whose sums are exact in fp32 up to 2^24."""
+    return torch.randint(-3, 4, shape, device=DEV, generator=g).to(dtype)
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.mark.parametrize("fill", [0, 7, -1, 2 ** 31 - 1])
+def test_larger_buffers_for_a_grouping(fill):
+    """order, ranks and offsets in buffers that are larger than needed, filled
+    with anything: what is returned is the result alone, in its shape, and the
+    calls that take it on do not meet the rest."""
+    g = _gen(51)
+    n, vocab, width = 5000, 300, 24
+    ids = torch.randint(-1, vocab, (n // 4, 4), device=DEV, generator=g)
+    dout = _small_integers(g, n // 4, 4, width, dtype=torch.bfloat16)
+    want = torch.zeros(vocab + 1, width, device=DEV).index_add_(0, ids.view(-1) % (vocab + 1), dout.view(n, width).float())[:-1]
+    worder, wranks, woffsets = ssc.group_by_key(ids, vocab)
+
+    def buffer(size):
+        return torch.full((size,), fill, dtype=torch.int32, device=DEV)
+    buf = buffer(2000)
+    order, ranks, offsets = ssc.group_by_key(ids, vocab, order=buffer(9000), ranks=buffer(9000), offsets=buf)
+    assert order.shape == (n,) and ranks.shape == ids.shape and offsets.shape == (vocab + 1,)
+    kept = int(offsets[-1])
+    assert torch.equal(order[:kept], worder[:kept]) and torch.equal(ranks, wranks) and torch.equal(offsets, woffsets)
+    assert bool((buf[vocab + 1:] == fill).all()) and offsets.data_ptr() == buf.data_ptr()
+    for kw in ({"offsets": offsets}, {"offsets": buf, "vocab": vocab}):
+        grad = ssc.embed_rows_grad(dout, ids, order, dtype=torch.float32, **kw)
+        assert grad.shape == (vocab, width) and torch.equal(grad, want)
+    # rows there and back by ranks out of a larger buffer
+    x = _small_integers(g, n // 4, width)
+    back = ssc.dispatch_rows_grad(ssc.dispatch_rows(x, ranks), ranks)
+    assert torch.equal(back, x * (ids >= 0).sum(1, keepdim=True))
+    # a tensor of the right shape is returned as it is
+    assert ssc.group_by_key(ids, vocab, offsets=offsets)[2] is offsets
+    with pytest.raises(ValueError):
+        ssc.embed_rows_grad(dout, ids, order, offsets, vocab=vocab + 1)
+    with pytest.raises(ValueError):
+        ssc.embed_rows_grad(dout, ids, order, offsets, vocab=0)
