@@ -645,7 +645,9 @@ def compact_kv(keys: torch.Tensor, vals: torch.Tensor, pred="nonzero", pa=0, pb=
 
 
 # ---- rows moved by a key, and the choice of the next token ----------------
-# These calls compute outside autograd: a gradient is a call of its own.
+# These calls compute outside autograd: a gradient is a call of its own. Where
+# the result of a call goes to a given larger tensor, the part that holds it is
+# returned, in the documented shape.
 
 
 def _rows(x: torch.Tensor, name: str) -> tuple[int, int]:
@@ -714,15 +716,14 @@ def group_by_key(keys: torch.Tensor, groups: int, *, order=True, ranks=True,
     the key in slot s, its entries past offsets[groups] not written;
     offsets[g] is the first slot of group g, offsets[groups] the number of
     slots taken. order and ranks are True (a new tensor), False (None is
-    returned) or the int32 tensor to write. Of a larger tensor than needed, the
-    part that holds the result is returned."""
+    returned) or the int32 tensor to write."""
     _dev(keys)
     n = keys.numel()
     name = "ssc_group_by_key_" + _ids(keys, "keys")
     if not 1 <= groups < 2**31 - 1:
         raise ValueError(f"groups must be in [1, 2^31 - 2], not {groups}")
     order = _optional(order, "order", keys, n)
-    ranks = _optional(ranks, "ranks", keys, *keys.shape)
+    ranks = _optional(ranks, "ranks", keys, *((n,) if keys.dim() == 1 else keys.shape))
     offsets = (keys.new_empty(groups + 1, dtype=torch.int32) if offsets is None
                else _shaped(_need(offsets, "offsets", keys, (torch.int32,), groups + 1), groups + 1))
     scratch = _work_bytes(scratch, keys, group_scratch_bytes(n, groups))
@@ -740,7 +741,7 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
     name = "ssc_embed_rows_" + _ids(ids, "ids") if isinstance(ids, torch.Tensor) else ""
     n = _need(ids, "ids", table, None, 0).numel()
     out = (table.new_empty((n, width) if ids.dim() == 1 else (*ids.shape, width)) if out is None
-           else _need(out, "out", table, (table.dtype,), n * width))
+           else _shaped(_need(out, "out", table, (table.dtype,), n * width), *ids.shape, width))
     _row_call(name, table, table, DTYPE[table.dtype], vocab, width, ids, n, float(scale), out)
     return out
 
@@ -776,7 +777,7 @@ def embed_rows_grad(dout: torch.Tensor, ids: torch.Tensor, order: torch.Tensor, 
             raise ValueError("accumulate adds to a given out")
         out = dout.new_empty((vocab, width), dtype=dtype)
     else:
-        _need(out, "out", dout, None, vocab * width)
+        out = _shaped(_need(out, "out", dout, None, vocab * width), vocab, width)
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out is {out.dtype}, not {dtype}")
     if out.dtype not in (dout.dtype, torch.float32):
@@ -833,7 +834,7 @@ def combine_rows(y: torch.Tensor, ranks: torch.Tensor, weights: torch.Tensor | N
     if weights is not None:
         _weights(weights, y, ranks)
     out = (y.new_empty((tokens, width)) if out is None
-           else _need(out, "out", y, (y.dtype,), tokens * width))
+           else _shaped(_need(out, "out", y, (y.dtype,), tokens * width), tokens, width))
     _row_call("ssc_combine_rows", y, y, DTYPE[y.dtype], rows, width, ranks, weights, tokens, per, out)
     return out
 
@@ -860,9 +861,10 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, ranks: torch.Tensor, 
     if ywidth != width:
         raise ValueError("y has rows of dout's width")
     _weights(weights, dout, ranks)
-    dy = torch.empty_like(y) if dy is None else _need(dy, "dy", dout, (dout.dtype,), rows * width)
+    dy = (torch.empty_like(y) if dy is None
+          else _shaped(_need(dy, "dy", dout, (dout.dtype,), rows * width), rows, width))
     dweights = (torch.empty_like(weights) if dweights is None
-                else _need(dweights, "dweights", dout, (torch.float32,), tokens * per))
+                else _shaped(_need(dweights, "dweights", dout, (torch.float32,), tokens * per), *weights.shape))
     _row_call("ssc_combine_rows_grad", dout, dout, y, DTYPE[dout.dtype], rows, width, ranks, weights, tokens, per,
               dy, dweights)
     return dy, dweights
@@ -904,7 +906,7 @@ def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor
             raise ValueError(f"{name} holds one value a row")
         settings.append(t)
     tokens, kept, logprobs = (
-        logits.new_empty(rows, dtype=dt) if t is None else _need(t, name, logits, (dt,), rows)
+        logits.new_empty(rows, dtype=dt) if t is None else _shaped(_need(t, name, logits, (dt,), rows), rows)
         for t, name, dt in ((tokens, "tokens", torch.int32), (kept, "kept", torch.int32),
                             (logprobs, "logprobs", torch.float32)))
     scratch = _work_bytes(scratch, logits, sample_scratch_bytes(rows, vocab))

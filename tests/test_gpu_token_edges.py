@@ -83,3 +83,39 @@ def test_larger_buffers_for_a_grouping(fill):
         ssc.embed_rows_grad(dout, ids, order, offsets, vocab=vocab + 1)
     with pytest.raises(ValueError):
         ssc.embed_rows_grad(dout, ids, order, offsets, vocab=0)
+
+
+def test_larger_buffers_for_rows_and_tokens():
+    """Outputs in larger buffers come back as the result alone, in its shape:
+    the tokens of a step, say, that the lookup takes next."""
+    g = _gen(52)
+    rows, vocab, width, experts, per = 5, 200, 16, 6, 2
+    logits = _small_integers(g, rows, vocab)
+    u = torch.rand(rows, device=DEV, generator=g)
+    table = _small_integers(g, vocab, width)
+
+    def buffer(dtype):
+        return torch.full((4000,), 3, dtype=dtype, device=DEV)
+    i32, f32 = torch.int32, torch.float32
+    bufs = [buffer(i32), buffer(i32), buffer(f32)]
+    got = ssc.sample_rows(logits, u, tokens=bufs[0], kept=bufs[1], logprobs=bufs[2])
+    for a, b, buf in zip(got, ssc.sample_rows(logits, u), bufs):
+        assert torch.equal(a, b) and a.data_ptr() == buf.data_ptr() and bool((buf[rows:] == 3).all())
+    tokens = got[0]
+    out = buffer(f32)
+    x = ssc.embed_rows(table, tokens.view(rows, 1), out=out)
+    assert x.shape == (rows, 1, width) and torch.equal(x[:, 0], table[tokens.long()]) and bool((out[x.numel():] == 3).all())
+    x = x.view(rows, width)
+    _, ranks, _ = ssc.group_by_key(torch.randint(0, experts, (rows, per), device=DEV, generator=g), experts)
+    y = ssc.dispatch_rows(x, ranks)
+    w = _small_integers(g, rows, per)
+    back = ssc.combine_rows(y, ranks, w, out=buffer(f32))
+    assert back.shape == (rows, width) and torch.equal(back, x * w.sum(1, keepdim=True))
+    dy, dw = ssc.combine_rows_grad(x, y, ranks, w, dy=buffer(f32), dweights=buffer(f32))
+    want = ssc.combine_rows_grad(x, y, ranks, w)
+    assert dy.shape == y.shape and dw.shape == w.shape and torch.equal(dy, want[0]) and torch.equal(dw, want[1])
+    order, _, offsets = ssc.group_by_key(tokens, vocab)
+    grad = ssc.embed_rows_grad(x, tokens, order, offsets, out=buffer(f32))
+    assert grad.shape == (vocab, width) and torch.equal(grad, ssc.embed_rows_grad(x, tokens, order, offsets))
+    # a tensor of the right shape is returned as it is
+    assert ssc.embed_rows(table, tokens, out=x) is x and ssc.combine_rows(y, ranks, w, out=back) is back
