@@ -426,7 +426,7 @@ size_t ssc_embed_grad_scratch_bytes(int64_t n, int64_t width);
 
 /* Gradient of the lookup with respect to the table, by sorted tokens:
  * grad[v] = scale * (sum of dout[i] over all i with ids[i] = v), given the
- * grouping of the ids (`order` and `offsets` of ssc_group_by_key with groups
+ * grouping of these ids (`order` and `offsets` of ssc_group_by_key with groups
  * = vocab). accumulate = 0 writes every row of grad, zeros where no token
  * has the id; otherwise the sum is added to the row, and rows without tokens
  * are not touched. grad_dtype is dtype or SSC_F32. */

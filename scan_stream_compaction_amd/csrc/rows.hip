@@ -703,12 +703,22 @@ struct BlockSums {
     int levels;
 };
 
-// ids of the block's first and last position are the same
+// The sorted positions that hold tokens of the vocabulary. A block's sum is
+// read only where a row's range holds all of it, and made where it may be: the
+// two kernels agree on which blocks end before this.
+__device__ __forceinline__ uint32_t sorted_tokens(const int32_t *offsets, int64_t vocab, uint32_t n) {
+    const uint32_t kept = static_cast<uint32_t>(offsets[vocab]);
+    return kept < n ? kept : n;
+}
+
+// Whether the block's first and last position hold the same id, as far as
+// they hold one: a position outside [0, n) adds nothing to the sum, but leaves
+// open whose block it is.
 template <class I>
 __device__ __forceinline__ bool one_id(const I *ids, const int32_t *order, int64_t lo, int64_t hi, uint32_t n,
                                        int64_t vocab) {
     const uint32_t i0 = static_cast<uint32_t>(order[lo]), i1 = static_cast<uint32_t>(order[hi]);
-    if (i0 >= n || i1 >= n) return false;
+    if (i0 >= n || i1 >= n) return true;
     const int64_t a = ids[i0], b = ids[i1];
     return a == b && a >= 0 && a < vocab;
 }
@@ -722,8 +732,7 @@ __global__ __launch_bounds__(kRowBlock) void grad_blocks_kernel(
     const int lg = kSumLg * (level + 1);
     const int64_t block = row_of<WAVE>(m);
     const int64_t lo = block << lg, hi = lo + (int64_t{1} << lg) - 1;
-    const int64_t kept = offsets[vocab] < static_cast<int64_t>(n) ? offsets[vocab] : n;
-    if (hi >= kept || !one_id(ids, order, lo, hi, n, vocab)) return;
+    if (hi >= sorted_tokens(offsets, vocab, n) || !one_id(ids, order, lo, hi, n, vocab)) return;
     float *dst = sums.level[level] + block * m.width;
     for (int c = col_of(m); c < m.chunks; c += col_step(m)) {
         const int at = chunk_start<N>(c, m);
@@ -770,7 +779,8 @@ __global__ __launch_bounds__(kRowBlock) void embed_grad_kernel(
     if (v >= vocab) return;
     const uint32_t a = static_cast<uint32_t>(offsets[v]);
     uint32_t b = static_cast<uint32_t>(offsets[v + 1]);
-    if (b > n) b = n;
+    const uint32_t kept = sorted_tokens(offsets, vocab, n);
+    if (b > kept) b = kept;
     if (accumulate && a >= b) return;
     G *dst = grad + v * m.width;
     const int step = col_step(m);

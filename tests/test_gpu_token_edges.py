@@ -119,3 +119,43 @@ def test_larger_buffers_for_rows_and_tokens():
     assert grad.shape == (vocab, width) and torch.equal(grad, ssc.embed_rows_grad(x, tokens, order, offsets))
     # a tensor of the right shape is returned as it is
     assert ssc.embed_rows(table, tokens, out=x) is x and ssc.combine_rows(y, ranks, w, out=back) is back
+
+
+@pytest.mark.parametrize("n,vocab", [(256, 1), (4999, 3), (70_001, 2), (300_007, 3)])
+def test_embed_grad_of_positions_outside(n, vocab):
+    """Positions outside [0, n) add nothing, also where they begin or end a
+    block of 16, 256 or 4096 sorted tokens whose sum is made first; and where
+    the last offset cuts ranges short, nothing is taken from sums that were
+    not made. The scratch holds NaN before each call."""
+    g = _gen(n)
+    width = 24
+    ids = torch.randint(0, vocab, (n,), device=DEV, generator=g)
+    dout = _small_integers(g, n, width, dtype=torch.bfloat16)
+    order, _, offsets = ssc.group_by_key(ids, vocab, ranks=False)
+    size = ssc.lib().ssc_embed_grad_scratch_bytes(n, width)
+
+    def check(order, offsets):
+        group = torch.bucketize(torch.arange(n, device=DEV), offsets[1:].long(), right=True).clamp(max=vocab)
+        inside = (order >= 0) & (order < n) & (group < vocab)
+        rows = dout.float()[order.long().clamp(0, n - 1)] * inside[:, None]
+        want = torch.zeros(vocab + 1, width, device=DEV).index_add_(0, group, rows)[:-1]
+        scratch = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+        got = ssc.embed_rows_grad(dout, ids, order, offsets, 0.5, dtype=torch.float32, scratch=scratch)
+        assert torch.equal(got, want * 0.5)
+    check(order, offsets)
+    for outside in (-1, n, 2 ** 31 - 1, -2 ** 31):
+        for at in (torch.arange(0, n, 16), torch.arange(15, n, 16), torch.arange(0, n, 4096), torch.arange(255, n, 256),
+                   torch.randint(0, n, (n // 5,))):
+            bad = order.clone()
+            bad[at.to(DEV)] = outside
+            check(bad, offsets)
+    check(torch.full_like(order, n), offsets)
+    for last in (0, int(offsets[-1]) - 100):
+        cut = offsets.clamp(max=last)
+        check(order, cut)
+        if vocab > 1:  # the last offset alone: earlier rows reach past it
+            cut = offsets.clone()
+            cut[-1] = last
+            scratch = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+            got = ssc.embed_rows_grad(dout, ids, order, cut, 0.5, dtype=torch.float32, scratch=scratch)
+            assert torch.equal(got, ssc.embed_rows_grad(dout, ids, order, cut.clamp(max=last), 0.5, dtype=torch.float32))
