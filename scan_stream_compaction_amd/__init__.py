@@ -668,13 +668,24 @@ def _ids(x: torch.Tensor, name: str) -> str:
     raise TypeError(f"{name} must be int32 or int64, not {x.dtype}")
 
 
+def _on_device(fn, device: int):
+    """fn with `device` current while it runs, whichever is when it is called."""
+    def call(*raw):
+        if device == _current_device():
+            return fn(*raw)
+        with torch.cuda.device(device):
+            return fn(*raw)
+    return call
+
+
 def _row_call(name: str, like: torch.Tensor, *args) -> None:
-    """_call on like's stream, with its device current."""
-    if like.get_device() == _current_device():
-        _call(name, getattr(_lib or lib(), name), *args, _stream(like))
-    else:
-        with torch.cuda.device(like.device):
-            _call(name, getattr(_lib or lib(), name), *args, _stream(like))
+    """_call on like's stream, with its device current, also when it is
+    repeated by a prepared call."""
+    fn = getattr(_lib or lib(), name)
+    device = like.get_device()
+    if _recording is not None or device != _current_device():
+        fn = _on_device(fn, device)
+    _call(name, fn, *args, _stream(like))
 
 
 def _work_bytes(scratch, like: torch.Tensor, nbytes: int) -> torch.Tensor | None:

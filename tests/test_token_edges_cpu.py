@@ -6,6 +6,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
+
+import scan_stream_compaction_amd as ssc
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "scan_stream_compaction_amd", "csrc")
@@ -23,3 +26,52 @@ def test_the_steps_over_the_most_assignments(tmp_path):
                    check=True)
     res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and res.stdout == "ok\n", res.stdout + res.stderr
+
+
+class _Device:
+    """What torch.cuda.device does to the current device, without a GPU."""
+    current = 0
+
+    def __init__(self, device):
+        self.device = device if isinstance(device, int) else device.index
+
+    def __enter__(self):
+        self.before, _Device.current = _Device.current, self.device
+
+    def __exit__(self, *_):
+        _Device.current = self.before
+
+
+class _On:
+    """A tensor's device, for a call that reads nothing else of it."""
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+@pytest.mark.parametrize("at_record", [0, 1])
+def test_a_prepared_row_call_runs_on_its_tensors_device(monkeypatch, at_record):
+    """Called and repeated with the tensors' device current, whichever device
+    is current at the time, and with the current one back afterwards."""
+    ran = []
+
+    class Lib:
+        @staticmethod
+        def ssc_dispatch_rows(*raw):
+            ran.append((_Device.current, raw))
+            return 0
+
+    monkeypatch.setattr(_Device, "current", at_record)
+    monkeypatch.setattr(ssc, "_lib", Lib)
+    monkeypatch.setattr(ssc, "_current_device", lambda: _Device.current)
+    monkeypatch.setattr(ssc, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(torch.cuda, "device", _Device)
+    call = ssc.prepared(ssc._row_call, "ssc_dispatch_rows", _On(1), 5)
+    for current in (0, 1, 2):
+        _Device.current = current
+        call()
+        ssc._row_call("ssc_dispatch_rows", _On(1), 5)
+        assert _Device.current == current
+    assert ran == [(1, (5, 1001))] * 7
