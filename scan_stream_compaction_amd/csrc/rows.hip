@@ -395,12 +395,6 @@ struct Chunk {
         else
             return *p;
     }
-    __device__ static __forceinline__ void store(T *p, Raw r) {
-        if constexpr (VEC)
-            *reinterpret_cast<u32x4_any *>(p) = r;
-        else
-            *p = r;
-    }
     // what a call reads or writes once goes past the caches
     __device__ static __forceinline__ Raw load_stream(const T *p) {
         if constexpr (VEC)
