@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import scan_stream_compaction_amd as ssc
+from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, block_case, group_sums
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -159,3 +160,22 @@ def test_embed_grad_of_positions_outside(n, vocab):
             scratch = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
             got = ssc.embed_rows_grad(dout, ids, order, cut, 0.5, dtype=torch.float32, scratch=scratch)
             assert torch.equal(got, ssc.embed_rows_grad(dout, ids, order, cut.clamp(max=last), 0.5, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("n,vocab,hot", BLOCK_CASES)
+def test_embed_grad_block_sums_exactly(n, vocab, hot):
+    """Sums through every level of blocks, of whole numbers that fp32 holds:
+    equal to the last bit, whatever the order, with a power of two as scale."""
+    ids, rows = block_case(n, vocab, hot)
+    want = torch.from_numpy(group_sums(ids, rows, vocab)).to(DEV).double() * 0.25
+    ids = torch.from_numpy(ids).to(DEV)
+    order, _, offsets = ssc.group_by_key(ids, vocab, ranks=False)
+    for dtype in TYPES:
+        dout = torch.from_numpy(rows).to(DEV).to(dtype)
+        grad = ssc.embed_rows_grad(dout, ids, order, offsets, 0.25, dtype=torch.float32)
+        assert torch.equal(grad.double(), want)
+        if dtype is not torch.float16:  # whose range the sums may leave
+            base = torch.ones(vocab, BLOCK_WIDTH, dtype=torch.float32, device=DEV)
+            assert torch.equal(ssc.embed_rows_grad(dout, ids, order, offsets, 0.25), want.to(dtype))
+            ssc.embed_rows_grad(dout, ids, order, offsets, 0.25, out=base, accumulate=True)
+            assert torch.equal(base.double(), want + 1)

@@ -5,10 +5,12 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
 import scan_stream_compaction_amd as ssc
+from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, block_case, group_sums
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "scan_stream_compaction_amd", "csrc")
@@ -75,3 +77,24 @@ def test_a_prepared_row_call_runs_on_its_tensors_device(monkeypatch, at_record):
         ssc._row_call("ssc_dispatch_rows", _On(1), 5)
         assert _Device.current == current
     assert ran == [(1, (5, 1001))] * 7
+
+
+@pytest.mark.parametrize("n,vocab,hot", BLOCK_CASES)
+def test_every_block_sum_shows(n, vocab, hot):
+    """The inputs of the block sums' exact test: leaving out, doubling or
+    exchanging any one block of 16, 256 or 4096 sorted positions of an id
+    changes that id's sums, and no partial sum leaves fp32's whole numbers."""
+    ids, rows = block_case(n, vocab, hot)
+    assert 3 * n < 2 ** 24
+    order = np.argsort(ids, kind="stable")
+    key, rows = ids[order], rows[order]
+    for size in (16, 256, 4096):
+        m = n // size
+        sums = rows[:m * size].reshape(m, size, BLOCK_WIDTH).sum(1, dtype=np.int64)
+        whole = key[:m * size:size] == key[size - 1:m * size:size]
+        assert bool((sums[whole] != 0).any(1).all())
+        first = sums[whole]
+        assert len(np.unique(first, axis=0)) == len(first)
+    want = np.zeros((vocab, rows.shape[1]), np.int64)
+    np.add.at(want, key, rows)
+    assert np.array_equal(group_sums(key, rows, vocab), want)
