@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import scan_stream_compaction_amd as ssc
-from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, block_case, group_sums
+from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, EQUAL_ROWS, block_case, group_sums
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -179,3 +179,28 @@ def test_embed_grad_block_sums_exactly(n, vocab, hot):
             assert torch.equal(ssc.embed_rows_grad(dout, ids, order, offsets, 0.25), want.to(dtype))
             ssc.embed_rows_grad(dout, ids, order, offsets, 0.25, out=base, accumulate=True)
             assert torch.equal(base.double(), want + 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", sorted({c[0] for c in EQUAL_ROWS}))
+def test_equal_weights_meet_the_border(dtype, vocab):
+    """top_p times the sum is met exactly by the running weight of equal
+    logits: the token at the border is not kept, in rows whose border logits
+    are collected and in rows that have more of them. u at exact borders, too."""
+    cases = [c for c in EQUAL_ROWS if c[0] == vocab]
+    logits = torch.full((len(cases), vocab), 0.5, device=DEV, dtype=dtype)
+    for r, (_, step, *_) in enumerate(cases):
+        logits[r, torch.arange(vocab, device=DEV) % step != 0] = float("-inf")
+    step, k, p, kept = (torch.tensor([c[i] for c in cases], device=DEV) for i in (1, 2, 3, 4))
+    p = p.float()
+    for j in (torch.zeros_like(kept), torch.ones_like(kept), kept // 2, kept - 1):
+        # u in fp32 may lie below j / kept by a step: the token before is then the first past it
+        u = (j.double() / kept).float()
+        want = (u.double() * kept).floor().long() * step
+        tokens, count, logprobs = ssc.sample_rows(logits, u, top_k=k.int(), top_p=p)
+        assert torch.equal(count.long(), kept) and torch.equal(tokens.long(), want)
+        lp = -kept.double().log()
+        assert bool(((logprobs.double() - lp).abs() <= 2.0 ** -24 * lp.abs() + 2.0 ** -45).all())
+    up = torch.nextafter(p, torch.ones_like(p))
+    _, count, _ = ssc.sample_rows(logits, torch.zeros(len(cases), device=DEV), top_k=k.int(), top_p=up)
+    assert torch.equal(count.long(), kept + 1)

@@ -10,7 +10,8 @@ import pytest
 import torch
 
 import scan_stream_compaction_amd as ssc
-from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, block_case, group_sums
+from tests.sample_reference import sample_row
+from tests.token_inputs import BLOCK_CASES, BLOCK_WIDTH, EQUAL_ROWS, block_case, group_sums
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "scan_stream_compaction_amd", "csrc")
@@ -98,3 +99,14 @@ def test_every_block_sum_shows(n, vocab, hot):
     want = np.zeros((vocab, rows.shape[1]), np.int64)
     np.add.at(want, key, rows)
     assert np.array_equal(group_sums(key, rows, vocab), want)
+
+
+@pytest.mark.parametrize("vocab,step,k,p,kept", [c for c in EQUAL_ROWS if c[0] <= 16_384])
+def test_equal_weights_meet_the_border(vocab, step, k, p, kept):
+    """The reference on equal logits: the count worked by hand, and one more
+    where the comparison of the definition (less than) is taken as "or equal"."""
+    x = np.where(np.arange(vocab) % step == 0, 0.5, -np.inf)
+    for j in (0, 1, kept // 2, kept - 1):
+        token, count, logprob = sample_row(x, j / kept, k=k, p=p)
+        assert (token, count) == (j * step, kept) and abs(logprob + np.log(kept)) < 1e-12
+    assert sample_row(x, 0.0, k=k, p=np.nextafter(p, 1))[1] == kept + 1

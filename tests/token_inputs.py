@@ -1,5 +1,5 @@
 """Inputs whose results are exact, so that a call's are compared for equality:
-small whole numbers as rows."""
+small whole numbers as rows, and equal logits as weights."""
 from __future__ import annotations
 
 import numpy as np
@@ -25,3 +25,14 @@ def group_sums(ids, rows, vocab):
     ends = np.cumsum(np.bincount(ids, minlength=vocab))
     run = np.concatenate([np.zeros((1, rows.shape[1]), np.int64), np.cumsum(rows[order], axis=0, dtype=np.int64)])
     return run[ends] - run[np.concatenate([[0], ends[:-1]])]
+
+
+# Equal logits all weigh 1, so that with a share of 1/4, 1/2 or 3/4 the running
+# weight meets top_p times the sum exactly: the tokens before the border are
+# kept, the one at it is not. Rows of: vocabulary, every step-th logit a token
+# (the others masked), top_k, top_p, kept.
+EQUAL_ROWS = [(vocab, step, k, p, int((min(k, vocab // step) if k else vocab // step) * p))
+              for vocab in (64, 4096, 16_384, 131_072)
+              for step in (1, 2)
+              for k in (0, 32, 2048, 4096, 65_536)
+              for p in (0.25, 0.5, 0.75)]
