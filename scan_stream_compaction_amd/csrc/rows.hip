@@ -1024,19 +1024,27 @@ int with_type(int dtype, int64_t width, F f) {
 // against 222, dispatch 101 against 97.7). Up to 256 chunks a row gets a
 // thread a chunk, or half the threads with two chunks each, all of a row's
 // loads in flight: where the chunks fill at most `halve` eighths of the
-// threads. 40,000 rows of bf16, a table of 60,000, one chunk against two, us:
-//   chunks               65           138          192          256
-//   threads           128   64     256   128    256   128    256   128
-//   embed            17.5  14.4   28.6  27.0   39.7  36.0   49.3  47.7
-//   embed's gradient 30.7  27.5   48.3  49.0   54.8  42.8   76.1  57.8
-//   combine          28.3  23.0   49.5  45.6   61.5  58.4   79.0  79.2
-//   its gradient     60.0  43.9    116  86.5    121  97.2    144   124
-//   dispatch         26.0  27.8   50.9  55.8
-// so all rows for 8, combine up to 5/8 (9,973 x 6 rows of 182 chunks 35.5
-// against 38.7) and dispatch none. A small table's gradient stays at one (10,007
-// rows of 65 chunks 10.1 against 11.5). Where the rows are too few to fill the
-// chip (fewer than two workgroups a compute unit), columns go over several
-// workgroups (split).
+// threads. Rows of bf16, one chunk against two, us a call; 40,000 ids drawn
+// evenly, or falling as 1/rank as in text:
+//   chunks                               65           138          192          256
+//   threads                           128   64     256   128    256   128    256   128
+//   embed, table of 60,000, even     17.0  14.8   28.9  28.7   36.3  37.9   51.5  48.6
+//     as in text                     16.3  11.2   25.6  21.2   28.5  27.1   38.2  35.9
+//   combine's gradient, 20,000 x 2   31.5  24.6   60.3  46.3   64.8  54.5   74.3  70.7
+//   combine, 10,000 x 2               8.2   6.3   13.3  11.7   15.4  15.8   20.4  20.6
+//     40,000 x 6                     53.1  52.5    110   109    150   148    200   198
+//   dispatch                         26.0  27.8   50.9  55.8
+//   embed's gradient, text, 16,384   27.6  32.2   35.4  39.2   43.7  48.8   53.4  59.1
+//     32,768                         29.6  33.5   44.5  46.2   52.3  53.2   63.6  65.8
+//     60,000                         36.9  38.3   59.2  58.5   70.0  68.0   82.8  81.0
+//     90,000                         45.8  42.1   73.6  73.0   86.8  84.0    102   102
+//     even, 60,000                   36.4  31.9   57.6  56.1   61.4  61.0   75.4  74.4
+// so embed and combine's gradient always; combine up to 5/8 (160 chunks 14.2
+// against 12.8, from 182 on within 3% either way); dispatch never; embed's
+// gradient from tables of 65,536 rows on, below which the long run of a frequent
+// id, two chunks to a thread, counts for more than what evenly drawn ids gain.
+// Where the rows are too few to fill the chip (fewer than two workgroups a
+// compute unit), columns go over several workgroups (split).
 struct RowLaunch {
     RowMap map;
     dim3 grid;
@@ -1176,7 +1184,7 @@ int embed_grad_impl(const void *dout, int dtype, int64_t n, int64_t width, const
                                    static_cast<const T *>(dout), ids, order, offsets, un, vocab, l, sums, r.map);
             SSC_TRY(launched());
         }
-        const RowLaunch r = row_launch(vocab, width, Chunk<T, V>::kN, true, vocab >= 16384 ? 8 : 0);
+        const RowLaunch r = row_launch(vocab, width, Chunk<T, V>::kN, true, vocab >= 65536 ? 8 : 0);
         const auto launch = [&](auto *g) {
             using G = std::remove_pointer_t<decltype(g)>;
             return with_shape(r, [&](auto wave, auto ch) {

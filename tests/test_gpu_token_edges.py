@@ -204,3 +204,25 @@ def test_equal_weights_meet_the_border(dtype, vocab):
     up = torch.nextafter(p, torch.ones_like(p))
     _, count, _ = ssc.sample_rows(logits, torch.zeros(len(cases), device=DEV), top_k=k.int(), top_p=up)
     assert torch.equal(count.long(), kept + 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("chunks,extra", [(65, 0), (65, 1), (129, 3), (200, 0), (256, 0), (256, 1)])
+@pytest.mark.parametrize("vocab", [65_535, 65_536])
+def test_embed_grad_of_larger_tables(vocab, dtype, chunks, extra):
+    """Tables on both sides of the size from which half the threads take two
+    chunks of a row each, with a last chunk that starts early; ids that occur
+    often, once and never, and rows added to what is there."""
+    width = chunks * (16 // torch.empty(0, dtype=dtype).element_size()) - extra
+    g = _gen(width)
+    n = 1500
+    ids = (torch.rand(n, device=DEV, generator=g) ** 8 * (vocab + 1)).long() - 1
+    ids[::50] = vocab - 1
+    dout = _small_integers(g, n, width, dtype=dtype)
+    order, _, offsets = ssc.group_by_key(ids, vocab, ranks=False)
+    inside = ids >= 0
+    want = torch.zeros(vocab, width, device=DEV).index_add_(0, ids[inside], dout[inside].float())
+    assert torch.equal(ssc.embed_rows_grad(dout, ids, order, offsets, dtype=torch.float32), want)
+    assert torch.equal(ssc.embed_rows_grad(dout, ids, order, offsets, 0.5), (want * 0.5).to(dtype))
+    base = torch.ones(vocab, width, device=DEV)
+    assert torch.equal(ssc.embed_rows_grad(dout, ids, order, offsets, out=base, accumulate=True), want + 1)
