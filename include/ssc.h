@@ -460,7 +460,8 @@ int ssc_combine_rows_grad(const void *dout, const void *y, int dtype, int64_t ro
                           const int32_t *ranks, const float *weights, int64_t tokens, int64_t per,
                           void *dy, float *dweights, void *stream);
 
-/* Scratch bytes of ssc_sample_rows. */
+/* Scratch bytes of ssc_sample_rows: about 56 KiB a row and 20 bytes for each
+ * 4096 logits of it, whatever the filters. */
 size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
 
 /* The next token of each row of logits (row r at logits + r * stride
@@ -485,8 +486,13 @@ size_t ssc_sample_scratch_bytes(int64_t rows, int64_t vocab);
  * tokens, logprobs[r] (nullable) the logarithm of the chosen weight over the
  * kept ones' sum. Weights are computed in fp64 and summed as fixed-point
  * integers, so that neither the order of a sum nor the split of a row changes
- * a result: of 62 - ceil(log2(vocab + 1)) fractional bits, at most 50, each
- * off by half the last one, where the largest weight is 1.
+ * a result: of 62 - ceil(log2(vocab + 1)) fractional bits, at most 50, where
+ * the largest weight is 1. Each is off by half the last bit and, by its fp64
+ * exponential, by less than 2^-46 (the largest, and those equal to it, by
+ * nothing), so a sum over the row by vocab times that at most, and a border of
+ * top_p or u that lies as near a running sum may fall on either side of it:
+ * 2^-28 of the largest weight for 131,072 logits, 2^-18 for 2^22, where
+ * rounding all goes one way.
  * 1 <= vocab <= 2^22 and at most 65,535 rows. */
 int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                     const float *u, const float *temperature, const int32_t *top_k,

@@ -746,7 +746,8 @@ def embed_rows(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """out[i] = scale * table[ids[i]], of shape (*ids.shape, width) and the
     table's type (float32, bfloat16 or float16); an id outside the table
-    gives a row of zeros. ids are int32 or int64."""
+    gives a row of zeros. ids are int32 or int64. The result carries no autograd
+    history, whatever the table: embed_rows_grad is its gradient."""
     _dev(table)
     vocab, width = _rows(table, "table")
     name = "ssc_embed_rows_" + _ids(ids, "ids") if isinstance(ids, torch.Tensor) else ""
@@ -813,7 +814,8 @@ def dispatch_rows(x: torch.Tensor, ranks: torch.Tensor, *, out: torch.Tensor | N
     """out[ranks[t, k]] = x[t]: each token's row to the slots that
     group_by_key gave its assignments (ranks of shape (tokens, per) or
     (tokens,)). out has tokens * per rows unless one is given; ranks that it
-    does not hold move nothing, and rows that no rank names are not written."""
+    does not hold move nothing, and rows that no rank names are not written. The
+    result carries no autograd history: dispatch_rows_grad is its gradient."""
     _dev(x)
     tokens, width = _rows(x, "x")
     tokens, per = _routed(ranks, x, tokens)
@@ -838,7 +840,8 @@ def combine_rows(y: torch.Tensor, ranks: torch.Tensor, weights: torch.Tensor | N
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """out[t] = sum over k of weights[t, k] * y[ranks[t, k]], (tokens, width):
     the rows of a token's assignments weighted (float32; None for ones) and
-    summed in float32. A rank that y does not hold adds nothing."""
+    summed in float32. A rank that y does not hold adds nothing. The result
+    carries no autograd history: combine_rows_grad is its gradient."""
     _dev(y)
     rows, width = _rows(y, "y")
     tokens, per = _routed(ranks, y, None)
