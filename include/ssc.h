@@ -499,6 +499,130 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
                     const float *top_p, const float *min_p, int32_t *tokens, int32_t *kept,
                     float *logprobs, void *scratch, size_t scratch_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Before the grouping: the router of a mixture of experts. Conventions of the
+ * row calls above; rows of logits may lie apart (row t at logits + t * stride
+ * elements, stride >= experts). 1 <= experts <= 1024, 1 <= per <= experts and
+ * per <= 64. */
+
+/* Scratch bytes of ssc_route_rows with its balance (0 without). */
+size_t ssc_route_scratch_bytes(int64_t tokens, int64_t experts);
+
+/* The experts of each token: ids[t, :] (tokens x per) are the experts of its
+ * `per` largest logits, largest first, equal ones by index, and weights[t, :]
+ * their shares of the softmax over the row, with `normalize` divided by their
+ * sum. A logit of NaN or -infinity is no expert, and beside one of +infinity no
+ * other is (those of +infinity weigh the same); places that a row has no expert
+ * for get id -1 and weight 0. A token with live[t] == 0 (nullable: all live) has
+ * no expert.
+ * The balance (counts, share and loss, all three or none) over the n tokens with
+ * an expert, p their softmax:
+ *   counts[e]  = assignments of expert e, for e < experts; counts[experts] = n
+ *   share[e]   = mean of p[t, e] over them (0 for n = 0)
+ *   loss       = experts * sum over e of counts[e] / (per * n) * share[e]: 1 where
+ *                tokens fall evenly (0 for n = 0)
+ * Sums over tokens are fp32 up to 64 rows of a lane and fp64 beyond. */
+int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
+                   const uint8_t *live, int64_t per, int normalize, int32_t *ids, float *weights,
+                   int32_t *counts, float *share, float *loss, void *scratch, size_t scratch_bytes,
+                   void *stream);
+
+/* The gradient with respect to the logits (dlogits: tokens x experts of dtype,
+ * contiguous) of <dweights, weights> + dloss * loss, given the ids that
+ * ssc_route_rows gave. dweights (with ids) and dloss (one value in device memory,
+ * with counts) are nullable, each for 0. counts may be those of several calls
+ * added up, n among them: the loss is then that of all of them. As in the
+ * forward pass, counts are constants. Ids outside [0, experts) add nothing, one
+ * that a row names twice counts twice; rows of tokens that are not live or have no
+ * expert are zeros. */
+int ssc_route_rows_grad(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
+                        const uint8_t *live, const int32_t *ids, int64_t per, int normalize,
+                        const float *dweights, const int32_t *counts, const float *dloss,
+                        void *dlogits, void *stream);
+
+/* ------------------------------------------------------------------------
+ * After the choice of tokens: drafts verified. */
+
+/* Scratch bytes of ssc_verify_rows: about 8 for each 1024 tokens of the
+ * vocabulary and row. */
+size_t ssc_verify_scratch_bytes(int64_t rows, int64_t vocab);
+
+/* Drafted tokens held against the probabilities of the model that they were
+ * drafted for. probs holds drafts + 1 rows of `vocab` probabilities for each of
+ * `rows` sequences (row i of sequence b at probs + b * stride_row + i *
+ * stride_place elements), draft_probs the `drafts` rows that the drafts were drawn
+ * by, with strides of its own (nullable: drafted without chance, probability 1);
+ * drafted is rows x drafts, u rows x (drafts + 1) of [0, 1). lengths[b] (nullable:
+ * drafts) is the number of drafts of a sequence, held to [0, drafts].
+ * Draft i stands if all before it do and u[b, i] * q_i(x_i) < p_i(x_i); a token
+ * outside the vocabulary falls. With a the number that stand, one more token is
+ * drawn by weights w: max(p_a - q_a, 0) where draft a fell (p_a without x_a if
+ * draft_probs is NULL; p_a, where none of these is above 0), p_a where all stood. It
+ * is the first index at which the running sum of w exceeds u[b, drafts] times
+ * their sum. Then
+ *   tokens[b, :]  = the a drafts, the drawn token, -1 for the rest (rows x (drafts + 1))
+ *   accepted[b]   = a
+ * Probabilities need not sum to 1; what is not above 0 or not finite weighs
+ * nothing, and a sequence without weights draws -1. A u outside [0, 1) is taken as
+ * the nearest in it (NaN as 0). Products, differences and sums are fp64, in an
+ * order that the sizes fix: a border that lies within some 2^-50 of their sum may fall on
+ * either side. 1 <= vocab <= 2^22, at most 65,535 rows and 2^20 drafts. */
+int ssc_verify_rows_i32(const void *probs, int dtype, int64_t rows, int64_t drafts, int64_t vocab,
+                        int64_t stride_row, int64_t stride_place, const int32_t *drafted,
+                        const void *draft_probs, int64_t draft_stride_row, int64_t draft_stride_place,
+                        const float *u, const int32_t *lengths, int32_t *tokens, int32_t *accepted,
+                        void *scratch, size_t scratch_bytes, void *stream);
+int ssc_verify_rows_i64(const void *probs, int dtype, int64_t rows, int64_t drafts, int64_t vocab,
+                        int64_t stride_row, int64_t stride_place, const int64_t *drafted,
+                        const void *draft_probs, int64_t draft_stride_row, int64_t draft_stride_place,
+                        const float *u, const int32_t *lengths, int32_t *tokens, int32_t *accepted,
+                        void *scratch, size_t scratch_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A cache cut to the rows that were attended to most. Caches are batch x heads x
+ * capacity (x width) with strides in elements for all but the last dimension,
+ * which is contiguous; strides are not negative, and what a call writes does not
+ * overlap itself. At most 65,535 batch * heads and 2^31 - 4097 positions.
+ * lengths[b] (nullable: all) is the number of positions in use, held to what there
+ * is. */
+
+/* The attention weights that each cached position got, added up: for i <
+ * min(length, lengths[b])
+ *   scores[b, h, i] = decay * scores[b, h, i] + sum of weights[b, g, q, i]
+ * over the heads g in [h * group, (h + 1) * group) and all queries. Of the last
+ * `fresh` of these positions (new ones) the score is not read but taken as 0.
+ * Positions past them are left as they were. A weight of NaN adds nothing. weights
+ * is batch x (heads * group) x queries x length, length <= capacity. */
+int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t capacity,
+                           int64_t score_stride_batch, int64_t score_stride_head, const void *weights,
+                           int dtype, int64_t group, int64_t queries, int64_t length,
+                           int64_t weight_stride_batch, int64_t weight_stride_head,
+                           int64_t weight_stride_query, const int32_t *lengths, int64_t fresh,
+                           float decay, void *stream);
+
+/* The positions that stay when every head is cut to `keep` rows: kept (batch x
+ * heads x keep, contiguous) holds them increasing, -1 behind them, and counts
+ * (batch x heads) their number. A sequence of up to `keep` positions keeps all; a
+ * longer one its `first` first and `recent` last, and of the others those with the
+ * largest scores, of equal ones the first (NaN is the lowest). first + recent <=
+ * keep <= capacity, keep >= 1. The selection and compaction of
+ * ssc_select_index_f32 with a threshold that is found. */
+int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t capacity,
+                   int64_t score_stride_batch, int64_t score_stride_head, const int32_t *lengths,
+                   int64_t keep, int64_t first, int64_t recent, int32_t *kept, int32_t *counts,
+                   void *stream);
+
+/* Rows of a cache moved together: out[b, h, s, :] = cache[b, h, kept[b, h, s], :]
+ * for s < keep, bit for bit, for elements of 1, 2, 4 or 8 bytes. Slots whose position
+ * lies outside [0, capacity) are not written. out may be the cache itself (the same
+ * address and strides): then positions that lie before their slot, which
+ * ssc_evict_rows gives none of, are not moved. Any other overlap is an error. */
+int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t heads, int64_t capacity,
+                  int64_t width, int64_t cache_stride_batch, int64_t cache_stride_head,
+                  int64_t cache_stride_row, const int32_t *kept, int64_t keep, void *out,
+                  int64_t out_stride_batch, int64_t out_stride_head, int64_t out_stride_row,
+                  void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssc_status_str(int status);
 

@@ -83,6 +83,15 @@ SIGNATURES = {
     "ssc_combine_rows_grad": (_INT, [_P, _P, _INT, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
     "ssc_sample_scratch_bytes": (_SZ, [_I64, _I64]),
     "ssc_sample_rows": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_route_scratch_bytes": (_SZ, [_I64, _I64]),
+    "ssc_route_rows": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_route_rows_grad": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _I64, _INT, _P, _P, _P, _P, _P]),
+    "ssc_verify_scratch_bytes": (_SZ, [_I64, _I64]),
+    "ssc_verify_rows_i32": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_verify_rows_i64": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ssc_accumulate_weights": (_INT, [_P] + [_I64] * 5 + [_P, _INT] + [_I64] * 6 + [_P, _I64, _F32, _P]),
+    "ssc_evict_rows": (_INT, [_P] + [_I64] * 5 + [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ssc_move_rows": (_INT, [_P, _INT] + [_I64] * 7 + [_P, _I64, _P] + [_I64] * 3 + [_P]),
     "ssc_status_str": (ctypes.c_char_p, [_INT]),
     "ssc_last_hip_error": (_INT, []),
 }
@@ -927,3 +936,255 @@ def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor
     _row_call("ssc_sample_rows", logits, logits, DTYPE[logits.dtype], rows, vocab, stride, *settings, tokens, kept,
               logprobs, scratch, _numel(scratch))
     return tokens, kept, logprobs
+
+
+# ---- the router before the grouping ---------------------------------------
+
+
+def _view(t, name: str, dims: int, dtypes, like: torch.Tensor | None = None) -> torch.Tensor:
+    """Checks a GPU tensor of `dims` dimensions whose last is contiguous and
+    whose others may lie apart: on like's device, of one of `dtypes` (None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU (no CPU path)")
+    if like is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, the input on {like.device}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be of dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {dims} dimensions, not {t.dim()}")
+    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t
+
+
+def _live(live, like: torch.Tensor, tokens: int) -> torch.Tensor | None:
+    if live is None:
+        return None
+    _need(live, "live", like, (torch.bool, torch.uint8), tokens)
+    if live.numel() != tokens:
+        raise ValueError("live holds one value a token")
+    return live
+
+
+def route_scratch_bytes(tokens: int, experts: int) -> int:
+    return int(lib().ssc_route_scratch_bytes(tokens, experts))
+
+
+def route_rows(logits: torch.Tensor, per: int, *, normalize: bool = True, live: torch.Tensor | None = None,
+               balance: bool = False, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+               counts: torch.Tensor | None = None, share: torch.Tensor | None = None,
+               loss: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
+    """(ids, weights), with balance=True (ids, weights, counts, share, loss): the
+    router in front of group_by_key and combine_rows. ids (tokens, per; int32) are
+    the experts of each token's `per` largest logits (tokens, experts), largest
+    first, equal ones by index; weights (float32) their shares of the softmax over
+    the row, normalize=True divided by their sum. Places without an expert (of NaN
+    and -infinity, and of tokens whose `live` is false) have id -1 and weight 0.
+    counts (experts + 1; int32) holds each expert's assignments and, last, the
+    number n of tokens with an expert; share (experts; float32) the mean softmax
+    over these; loss (1; float32) experts * sum of counts / (per * n) * share, 1
+    where tokens fall evenly. The rows may lie apart. No result carries autograd
+    history: route_rows_grad is the gradient."""
+    _view(logits, "logits", 2, DTYPE)
+    tokens, experts = logits.shape
+    stride = logits.stride(0) if tokens > 1 else max(experts, 1)
+    if stride < experts:
+        raise ValueError("rows of logits do not overlap")
+    if not 1 <= per <= experts:
+        raise ValueError(f"per must be in [1, {experts}], not {per}")
+    live = _live(live, logits, tokens)
+    ids = (logits.new_empty((tokens, per), dtype=torch.int32) if ids is None
+           else _shaped(_need(ids, "ids", logits, (torch.int32,), tokens * per), tokens, per))
+    weights = (logits.new_empty((tokens, per), dtype=torch.float32) if weights is None
+               else _shaped(_need(weights, "weights", logits, (torch.float32,), tokens * per), tokens, per))
+    if balance:
+        counts, share, loss = (
+            logits.new_empty(n, dtype=dt) if t is None else _shaped(_need(t, name, logits, (dt,), n), n)
+            for t, name, dt, n in ((counts, "counts", torch.int32, experts + 1), (share, "share", torch.float32, experts),
+                                   (loss, "loss", torch.float32, 1)))
+        scratch = _work_bytes(scratch, logits, route_scratch_bytes(tokens, experts))
+    elif counts is not None or share is not None or loss is not None:
+        raise ValueError("counts, share and loss come with balance=True")
+    else:
+        scratch = None
+    _row_call("ssc_route_rows", logits, logits, DTYPE[logits.dtype], tokens, experts, stride, live, per, int(normalize),
+              ids, weights, counts, share, loss, scratch, _numel(scratch))
+    return (ids, weights, counts, share, loss) if balance else (ids, weights)
+
+
+def route_rows_grad(logits: torch.Tensor, ids: torch.Tensor | None, dweights: torch.Tensor | None, *,
+                    normalize: bool = True, live: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                    dloss: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of route_rows with respect to the logits, (tokens, experts) of
+    their type: of the weights by dweights (tokens, per; float32; None for 0) with
+    the ids that route_rows gave, and of the loss by dloss (1; float32; None for 0)
+    with its counts, which are constants, and may be those of several calls added
+    up. normalize and live as in route_rows."""
+    _view(logits, "logits", 2, DTYPE)
+    tokens, experts = logits.shape
+    stride = logits.stride(0) if tokens > 1 else max(experts, 1)
+    if stride < experts:
+        raise ValueError("rows of logits do not overlap")
+    per = 1
+    if ids is not None:
+        _need(ids, "ids", logits, (torch.int32,), 0)
+        if ids.dim() != 2 or ids.shape[0] != tokens:
+            raise ValueError("ids is (tokens, per)")
+        per = ids.shape[1]
+    elif dweights is not None:
+        raise ValueError("dweights comes with ids")
+    if dweights is not None:
+        _need(dweights, "dweights", logits, (torch.float32,), 0)
+        if dweights.shape != ids.shape:
+            raise ValueError("one gradient per weight")
+    if (counts is None) != (dloss is None):
+        raise ValueError("dloss comes with counts")
+    if counts is not None:
+        _need(counts, "counts", logits, (torch.int32,), experts + 1)
+        if counts.numel() != experts + 1:
+            raise ValueError("counts holds experts + 1 values")
+        _need(dloss, "dloss", logits, (torch.float32,), 1)
+    out = (logits.new_empty((tokens, experts)) if out is None
+           else _shaped(_need(out, "out", logits, (logits.dtype,), tokens * experts), tokens, experts))
+    _row_call("ssc_route_rows_grad", logits, logits, DTYPE[logits.dtype], tokens, experts, stride,
+              _live(live, logits, tokens), ids, per, int(normalize), dweights, counts, dloss, out)
+    return out
+
+
+# ---- drafts verified, after the choice of tokens ---------------------------
+
+
+def verify_scratch_bytes(rows: int, vocab: int) -> int:
+    return int(lib().ssc_verify_scratch_bytes(rows, vocab))
+
+
+def verify_rows(probs: torch.Tensor, drafted: torch.Tensor, u: torch.Tensor, draft_probs: torch.Tensor | None = None, *,
+                lengths: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                accepted: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
+    """(tokens, accepted): drafted tokens (rows, drafts; int32 or int64) held
+    against the target's probabilities (rows, drafts + 1, vocab), so that the
+    tokens come as if drawn by these alone, from random numbers u (rows, drafts +
+    1; float32, [0, 1)). draft_probs (rows, drafts, vocab; of probs' type) is what
+    the drafts were drawn by, None for drafts without chance; lengths (rows;
+    int32) the number of drafts of each row. accepted (rows; int32) drafts stand;
+    tokens (rows, drafts + 1; int32) holds them, one token drawn after them, and
+    -1. The first two dimensions of the probabilities may lie apart;
+    include/ssc.h states the rules."""
+    _view(probs, "probs", 3, DTYPE)
+    rows, places, vocab = probs.shape
+    drafts = places - 1
+    if drafts < 0:
+        raise ValueError("probs holds one row more than there are drafts")
+    name = "ssc_verify_rows_" + _ids(drafted, "drafted") if isinstance(drafted, torch.Tensor) else ""
+    _need(drafted, "drafted", probs, None, 0)
+    if drafted.shape != (rows, drafts):
+        raise ValueError(f"drafted is {(rows, drafts)}, not {tuple(drafted.shape)}")
+    _need(u, "u", probs, (torch.float32,), 0)
+    if u.shape != (rows, places):
+        raise ValueError(f"u is {(rows, places)}, not {tuple(u.shape)}")
+    strides = 0, 0
+    if draft_probs is not None:
+        _view(draft_probs, "draft_probs", 3, (probs.dtype,), probs)
+        if draft_probs.shape != (rows, drafts, vocab):
+            raise ValueError(f"draft_probs is {(rows, drafts, vocab)}, not {tuple(draft_probs.shape)}")
+        strides = draft_probs.stride(0), draft_probs.stride(1)
+        if drafts == 0:
+            draft_probs = None
+    if lengths is not None:
+        _need(lengths, "lengths", probs, (torch.int32,), rows)
+        if lengths.numel() != rows:
+            raise ValueError("lengths holds one value a row")
+    tokens = (probs.new_empty((rows, places), dtype=torch.int32) if tokens is None
+              else _shaped(_need(tokens, "tokens", probs, (torch.int32,), rows * places), rows, places))
+    accepted = (probs.new_empty(rows, dtype=torch.int32) if accepted is None
+                else _shaped(_need(accepted, "accepted", probs, (torch.int32,), rows), rows))
+    scratch = _work_bytes(scratch, probs, verify_scratch_bytes(rows, vocab))
+    _row_call(name, probs, probs, DTYPE[probs.dtype], rows, drafts, vocab, probs.stride(0), probs.stride(1), drafted,
+              draft_probs, *strides, u, lengths, tokens, accepted, scratch, _numel(scratch))
+    return tokens, accepted
+
+
+# ---- a cache cut to the rows that were attended to most --------------------
+
+
+def _lengths(lengths, like: torch.Tensor, batch: int) -> torch.Tensor | None:
+    if lengths is not None:
+        _need(lengths, "lengths", like, (torch.int32,), batch)
+        if lengths.numel() != batch:
+            raise ValueError("lengths holds one value a sequence")
+    return lengths
+
+
+def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: torch.Tensor | None = None,
+                       fresh: int = 0, decay: float = 1.0) -> torch.Tensor:
+    """Adds to scores (batch, heads, capacity; float32, in place, and returned) the
+    attention weights that each cached position got: weights (batch, heads * group,
+    queries, length) of any row type, summed over the queries and over the group of
+    heads that share a cache head. The earlier score is multiplied by decay; of the
+    last `fresh` positions of each sequence (lengths: batch; int32; None for length)
+    it is not read but taken as 0. Positions past a sequence are left as they were.
+    A weight of NaN adds nothing. Both may lie apart in all but the last dimension."""
+    _view(scores, "scores", 3, (torch.float32,))
+    _view(weights, "weights", 4, DTYPE, scores)
+    batch, heads, capacity = scores.shape
+    count, length = weights.shape[1], weights.shape[3]
+    if weights.shape[0] != batch or heads < 1 or count < 1 or count % heads or length > capacity:
+        raise ValueError("weights is (batch, heads * group, queries, up to capacity)")
+    if fresh < 0:
+        raise ValueError("fresh is not negative")
+    _row_call("ssc_accumulate_weights", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
+              weights, DTYPE[weights.dtype], count // heads, weights.shape[2], length, weights.stride(0),
+              weights.stride(1), weights.stride(2), _lengths(lengths, scores, batch), fresh, float(decay))
+    return scores
+
+
+def evict_rows(scores: torch.Tensor, keep: int, *, first: int = 0, recent: int = 0,
+               lengths: torch.Tensor | None = None, kept: torch.Tensor | None = None,
+               counts: torch.Tensor | None = None):
+    """(kept, counts): the positions that stay when each head of a cache is cut to
+    `keep` rows, by scores (batch, heads, capacity; float32): of a sequence longer
+    than that (lengths: batch; int32; None for capacity) the `first` first, the
+    `recent` last, and the largest of the others, of equal ones the first. kept
+    (batch, heads, keep; int32) holds them increasing, -1 behind them, counts
+    (batch, heads; int32) their number. scores may lie apart in all but the last
+    dimension. move_rows takes a cache's rows, and the scores, there."""
+    _view(scores, "scores", 3, (torch.float32,))
+    batch, heads, capacity = scores.shape
+    if not 1 <= keep <= capacity:
+        raise ValueError(f"keep must be in [1, {capacity}], not {keep}")
+    if first < 0 or recent < 0 or first + recent > keep:
+        raise ValueError("first and recent are not negative, and keep holds both")
+    kept = (scores.new_empty((batch, heads, keep), dtype=torch.int32) if kept is None
+            else _shaped(_need(kept, "kept", scores, (torch.int32,), batch * heads * keep), batch, heads, keep))
+    counts = (scores.new_empty((batch, heads), dtype=torch.int32) if counts is None
+              else _shaped(_need(counts, "counts", scores, (torch.int32,), batch * heads), batch, heads))
+    _row_call("ssc_evict_rows", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
+              _lengths(lengths, scores, batch), keep, first, recent, kept, counts)
+    return kept, counts
+
+
+def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[b, h, s] = cache[b, h, kept[b, h, s]]: the rows of a cache (batch, heads,
+    capacity, width; elements of 1, 2, 4 or 8 bytes) that evict_rows keeps, moved
+    together. Without out in place, and the cache is returned; otherwise the part
+    of out (batch, heads, at least keep, width) that holds them. Slots whose
+    position lies outside the cache are not written. All but the last dimension may
+    lie apart; scores move as scores.unsqueeze(3)."""
+    _view(cache, "cache", 4, None)
+    batch, heads, capacity, width = cache.shape
+    _need(kept, "kept", cache, (torch.int32,), 0)
+    if kept.dim() != 3 or kept.shape[0] != batch or kept.shape[1] != heads:
+        raise ValueError("kept is (batch, heads, keep)")
+    keep = kept.shape[2]
+    to = cache
+    if out is not None:
+        to = out = _view(out, "out", 4, (cache.dtype,), cache)
+        if out.shape[0] != batch or out.shape[1] != heads or out.shape[3] != width or out.shape[2] < keep:
+            raise ValueError("out is (batch, heads, at least keep, width)")
+        if out.shape[2] != keep:
+            out = out[:, :, :keep]
+    _row_call("ssc_move_rows", cache, cache, cache.element_size(), batch, heads, capacity, width, cache.stride(0),
+              cache.stride(1), cache.stride(2), kept, keep, to, to.stride(0), to.stride(1), to.stride(2))
+    return cache if out is None else out

@@ -24,7 +24,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCE = "ssc.hip"                          # its code follows the test builds' switches
-SHARED_SOURCES = ("rows.hip", "sample.hip")  # the same in every build
+SHARED_SOURCES = ("rows.hip", "sample.hip", "route.hip", "verify.hip", "cache.hip")  # the same in every build
 LIB = os.path.join(PKG, "libssc.so")
 PERTURB_LIB = os.path.join(PKG, "libssc_perturb.so")
 STRESS_LIB = os.path.join(PKG, "libssc_stress.so")

@@ -1007,9 +1007,6 @@ int group_impl(const K *keys, int64_t n, int64_t groups, int32_t *order, int32_t
     return p.passes > 1 ? launch_offsets(sorted, un, ug, offsets, s) : SSC_OK;
 }
 
-size_t elem_bytes(int dtype) { return dtype == SSC_F32 ? 4 : 2; }
-bool dtype_ok(int dtype) { return dtype == SSC_F32 || dtype == SSC_BF16 || dtype == SSC_F16; }
-
 // Calls f with the element type of dtype and whether a row holds a 16-byte chunk.
 template <class F>
 int with_type(int dtype, int64_t width, F f) {

@@ -86,4 +86,57 @@ bool spans_overlap(const Span (&a)[N]) {
     return false;
 }
 
+inline size_t elem_bytes(int dtype) { return dtype == SSC_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == SSC_F32 || dtype == SSC_BF16 || dtype == SSC_F16; }
+
+// Calls f with a value of the element type of dtype (an ssc_dtype).
+template <class F>
+int with_dtype(int dtype, F f) {
+    switch (dtype) {
+    case SSC_F32: return f(float{});
+    case SSC_BF16: return f(__bf16{});
+    default: return f(_Float16{});
+    }
+}
+
+// A view of `dims` nested sizes with strides in elements, the innermost
+// contiguous: the elements from its first to past its last (0 for an empty
+// one), and whether no two of its indexes share an element.
+template <int DIMS>
+struct View {
+    int64_t size[DIMS], stride[DIMS];
+
+    bool strides_ok() const {  // products of sizes and strides fit into 62 bits
+        for (int i = 0; i < DIMS; ++i)
+            if (stride[i] < 0 || stride[i] > (int64_t{1} << 46) || size[i] > INT32_MAX) return false;
+        for (int i = 0; i < DIMS; ++i)
+            if (size[i] > 1 && static_cast<__int128>(size[i]) * stride[i] > (int64_t{1} << 60)) return false;
+        return true;
+    }
+    int64_t extent() const {
+        int64_t n = 1;
+        for (int i = 0; i < DIMS; ++i) {
+            if (size[i] == 0) return 0;
+            n += (size[i] - 1) * stride[i];
+        }
+        return n;
+    }
+    bool distinct() const {
+        int64_t covered = 1;  // elements spanned by the dimensions of smaller strides
+        bool used[DIMS] = {};
+        for (int i = 0; i < DIMS; ++i) {
+            int next = -1;
+            for (int j = 0; j < DIMS; ++j)
+                if (!used[j] && (next < 0 || stride[j] < stride[next] ||
+                                 (stride[j] == stride[next] && size[j] < size[next])))
+                    next = j;
+            used[next] = true;
+            if (size[next] <= 1) continue;
+            if (stride[next] < covered) return false;
+            covered += (size[next] - 1) * stride[next];
+        }
+        return true;
+    }
+};
+
 }  // namespace ssc

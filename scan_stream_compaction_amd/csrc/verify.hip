@@ -1,0 +1,418 @@
+// Drafted tokens held against the probabilities of the model that they were
+// drafted for, from given random numbers: HIP kernels for MI355X (gfx950) and
+// their part of the C ABI in include/ssc.h.
+//
+// Draft i of a sequence stands while u_i * q_i(x_i) < p_i(x_i); after the a
+// drafts that stand one token is drawn by the weights max(p_a - q_a, 0), after
+// all of them by p_a: the first index at which their running sum exceeds
+// u_last times their sum. The tokens then come as from p alone. Of the (drafts
+// + 1) rows of a sequence one is read, beside 2 * drafts single values.
+//
+// Two launches: every wavefront finds a (a few dependent loads) and sums
+// segments of 1024 weights; then a workgroup a sequence finds the segment by a
+// scan of the sums, and the token in it by reading it again. Sums are fp64, in
+// an order that the sizes fix: a border of u that fp32 sums would miss once in
+// some hundred rows (131,072 borders, 1e-8 of the sum each) is met.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssc.h"
+#include "ssc_device.h"
+#include "ssc_host.h"
+
+namespace ssc {
+namespace {
+
+constexpr int kSeg = 1024;             // weights of a segment: 16 a lane
+constexpr int kEach = kSeg / kWave;
+constexpr int kSumBlock = 256;
+constexpr int kSumWaves = kSumBlock / kWave;
+constexpr int kDrawBlock = 256;
+constexpr int64_t kVerifyVocabMax = int64_t{1} << 22;
+constexpr int kSegsMax = static_cast<int>(kVerifyVocabMax / kSeg);
+
+struct VerifyState {
+    int32_t accepted, length;
+};
+
+struct VerifyArgs {
+    const void *probs, *draft;  // draft null: a drafted token has probability 1
+    int64_t row, place, draft_row, draft_place;  // strides
+    const void *ids;
+    const float *u;
+    const int32_t *lengths;
+    int drafts, vocab, segs;
+    int32_t *tokens, *accepted;
+    VerifyState *state;  // [rows]
+    double *sums;        // [rows][segs]
+};
+
+// A random number outside [0, 1) as the nearest in it, NaN as 0.
+__device__ __forceinline__ float unit(float u) { return fminf(fmaxf(u, 0.0f), 0x1.fffffep-1f); }
+
+// How many drafts stand, by every wavefront for itself.
+template <class T, class I>
+__device__ __forceinline__ VerifyState drafts_that_stand(const VerifyArgs &a, int64_t b) {
+    int length = a.drafts;
+    if (a.lengths != nullptr) {
+        const int l = a.lengths[b];
+        length = l < 0 ? 0 : (l < a.drafts ? l : a.drafts);
+    }
+    for (int base = 0; base < length; base += kWave) {
+        const int i = base + lane_id();
+        bool falls = false;
+        if (i < length) {
+            const int64_t x = static_cast<const I *>(a.ids)[b * a.drafts + i];
+            const bool token = x >= 0 && x < a.vocab;
+            const int64_t at = token ? x : 0;
+            const double p = static_cast<float>(static_cast<const T *>(a.probs)[b * a.row + i * a.place + at]);
+            const double q = a.draft != nullptr ? static_cast<float>(static_cast<const T *>(
+                                                      a.draft)[b * a.draft_row + i * a.draft_place + at])
+                                                : 1.0f;
+            const double u = unit(a.u[b * (a.drafts + 1) + i]);
+            falls = !(token && u * q < p);
+        }
+        const uint64_t fallen = ballot(falls);
+        if (fallen != 0) return {base + __builtin_ctzll(fallen), length};
+    }
+    return {length, length};
+}
+
+// The weights that the token is drawn by. Neither a value that is not above 0
+// nor one that is not finite weighs anything.
+template <class T>
+struct Weights {
+    const T *p, *q;  // q null: nothing taken away but `without`
+    int n, without;
+
+    static constexpr int kN = 16 / static_cast<int>(sizeof(T));
+    typedef T V __attribute__((ext_vector_type(kN)));
+    typedef uint32_t Raw __attribute__((ext_vector_type(4)));
+    typedef uint32_t RawAny __attribute__((ext_vector_type(4), aligned(2), may_alias));
+
+    template <class I>
+    __device__ __forceinline__ Weights(const VerifyArgs &a, int64_t b, const VerifyState &s, const I *ids)
+        : p(static_cast<const T *>(a.probs) + b * a.row + s.accepted * a.place), q(nullptr), n(a.vocab), without(-1) {
+        if (s.accepted < s.length) {
+            if (a.draft != nullptr)
+                q = static_cast<const T *>(a.draft) + b * a.draft_row + s.accepted * a.draft_place;
+            else {
+                const int64_t x = ids[b * a.drafts + s.accepted];
+                without = x >= 0 && x < n ? static_cast<int>(x) : -1;
+            }
+        }
+    }
+    __device__ static __forceinline__ double weight(double w) { return w > 0.0 && w < __builtin_inf() ? w : 0.0; }
+    // weights [i, i + kN); past the end 0
+    __device__ __forceinline__ void load(int i, double (&w)[kN]) const {
+        if (i + kN <= n) {
+            const V x = __builtin_bit_cast(V, static_cast<Raw>(*reinterpret_cast<const RawAny *>(p + i)));
+            if (q != nullptr) {
+                const V y = __builtin_bit_cast(V, static_cast<Raw>(*reinterpret_cast<const RawAny *>(q + i)));
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    w[e] = weight(static_cast<double>(static_cast<float>(x[e])) -
+                                  static_cast<double>(static_cast<float>(y[e])));
+            } else {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) w[e] = weight(static_cast<double>(static_cast<float>(x[e])));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                double v = 0.0;
+                if (i + e < n) {
+                    v = static_cast<float>(p[i + e]);
+                    if (q != nullptr) v -= static_cast<double>(static_cast<float>(q[i + e]));
+                }
+                w[e] = weight(v);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kN; ++e) w[e] = i + e == without ? 0.0 : w[e];
+    }
+};
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_move_f64(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+    const uint64_t hi = dpp_move<CTRL, ROW_MASK>(static_cast<uint32_t>(b >> 32));
+    const uint64_t lo = dpp_move<CTRL, ROW_MASK>(static_cast<uint32_t>(b));
+    return __longlong_as_double(static_cast<long long>(hi << 32 | lo));
+}
+// Inclusive scan over the wavefront, as wave_inclusive_scan (0 is its identity).
+__device__ __forceinline__ double wave_scan_f64(double v) {
+    v += dpp_move_f64<0x111, 0xf>(v);
+    v += dpp_move_f64<0x112, 0xf>(v);
+    v += dpp_move_f64<0x114, 0xf>(v);
+    v += dpp_move_f64<0x118, 0xf>(v);
+    v += dpp_move_f64<0x142, 0xa>(v);
+    v += dpp_move_f64<0x143, 0xc>(v);
+    return v;
+}
+
+// Sum of a segment's weights over the wavefront, in its last lane.
+template <class T>
+__device__ __forceinline__ double segment_sum(const Weights<T> &w, int seg) {
+    constexpr int kN = Weights<T>::kN;
+    double v[kEach / kN][kN], s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kEach / kN; ++j) w.load(seg * kSeg + (j * kWave + lane_id()) * kN, v[j]);
+#pragma unroll
+    for (int j = 0; j < kEach / kN; ++j) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) s += v[j][e];
+    }
+    return wave_scan_f64(s);
+}
+
+template <class T, class I>
+__global__ __launch_bounds__(kSumBlock) void verify_sum_kernel(VerifyArgs a) {
+    const int64_t b = blockIdx.y;
+    const VerifyState s = drafts_that_stand<T, I>(a, b);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.state[b] = s;
+    const Weights<T> w(a, b, s, static_cast<const I *>(a.ids));
+    const int step = static_cast<int>(gridDim.x) * kSumWaves;
+    for (int seg = static_cast<int>(blockIdx.x) * kSumWaves + static_cast<int>(uniform(threadIdx.x / kWave));
+         seg < a.segs; seg += step) {
+        const double sum = segment_sum(w, seg);
+        if (lane_id() == kWave - 1) a.sums[b * a.segs + seg] = sum;
+    }
+}
+
+// Where the running sum of n values first exceeds goal (-1: nowhere), and the
+// sum before that place; by a workgroup. A value that adds nothing is no place.
+constexpr int kDrawWaves = kDrawBlock / kWave;
+
+struct DrawShared {
+    double sums[kSegsMax];
+    double wave[kDrawWaves];
+    int first[kDrawWaves];
+};
+
+template <class T, class I>
+__global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
+    __shared__ DrawShared sh;
+    const int64_t b = blockIdx.x;
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const VerifyState s = a.state[b];
+    Weights<T> weights(a, b, s, static_cast<const I *>(a.ids));
+    const double u = unit(a.u[b * (a.drafts + 1) + a.drafts]);
+    for (int i = threadIdx.x; i < a.segs; i += kDrawBlock) sh.sums[i] = a.sums[b * a.segs + i];
+    __syncthreads();
+    // a thread runs over consecutive segments
+    const int each = (a.segs + kDrawBlock - 1) / kDrawBlock;
+    const int begin = static_cast<int>(threadIdx.x) * each;
+    const int end = begin + each < a.segs ? begin + each : a.segs;
+    double own, incl, before, total;
+    const auto scan = [&]() {
+        own = 0.0;
+        for (int i = begin; i < end; ++i) own += sh.sums[i];
+        incl = wave_scan_f64(own);
+        if (lane == kWave - 1) sh.wave[w] = incl;
+        __syncthreads();
+        before = 0.0;
+        total = 0.0;
+        for (int v = 0; v < kDrawWaves; ++v) {
+            if (v < w) before += sh.wave[v];
+            total += sh.wave[v];
+        }
+    };
+    scan();
+    if (!(total > 0.0) && s.accepted < s.length) {  // q covers p: the token is drawn by p itself
+        weights.q = nullptr;
+        weights.without = -1;
+        __syncthreads();
+        for (int seg = w; seg < a.segs; seg += kDrawWaves) {
+            const double sum = segment_sum(weights, seg);
+            if (lane == kWave - 1) sh.sums[seg] = sum;
+        }
+        __syncthreads();
+        scan();
+    }
+    const double goal = u * total;
+    // the first segment at whose end the running sum exceeds the goal, or the
+    // last that weighs anything (where rounding leaves none)
+    double run = before + incl - own;
+    int seg = -1, last = -1;
+    for (int i = begin; i < end; ++i) {
+        const double v = sh.sums[i];
+        run += v;
+        if (v > 0.0) last = i;
+        if (seg < 0 && v > 0.0 && run > goal) seg = i;
+    }
+    {
+        const uint64_t found = ballot(seg >= 0), any = ballot(last >= 0);
+        int first = -1;
+        if (found != 0)
+            first = __builtin_amdgcn_readlane(seg, __builtin_ctzll(found));
+        else if (any != 0)
+            first = -2 - __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(any));
+        if (lane == 0) sh.first[w] = first;
+    }
+    __syncthreads();
+    int at = -1, fallback = -1;
+    for (int v = 0; v < kDrawWaves; ++v) {
+        const int f = sh.first[v];
+        if (f >= 0 && at < 0) at = f;
+        if (f < -1) fallback = -2 - f;
+    }
+    if (at < 0) at = fallback;
+    int32_t token = -1;
+    if (at >= 0) {
+        // the sum before the segment, added up as the search did
+        const int owner = at / each;
+        double base = 0.0;
+        if (static_cast<int>(threadIdx.x) == owner) {
+            base = before + incl - own;
+            for (int i = begin; i < at; ++i) base += sh.sums[i];
+            sh.wave[0] = base;  // the waves' totals have been read: a barrier lies between
+        }
+        __syncthreads();
+        base = sh.wave[0];
+        if (w == 0) {
+            constexpr int kN = Weights<T>::kN;
+            double v[kEach / kN][kN], sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < kEach / kN; ++j) weights.load(at * kSeg + lane * kEach + j * kN, v[j]);
+#pragma unroll
+            for (int j = 0; j < kEach / kN; ++j) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) sum += v[j][e];
+            }
+            double r = base + wave_scan_f64(sum) - sum;
+            int first = -1, any = -1;
+#pragma unroll
+            for (int j = 0; j < kEach / kN; ++j) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    r += v[j][e];
+                    const int i = at * kSeg + lane * kEach + j * kN + e;
+                    if (v[j][e] > 0.0) any = i;
+                    if (first < 0 && v[j][e] > 0.0 && r > goal) first = i;
+                }
+            }
+            const uint64_t found = ballot(first >= 0), some = ballot(any >= 0);
+            if (found != 0)
+                token = __builtin_amdgcn_readlane(first, __builtin_ctzll(found));
+            else if (some != 0)
+                token = __builtin_amdgcn_readlane(any, 63 - __builtin_clzll(some));
+        }
+    }
+    if (w == 0) {
+        const I *ids = static_cast<const I *>(a.ids) + b * a.drafts;
+        for (int i = lane; i <= a.drafts; i += kWave)
+            a.tokens[b * (a.drafts + 1) + i] =
+                i < s.accepted ? static_cast<int32_t>(ids[i]) : (i == s.accepted ? token : -1);
+        if (lane == 0) a.accepted[b] = s.accepted;
+    }
+}
+
+// ============================================================ host side ---
+struct VerifyPlan {
+    int segs;
+    size_t sums, bytes;
+};
+VerifyPlan verify_plan(int64_t rows, int64_t vocab) {
+    VerifyPlan p{};
+    p.segs = static_cast<int>((vocab + kSeg - 1) / kSeg);
+    p.sums = (static_cast<size_t>(rows) * sizeof(VerifyState) + 15) / 16 * 16;
+    p.bytes = p.sums + static_cast<size_t>(rows) * p.segs * sizeof(double);
+    return p;
+}
+bool verify_sizes_ok(int64_t rows, int64_t vocab) {
+    return rows >= 0 && rows <= 65535 && vocab >= 1 && vocab <= kVerifyVocabMax;
+}
+
+template <class I>
+int verify_impl(const void *probs, int dtype, int64_t rows, int64_t drafts, int64_t vocab, int64_t row, int64_t place,
+                const I *ids, const void *draft, int64_t draft_row, int64_t draft_place, const float *u,
+                const int32_t *lengths, int32_t *tokens, int32_t *accepted, void *scratch, size_t scratch_bytes,
+                void *stream) {
+    if (!dtype_ok(dtype) || rows < 0 || drafts < 0 || vocab < 1) return SSC_ERR_ARG;
+    if (!verify_sizes_ok(rows, vocab) || drafts > (1 << 20)) return SSC_ERR_SIZE;
+    const View<3> p{{rows, drafts + 1, vocab}, {row, place, 1}};
+    const View<3> q{{rows, draft != nullptr ? drafts : 0, vocab}, {draft_row, draft_place, 1}};
+    if (!p.strides_ok() || (draft != nullptr && !q.strides_ok())) return SSC_ERR_ARG;
+    if (rows > 0 && (probs == nullptr || u == nullptr || tokens == nullptr || accepted == nullptr ||
+                     (drafts > 0 && ids == nullptr)))
+        return SSC_ERR_ARG;
+    const size_t es = elem_bytes(dtype);
+    if (!aligned(probs, es) || !aligned(draft, es) || !aligned(ids, sizeof(I)) || !aligned(u, 4) ||
+        !aligned(lengths, 4) || !aligned(tokens, 4) || !aligned(accepted, 4))
+        return SSC_ERR_ARG;
+    const VerifyPlan plan = verify_plan(rows, vocab);
+    if (rows > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < plan.bytes)) return SSC_ERR_SCRATCH;
+    const size_t n = static_cast<size_t>(rows);
+    const Span written[] = {{tokens, n * (drafts + 1) * 4}, {accepted, n * 4}, {scratch, plan.bytes}};
+    const Span read[] = {{probs, static_cast<size_t>(p.extent()) * es},
+                         {draft, static_cast<size_t>(q.extent()) * es},
+                         {ids, n * drafts * sizeof(I)},
+                         {u, n * (drafts + 1) * 4},
+                         {lengths, n * 4}};
+    if (spans_overlap(written)) return SSC_ERR_ALIAS;
+    for (const Span &x : written)
+        for (const Span &y : read)
+            if (overlap(x.p, x.bytes, y.p, y.bytes)) return SSC_ERR_ALIAS;
+    SSC_TRY(check_device());
+    if (rows == 0) return SSC_OK;
+    VerifyArgs a{};
+    a.probs = probs;
+    a.draft = draft;
+    a.row = row;
+    a.place = place;
+    a.draft_row = draft_row;
+    a.draft_place = draft_place;
+    a.ids = ids;
+    a.u = u;
+    a.lengths = lengths;
+    a.drafts = static_cast<int>(drafts);
+    a.vocab = static_cast<int>(vocab);
+    a.segs = plan.segs;
+    a.tokens = tokens;
+    a.accepted = accepted;
+    a.state = static_cast<VerifyState *>(scratch);
+    a.sums = reinterpret_cast<double *>(static_cast<char *>(scratch) + plan.sums);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int blocks = (plan.segs + kSumWaves - 1) / kSumWaves;
+    return with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((verify_sum_kernel<T, I>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(rows)),
+                           dim3(kSumBlock), 0, s, a);
+        SSC_TRY(launched());
+        hipLaunchKernelGGL((verify_draw_kernel<T, I>), dim3(static_cast<unsigned>(rows)), dim3(kDrawBlock), 0, s, a);
+        return launched();
+    });
+}
+
+}  // namespace
+}  // namespace ssc
+
+using namespace ssc;
+
+extern "C" {
+
+size_t ssc_verify_scratch_bytes(int64_t rows, int64_t vocab) {
+    return rows > 0 && verify_sizes_ok(rows, vocab) ? verify_plan(rows, vocab).bytes : 0;
+}
+
+int ssc_verify_rows_i32(const void *probs, int dtype, int64_t rows, int64_t drafts, int64_t vocab, int64_t stride_row,
+                        int64_t stride_place, const int32_t *drafted, const void *draft_probs, int64_t draft_stride_row,
+                        int64_t draft_stride_place, const float *u, const int32_t *lengths, int32_t *tokens,
+                        int32_t *accepted, void *scratch, size_t scratch_bytes, void *stream) {
+    return verify_impl(probs, dtype, rows, drafts, vocab, stride_row, stride_place, drafted, draft_probs,
+                       draft_stride_row, draft_stride_place, u, lengths, tokens, accepted, scratch, scratch_bytes,
+                       stream);
+}
+
+int ssc_verify_rows_i64(const void *probs, int dtype, int64_t rows, int64_t drafts, int64_t vocab, int64_t stride_row,
+                        int64_t stride_place, const int64_t *drafted, const void *draft_probs, int64_t draft_stride_row,
+                        int64_t draft_stride_place, const float *u, const int32_t *lengths, int32_t *tokens,
+                        int32_t *accepted, void *scratch, size_t scratch_bytes, void *stream) {
+    return verify_impl(probs, dtype, rows, drafts, vocab, stride_row, stride_place, drafted, draft_probs,
+                       draft_stride_row, draft_stride_place, u, lengths, tokens, accepted, scratch, scratch_bytes,
+                       stream);
+}
+
+}  // extern "C"
