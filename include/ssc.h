@@ -600,6 +600,10 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
                            int64_t weight_stride_query, const int32_t *lengths, int64_t fresh,
                            float decay, void *stream);
 
+/* Scratch bytes of ssc_evict_rows (0 for up to 16,384 positions): 16 KiB for each
+ * 8192 positions of a few heads, or each 32,768 of many. */
+size_t ssc_evict_scratch_bytes(int64_t batch, int64_t heads, int64_t capacity);
+
 /* The positions that stay when every head is cut to `keep` rows: kept (batch x
  * heads x keep, contiguous) holds them increasing, -1 behind them, and counts
  * (batch x heads) their number. A sequence of up to `keep` positions keeps all; a
@@ -610,7 +614,7 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
 int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t capacity,
                    int64_t score_stride_batch, int64_t score_stride_head, const int32_t *lengths,
                    int64_t keep, int64_t first, int64_t recent, int32_t *kept, int32_t *counts,
-                   void *stream);
+                   void *scratch, size_t scratch_bytes, void *stream);
 
 /* Rows of a cache moved together: out[b, h, s, :] = cache[b, h, kept[b, h, s], :]
  * for s < keep, bit for bit, for elements of 1, 2, 4 or 8 bytes. Slots whose position

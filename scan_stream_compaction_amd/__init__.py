@@ -90,7 +90,8 @@ SIGNATURES = {
     "ssc_verify_rows_i32": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "ssc_verify_rows_i64": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "ssc_accumulate_weights": (_INT, [_P] + [_I64] * 5 + [_P, _INT] + [_I64] * 6 + [_P, _I64, _F32, _P]),
-    "ssc_evict_rows": (_INT, [_P] + [_I64] * 5 + [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ssc_evict_scratch_bytes": (_SZ, [_I64, _I64, _I64]),
+    "ssc_evict_rows": (_INT, [_P] + [_I64] * 5 + [_P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
     "ssc_move_rows": (_INT, [_P, _INT] + [_I64] * 7 + [_P, _I64, _P] + [_I64] * 3 + [_P]),
     "ssc_status_str": (ctypes.c_char_p, [_INT]),
     "ssc_last_hip_error": (_INT, []),
@@ -1140,9 +1141,13 @@ def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: 
     return scores
 
 
+def evict_scratch_bytes(batch: int, heads: int, capacity: int) -> int:
+    return int(lib().ssc_evict_scratch_bytes(batch, heads, capacity))
+
+
 def evict_rows(scores: torch.Tensor, keep: int, *, first: int = 0, recent: int = 0,
                lengths: torch.Tensor | None = None, kept: torch.Tensor | None = None,
-               counts: torch.Tensor | None = None):
+               counts: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
     """(kept, counts): the positions that stay when each head of a cache is cut to
     `keep` rows, by scores (batch, heads, capacity; float32): of a sequence longer
     than that (lengths: batch; int32; None for capacity) the `first` first, the
@@ -1160,8 +1165,9 @@ def evict_rows(scores: torch.Tensor, keep: int, *, first: int = 0, recent: int =
             else _shaped(_need(kept, "kept", scores, (torch.int32,), batch * heads * keep), batch, heads, keep))
     counts = (scores.new_empty((batch, heads), dtype=torch.int32) if counts is None
               else _shaped(_need(counts, "counts", scores, (torch.int32,), batch * heads), batch, heads))
+    scratch = _work_bytes(scratch, scores, evict_scratch_bytes(batch, heads, capacity))
     _row_call("ssc_evict_rows", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
-              _lengths(lengths, scores, batch), keep, first, recent, kept, counts)
+              _lengths(lengths, scores, batch), keep, first, recent, kept, counts, scratch, _numel(scratch))
     return kept, counts
 
 

@@ -24,38 +24,51 @@ struct AccumulateArgs {
     float *scores;
     int64_t score_batch, score_head;
     const void *weights;
-    int64_t weight_batch, weight_head, weight_query;
+    int64_t weight_batch, weight_group, weight_head, weight_query;  // group: of the heads of a cache head
     const int32_t *lengths;
-    int heads, capacity, group, queries, length;
+    int length;
+    uint32_t group, queries;
     int64_t fresh;
     float decay;
 };
 
-template <class T, int WAVES>
+// EVEN: the rows of a cache head lie evenly apart (queries of one head)
+template <class T, int WAVES, bool EVEN>
 __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs a) {
     constexpr int kN = 16 / static_cast<int>(sizeof(T));
     constexpr int kFlight = 8;
     typedef T V __attribute__((ext_vector_type(kN)));
     typedef uint32_t Raw __attribute__((ext_vector_type(4)));
     typedef uint32_t RawAny __attribute__((ext_vector_type(4), aligned(2), may_alias));
+    typedef float Score __attribute__((ext_vector_type(4)));
+    typedef float ScoreAny __attribute__((ext_vector_type(4), aligned(4), may_alias));
     __shared__ float s_sum[WAVES > 1 ? WAVES - 1 : 1][WAVES > 1 ? kWave * kN : 1];
-    const int64_t bh = blockIdx.y;
-    const int64_t b = bh / a.heads, h = bh % a.heads;
+    const int64_t h = blockIdx.y, b = blockIdx.z;
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int lane = lane_id();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kWave * kN + lane * kN;
+    const T *from = static_cast<const T *>(a.weights) + b * a.weight_batch + h * a.weight_group + first;
+    float *to = a.scores + b * a.score_batch + h * a.score_head + first;
     int64_t len = a.length;
-    if (a.lengths != nullptr) len = a.lengths[b];
-    if (len > a.length) len = a.length;
-    const int64_t block_first = static_cast<int64_t>(blockIdx.x) * kWave * kN;
-    if (block_first >= len) return;
-    const int64_t first = block_first + lane * kN;
-    const T *from = static_cast<const T *>(a.weights) + b * a.weight_batch + h * a.group * a.weight_head + first;
+    if (a.lengths != nullptr) {
+        const int64_t l = a.lengths[b];
+        len = l < len ? l : len;
+    }
+    if (first - lane * kN >= len) return;
     const bool whole = first + kN <= a.length;
+    // the earlier scores are on their way while the weights are read
+    const int64_t old = len - a.fresh;  // positions with an earlier score
+    Score before[kN / 4];
+    const bool vector = first + kN <= len && first + kN <= old && w == 0;
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) {
+        before[i] = Score{0.0f, 0.0f, 0.0f, 0.0f};
+        if (vector) before[i] = *reinterpret_cast<const ScoreAny *>(to + 4 * i);
+    }
     float sum[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) sum[e] = 0.0f;
-    const uint32_t rows = static_cast<uint32_t>(a.group) * static_cast<uint32_t>(a.queries);
-    const uint32_t queries = static_cast<uint32_t>(a.queries);
+    const uint32_t rows = a.group * a.queries;
     // a weight that is no number (of a query whose mask left nothing) adds nothing
     const auto add = [&](const V &v) {
 #pragma unroll
@@ -64,21 +77,25 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
             sum[e] += x == x ? x : 0.0f;
         }
     };
-    const auto row = [&](uint32_t r) { return from + (r / queries) * a.weight_head + (r % queries) * a.weight_query; };
+    const auto row = [&](uint32_t r) {
+        if constexpr (EVEN) return from + r * a.weight_query;
+        return from + (r / a.queries) * a.weight_head + (r % a.queries) * a.weight_query;
+    };
     if (whole) {
         uint32_t r = w;
-        for (; r + (kFlight - 1) * WAVES < rows; r += kFlight * WAVES) {
-            Raw raw[kFlight];
+        const auto some = [&](auto count) {
+            constexpr int C = decltype(count)::value;
+            Raw raw[C];
 #pragma unroll
-            for (int j = 0; j < kFlight; ++j)
+            for (int j = 0; j < C; ++j)
                 raw[j] = __builtin_nontemporal_load(reinterpret_cast<const RawAny *>(row(r + j * WAVES)));
 #pragma unroll
-            for (int j = 0; j < kFlight; ++j) add(__builtin_bit_cast(V, raw[j]));
-        }
-        for (; r < rows; r += WAVES) {
-            const Raw raw = __builtin_nontemporal_load(reinterpret_cast<const RawAny *>(row(r)));
-            add(__builtin_bit_cast(V, raw));
-        }
+            for (int j = 0; j < C; ++j) add(__builtin_bit_cast(V, raw[j]));
+            r += C * WAVES;
+        };
+        while (r + (kFlight - 1) * WAVES < rows) some(std::integral_constant<int, kFlight>{});
+        if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
+        while (r < rows) some(std::integral_constant<int, 1>{});
     } else if (first < a.length) {
         for (uint32_t r = w; r < rows; r += WAVES) {
             const T *p = row(r);
@@ -100,25 +117,45 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
             for (int e = 0; e < kN; ++e) sum[e] += s_sum[v][e * kWave + lane];
         }
     }
-    float *to = a.scores + b * a.score_batch + h * a.score_head + first;
+    if (vector) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-        const int64_t i = first + e;
-        if (i >= len) continue;
-        const float old = i < len - a.fresh ? to[e] * a.decay : 0.0f;
-        to[e] = old + sum[e];
+        for (int i = 0; i < kN / 4; ++i) {
+            Score s;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(before[i][e], a.decay, sum[4 * i + e]);
+            *reinterpret_cast<ScoreAny *>(to + 4 * i) = s;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const int64_t i = first + e;
+            if (i < len) to[e] = i < old ? __builtin_fmaf(to[e], a.decay, sum[e]) : sum[e];
+        }
     }
 }
 
 // ------------------------------------------------------- which rows stay ---
-// A workgroup a row. The threshold is the `need`-th largest score, found by
-// its leading 11, 11 and 10 bits: counts by digit in LDS, a scan from the
-// largest digit down, then the digit's own members by the next one. What lies
-// above it stays, and of the scores equal to it the first ones. Wavefronts hold
-// consecutive positions, 64 at a time, so that a ballot ranks them.
+// The threshold is the `need`-th largest score, found by its leading 11, 11 and
+// 10 bits: counts by digit in LDS, a scan from the largest digit down, then the
+// digit's own members by the next one. What lies above it stays, and of the
+// scores equal to it the first ones. Wavefronts hold consecutive positions, 64
+// at a time, so that ballots rank them.
+//
+// Up to 32,768 positions a workgroup does all of a head, its scores in
+// registers. Longer heads, and those of a few that leave the chip empty, go over
+// several workgroups (splits) and four launches: a count by each digit, which
+// first joins the splits' counts of the one before, and the output.
 constexpr int kEvictBlock = 1024;
 constexpr int kEvictWaves = kEvictBlock / kWave;
 constexpr int kEvictBins = 2048;
+constexpr int kEvictPasses = 3;
+constexpr int kEvictHeld = 32 * kEvictBlock;  // positions of a head that one workgroup holds
+
+// What is known of the threshold: its leading digits, and how many of the
+// scores that share them stay. `all`: every one.
+struct Threshold {
+    uint32_t low, fixed, need, all;
+};
 
 struct EvictArgs {
     const float *scores;
@@ -127,6 +164,11 @@ struct EvictArgs {
     int heads;
     uint32_t capacity, keep, first, recent;
     int32_t *kept, *counts;
+    // of the splits
+    uint32_t splits, span;  // and positions of one, a multiple of kEvictTile
+    Threshold *found;       // [rows][passes]
+    uint32_t *before;       // [rows][splits] scores of earlier splits that stay, as far as known
+    uint32_t *hist;         // [2][rows][splits][bins] of this pass and the one before
 };
 
 // The score as an integer of the same order; NaN as the lowest, -0 as 0.
@@ -136,112 +178,135 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return x == x ? k : 0u;
 }
 
+__device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : (pass == 1 ? 10 : 0); }
+__device__ __forceinline__ uint32_t digit_bins(int pass) { return pass == 2 ? 1024u : 2048u; }
+
+// A head of the cache: its positions in use, and those that a score decides on.
+struct Head {
+    const float *scores;
+    int32_t *kept;
+    uint32_t len, begin, end, need;
+
+    __device__ __forceinline__ Head(const EvictArgs &a, int64_t h, int64_t b) {
+        const int64_t bh = b * a.heads + h;
+        scores = a.scores + b * a.score_batch + h * a.score_head;
+        kept = a.kept + bh * a.keep;
+        len = a.capacity;
+        if (a.lengths != nullptr) {
+            const int32_t l = a.lengths[b];
+            len = l < 0 ? 0u : (static_cast<uint32_t>(l) < a.capacity ? static_cast<uint32_t>(l) : a.capacity);
+        }
+        begin = a.first;
+        end = len - a.recent;  // used where len > keep
+        need = a.keep - a.first - a.recent;
+    }
+    __device__ __forceinline__ Threshold start() const { return {need == 0 ? ~0u : 0u, 0u, need, need == 0}; }
+    __device__ __forceinline__ bool open(uint32_t i) const { return i >= begin && i < end; }
+    __device__ __forceinline__ bool always(uint32_t i) const { return i < begin || (i >= end && i < len); }
+    // up to `keep` positions: all stay; by `stride` threads
+    __device__ __forceinline__ void keep_all(const EvictArgs &a, int64_t bh, uint32_t thread, uint32_t stride) const {
+        for (uint32_t s = thread; s < a.keep; s += stride) kept[s] = s < len ? static_cast<int32_t>(s) : -1;
+        if (thread == 0) a.counts[bh] = static_cast<int32_t>(len);
+    }
+};
+
 struct EvictShared {
     uint32_t hist[kEvictBins];
     uint32_t wave[kEvictWaves];
     uint32_t wave_equal[kEvictWaves];
-    uint32_t digit, above, inside;
+    uint32_t digit, above, inside, before;
 };
 
-// ITEMS: scores of a lane, held in registers; 0: read again each time.
+// Many scores may be equal (0 above all): the lanes that share the first active
+// lane's digit are counted by one add.
+__device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t d, bool counts) {
+    const uint64_t active = ballot(counts);
+    if (active == 0) return;
+    const int leader = __builtin_ctzll(active);
+    const uint32_t common = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(d), leader));
+    const uint64_t same = ballot(counts && d == common);
+    if (lane_id() == leader)
+        __hip_atomic_fetch_add(&hist[common], static_cast<uint32_t>(__builtin_popcountll(same)), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
+    else if (counts && d != common)
+        __hip_atomic_fetch_add(&hist[d], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// The digit that the need-th largest falls into; c0 and c1 are the counts of this
+// thread's bins, 2047 - 2 * thread and the one below. Every thread meets it.
+__device__ __forceinline__ void find_digit(EvictShared &sh, uint32_t c0, uint32_t c1, int pass, Threshold &t) {
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
+    const uint32_t incl = wave_inclusive_scan<SumU32>(c0 + c1);
+    if (lane_id() == kWave - 1) sh.wave[w] = incl;
+    __syncthreads();
+    const uint32_t totals = wave_inclusive_scan<SumU32>(lane_id() < kEvictWaves ? sh.wave[lane_id()] : 0u);
+    const uint32_t earlier =
+        w == 0 ? 0u : static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(totals), w - 1));
+    const uint32_t above = earlier + incl - c0 - c1;
+    if (above < t.need && t.need <= above + c0) {
+        sh.digit = top;
+        sh.above = above;
+        sh.inside = c0;
+    } else if (above + c0 < t.need && t.need <= above + c0 + c1) {
+        sh.digit = top - 1u;
+        sh.above = above + c0;
+        sh.inside = c1;
+    }
+    __syncthreads();
+    t.low |= sh.digit << digit_shift(pass);
+    t.fixed |= (digit_bins(pass) - 1u) << digit_shift(pass);
+    t.need -= sh.above;
+    t.all = t.need == sh.inside;
+}
+
+__device__ __forceinline__ bool better(const Threshold &t, uint32_t k) { return t.all ? k >= t.low : k > t.low; }
+
 template <int ITEMS>
 __global__ __launch_bounds__(kEvictBlock) void evict_kernel(EvictArgs a) {
     __shared__ EvictShared sh;
-    const int64_t bh = blockIdx.x;
-    const int64_t b = bh / a.heads, h = bh % a.heads;
-    const int lane = lane_id();
-    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    int32_t *kept = a.kept + bh * a.keep;
-    uint32_t len = a.capacity;
-    if (a.lengths != nullptr) {
-        const int32_t l = a.lengths[b];
-        len = l < 0 ? 0u : (static_cast<uint32_t>(l) < a.capacity ? static_cast<uint32_t>(l) : a.capacity);
-    }
-    if (len <= a.keep) {  // all stay
-        for (uint32_t s = threadIdx.x; s < a.keep; s += kEvictBlock) kept[s] = s < len ? static_cast<int32_t>(s) : -1;
-        if (threadIdx.x == 0) a.counts[bh] = static_cast<int32_t>(len);
+    const int64_t bh = static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
+    const Head head(a, blockIdx.x, blockIdx.y);
+    if (head.len <= a.keep) {
+        head.keep_all(a, bh, threadIdx.x, kEvictBlock);
         return;
     }
-    const float *scores = a.scores + b * a.score_batch + h * a.score_head;
-    const uint32_t begin = a.first, end = len - a.recent;  // those between stay by their score
-    uint32_t need = a.keep - a.first - a.recent;
-    const uint32_t sets = ITEMS > 0 ? ITEMS : (len + kEvictBlock - 1) / kEvictBlock;
-    const uint32_t base = static_cast<uint32_t>(w) * sets * kWave;
-    uint32_t held[ITEMS > 0 ? ITEMS : 1];
-    if constexpr (ITEMS > 0) {
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const uint32_t base = static_cast<uint32_t>(w) * ITEMS * kWave + lane;
+    uint32_t key[ITEMS];
+    {
         float x[ITEMS];
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            const uint32_t i = base + j * kWave + lane;
-            x[j] = i >= begin && i < end ? scores[i] : 0.0f;
+            const uint32_t i = base + j * kWave;
+            x[j] = head.open(i) ? head.scores[i] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) held[j] = score_key(x[j]);
+        for (int j = 0; j < ITEMS; ++j) key[j] = score_key(x[j]);
     }
-    // f(position, key, whether the score decides) for this lane's positions
-    const auto each = [&](auto f) {
-        if constexpr (ITEMS > 0) {
-#pragma unroll
-            for (int j = 0; j < ITEMS; ++j) {
-                const uint32_t i = base + j * kWave + lane;
-                f(i, held[j], i >= begin && i < end);
-            }
-        } else {
-            for (uint32_t j = 0; j < sets; ++j) {
-                const uint32_t i = base + j * kWave + lane;
-                const bool open = i >= begin && i < end;
-                f(i, open ? score_key(scores[i]) : 0u, open);
-            }
-        }
-    };
-    // scores from `low` on stay if all of a digit does; else those above, and
-    // `need` of those equal to it
-    uint32_t low = 0, fixed = 0;  // the digits found, and their bits
-    bool all = need == 0;
-    if (need == 0) low = 0xffffffffu;  // no score's
-    for (int pass = 0; pass < 3 && !all; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const uint32_t bins = pass == 2 ? 1024u : 2048u;
+    Threshold t = head.start();
+    for (int pass = 0; pass < kEvictPasses && !t.all; ++pass) {
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
         __syncthreads();
-        each([&](uint32_t, uint32_t k, bool open) {
-            if (open && (k & fixed) == low)
-                __hip_atomic_fetch_add(&sh.hist[(k >> shift) & (bins - 1u)], 1u, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
-        });
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+            count_digit(sh.hist, (key[j] >> digit_shift(pass)) & (digit_bins(pass) - 1u),
+                        head.open(base + j * kWave) && (key[j] & t.fixed) == t.low);
         __syncthreads();
-        // two bins a thread, the largest first
         const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
-        const uint32_t c0 = sh.hist[top], c1 = sh.hist[top - 1u];
-        const uint32_t incl = wave_inclusive_scan<SumU32>(c0 + c1);
-        if (lane == kWave - 1) sh.wave[w] = incl;
-        __syncthreads();
-        uint32_t above = incl - c0 - c1;
-        for (int v = 0; v < w; ++v) above += sh.wave[v];
-        if (above < need && need <= above + c0) {
-            sh.digit = top;
-            sh.above = above;
-            sh.inside = c0;
-        } else if (above + c0 < need && need <= above + c0 + c1) {
-            sh.digit = top - 1u;
-            sh.above = above + c0;
-            sh.inside = c1;
-        }
-        __syncthreads();
-        low |= sh.digit << shift;
-        fixed |= (bins - 1u) << shift;
-        need -= sh.above;
-        all = need == sh.inside;
+        find_digit(sh, sh.hist[top], sh.hist[top - 1u], pass, t);
     }
-    const auto better = [&](uint32_t k) { return all ? k >= low : k > low; };
     // the wavefront's share: those that stay in any case, and those equal
     uint32_t sure = 0, equal = 0;
-    each([&](uint32_t i, uint32_t k, bool open) {
-        const bool yes = i < begin || (i >= end && i < len) || (open && better(k));
-        const bool same = open && !all && k == low;
-        sure += static_cast<uint32_t>(__builtin_popcountll(ballot(yes)));
-        equal += static_cast<uint32_t>(__builtin_popcountll(ballot(same)));
-    });
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kWave;
+        const bool open = head.open(i);
+        sure += static_cast<uint32_t>(__builtin_popcountll(ballot(head.always(i) || (open && better(t, key[j])))));
+        equal += static_cast<uint32_t>(__builtin_popcountll(ballot(open && !t.all && key[j] == t.low)));
+    }
+    __syncthreads();
     if (lane == 0) {
         sh.wave[w] = sure;
         sh.wave_equal[w] = equal;
@@ -252,19 +317,172 @@ __global__ __launch_bounds__(kEvictBlock) void evict_kernel(EvictArgs a) {
         at += sh.wave[v];
         equals += sh.wave_equal[v];
     }
-    at += equals < need ? equals : need;
-    each([&](uint32_t i, uint32_t k, bool open) {
-        bool yes = i < begin || (i >= end && i < len) || (open && better(k));
-        const bool same = open && !all && k == low;
+    at += equals < t.need ? equals : t.need;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const uint32_t i = base + j * kWave;
+        const bool open = head.open(i);
+        const bool same = open && !t.all && key[j] == t.low;
         const uint64_t sames = ballot(same);
-        yes = yes || (same && equals + mbcnt64(sames) < need);
+        const bool yes = head.always(i) || (open && better(t, key[j])) || (same && equals + mbcnt64(sames) < t.need);
         equals += static_cast<uint32_t>(__builtin_popcountll(sames));
         const uint64_t yeses = ballot(yes);
         const uint32_t slot = at + mbcnt64(yeses);
-        if (yes && slot < a.keep) kept[slot] = static_cast<int32_t>(i);
+        if (yes && slot < a.keep) head.kept[slot] = static_cast<int32_t>(i);
         at += static_cast<uint32_t>(__builtin_popcountll(yeses));
-    });
+    }
     if (threadIdx.x == 0) a.counts[bh] = static_cast<int32_t>(a.keep);
+}
+
+// ---- by several workgroups ----
+constexpr int kEvictItems = 8;
+constexpr uint32_t kEvictTile = kEvictItems * kEvictBlock;
+
+// The counts of pass - 1 joined over the splits: the digit, and how many scores of
+// earlier splits stay for it (`equals`: of those that share the digits found, where
+// not all of them do).
+__device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh, int64_t bh, int pass, Threshold &t,
+                                            uint32_t &before, uint32_t &equals) {
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
+    const uint32_t *hist = a.hist + ((static_cast<int64_t>((pass - 1) & 1) * gridDim.x * gridDim.y + bh) * a.splits) * kEvictBins;
+    uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
+#pragma unroll 8
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const uint2 c = *reinterpret_cast<const uint2 *>(hist + static_cast<int64_t>(s) * kEvictBins + top - 1u);
+        c0 += c.y;
+        c1 += c.x;
+        b0 += s < blockIdx.z ? c.y : 0u;
+        b1 += s < blockIdx.z ? c.x : 0u;
+    }
+    find_digit(sh, c0, c1, pass - 1, t);
+    const uint32_t d = sh.digit;
+    const uint32_t mine = (top > d ? b0 : 0u) + (top - 1u > d ? b1 : 0u);
+    const uint32_t sum = wave_inclusive_scan<SumU32>(mine);
+    if (lane_id() == kWave - 1) sh.wave_equal[w] = sum;
+    if (top == d) sh.before = b0;
+    if (top - 1u == d) sh.before = b1;
+    __syncthreads();
+    for (int v = 0; v < kEvictWaves; ++v) before += sh.wave_equal[v];
+    equals = t.all ? 0u : sh.before;
+    if (t.all) before += sh.before;
+    __syncthreads();
+}
+
+// pass 0 .. 2: counts by a digit; 3: the output
+template <bool LAST>
+__global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, int pass) {
+    __shared__ EvictShared sh;
+    const uint32_t split = blockIdx.z;
+    const int64_t bh = static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
+    const Head head(a, blockIdx.x, blockIdx.y);
+    if (head.len <= a.keep) {
+        if (LAST) head.keep_all(a, bh, split * kEvictBlock + threadIdx.x, a.splits * kEvictBlock);
+        return;
+    }
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const uint32_t from = split * a.span;
+    const uint32_t to = head.len - (from < head.len ? from : head.len) < a.span ? head.len : from + a.span;
+    const int64_t rows = static_cast<int64_t>(gridDim.x) * gridDim.y;
+    Threshold t = head.start();
+    uint32_t before = 0, equals = 0;
+    if (pass > 0) {
+        if (pass > 1) {
+            t = a.found[bh * kEvictPasses + pass - 2];
+            before = a.before[bh * a.splits + split];
+        }
+        if (!t.all) join_splits(a, sh, bh, pass, t, before, equals);
+        if (!LAST && threadIdx.x == 0) {
+            if (split == 0) a.found[bh * kEvictPasses + pass - 1] = t;
+            a.before[bh * a.splits + split] = before;
+        }
+    }
+    const auto load = [&](uint32_t base, uint32_t(&key)[kEvictItems]) {
+        float x[kEvictItems];
+#pragma unroll
+        for (int j = 0; j < kEvictItems; ++j) {
+            const uint32_t i = base + j * kWave;
+            x[j] = i < to && head.open(i) ? head.scores[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kEvictItems; ++j) key[j] = score_key(x[j]);
+    };
+    if constexpr (!LAST) {
+        if (t.all) return;
+        for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
+        __syncthreads();
+        for (uint32_t tile = from; tile < to; tile += kEvictTile) {
+            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane;
+            uint32_t key[kEvictItems];
+            load(base, key);
+#pragma unroll
+            for (int j = 0; j < kEvictItems; ++j) {
+                const uint32_t i = base + j * kWave;
+                count_digit(sh.hist, (key[j] >> digit_shift(pass)) & (digit_bins(pass) - 1u),
+                            i < to && head.open(i) && (key[j] & t.fixed) == t.low);
+            }
+        }
+        __syncthreads();
+        uint32_t *hist =
+            a.hist + ((static_cast<int64_t>(pass & 1) * rows + bh) * a.splits + split) * kEvictBins;
+        for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) hist[i] = sh.hist[i];
+    } else {
+        // slots before this split: positions that stay in any case, better scores, and equal ones
+        uint32_t at = before + (from < head.begin ? from : head.begin) + (from > head.end ? from - head.end : 0u);
+        at += equals < t.need ? equals : t.need;
+        for (uint32_t tile = from; tile < to; tile += kEvictTile) {
+            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane;
+            uint32_t key[kEvictItems];
+            load(base, key);
+            uint32_t sure = 0, equal = 0;
+#pragma unroll
+            for (int j = 0; j < kEvictItems; ++j) {
+                const uint32_t i = base + j * kWave;
+                const bool in = i < to, open = in && head.open(i);
+                sure += static_cast<uint32_t>(
+                    __builtin_popcountll(ballot((in && head.always(i)) || (open && better(t, key[j])))));
+                equal += static_cast<uint32_t>(__builtin_popcountll(ballot(open && !t.all && key[j] == t.low)));
+            }
+            if (lane == 0) {
+                sh.wave[w] = sure;
+                sh.wave_equal[w] = equal;
+            }
+            __syncthreads();
+            const uint32_t tile_equals = equals;
+            uint32_t mine = at - (tile_equals < t.need ? tile_equals : t.need), all_sure = 0, all_equal = 0;
+            uint32_t run = tile_equals;
+            for (int v = 0; v < kEvictWaves; ++v) {
+                const uint32_t s = sh.wave[v], e = sh.wave_equal[v];
+                if (v < w) {
+                    mine += s;
+                    run += e;
+                }
+                all_sure += s;
+                all_equal += e;
+            }
+            mine += run < t.need ? run : t.need;
+#pragma unroll
+            for (int j = 0; j < kEvictItems; ++j) {
+                const uint32_t i = base + j * kWave;
+                const bool in = i < to, open = in && head.open(i);
+                const bool same = open && !t.all && key[j] == t.low;
+                const uint64_t sames = ballot(same);
+                const bool yes = (in && head.always(i)) || (open && better(t, key[j])) ||
+                                 (same && run + mbcnt64(sames) < t.need);
+                run += static_cast<uint32_t>(__builtin_popcountll(sames));
+                const uint64_t yeses = ballot(yes);
+                const uint32_t slot = mine + mbcnt64(yeses);
+                if (yes && slot < a.keep) head.kept[slot] = static_cast<int32_t>(i);
+                mine += static_cast<uint32_t>(__builtin_popcountll(yeses));
+            }
+            at += all_sure - (tile_equals < t.need ? tile_equals : t.need);
+            equals += all_equal;
+            at += equals < t.need ? equals : t.need;
+            __syncthreads();
+        }
+        if (split == 0 && threadIdx.x == 0) a.counts[bh] = static_cast<int32_t>(a.keep);
+    }
 }
 
 // ------------------------------------------------------------ rows moved ---
@@ -325,8 +543,7 @@ __device__ __forceinline__ int piece_at(const MoveArgs &a, int c) {
 template <int BYTES>
 __global__ __launch_bounds__(kMoveBlock) void move_kernel(MoveArgs a) {
     using P = Piece<BYTES>;
-    const int64_t bh = blockIdx.y;
-    const int64_t b = bh / a.heads, h = bh % a.heads;
+    const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.heads + h;
     const char *from = a.from + b * a.from_batch + h * a.from_head;
     char *to = a.to + b * a.to_batch + h * a.to_head;
     const int32_t *kept = a.kept + bh * a.keep;
@@ -356,8 +573,7 @@ constexpr int kPlaceBlock = 1024;
 template <int BYTES>
 __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) {
     using P = Piece<BYTES>;
-    const int64_t bh = blockIdx.y;
-    const int64_t b = bh / a.heads, h = bh % a.heads;
+    const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.heads + h;
     char *rows_at = a.to + b * a.to_batch + h * a.to_head;
     const int32_t *kept = a.kept + bh * a.keep;
     const int rows = kPlaceBlock >> a.lg;
@@ -396,12 +612,41 @@ int check_cache(int64_t batch, int64_t heads, int64_t capacity) {
     return SSC_OK;
 }
 
+// Splits of a head: of 8192 positions where that gives up to 512 workgroups,
+// else of 32,768, and longer ones where there would be over 64 of a head.
+struct EvictPlan {
+    uint32_t splits, span;
+    size_t found, before, bytes;  // offsets into the scratch
+};
+
+EvictPlan evict_plan(int64_t rows, int64_t capacity) {
+    EvictPlan p{};
+    p.splits = 1;
+    const int64_t tiles = (capacity + kEvictTile - 1) / kEvictTile;
+    const bool few = rows * tiles <= 512 && capacity > 2 * kEvictTile;
+    if (rows < 1 || (capacity <= kEvictHeld && !few)) return p;
+    int64_t each = few ? 1 : kEvictHeld / kEvictTile;
+    if (each < (tiles + 63) / 64) each = (tiles + 63) / 64;
+    p.splits = static_cast<uint32_t>((tiles + each - 1) / each);
+    p.span = static_cast<uint32_t>(each * kEvictTile);
+    const size_t all = static_cast<size_t>(rows) * p.splits;
+    p.found = 2 * all * kEvictBins * 4;
+    p.before = p.found + static_cast<size_t>(rows) * kEvictPasses * sizeof(Threshold);
+    p.bytes = p.before + all * 4;
+    return p;
+}
+
 }  // namespace
 }  // namespace ssc
 
 using namespace ssc;
 
 extern "C" {
+
+size_t ssc_evict_scratch_bytes(int64_t batch, int64_t heads, int64_t capacity) {
+    if (check_cache(batch, heads, capacity) != SSC_OK) return 0;
+    return evict_plan(batch * heads, capacity).bytes;
+}
 
 int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t capacity, int64_t score_batch,
                            int64_t score_head, const void *weights, int dtype, int64_t group, int64_t queries,
@@ -428,29 +673,34 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
     a.score_head = score_head;
     a.weights = weights;
     a.weight_batch = weight_batch;
+    a.weight_group = group * weight_head;
     a.weight_head = weight_head;
     a.weight_query = weight_query;
     a.lengths = lengths;
-    a.heads = static_cast<int>(heads);
-    a.capacity = static_cast<int>(capacity);
-    a.group = static_cast<int>(group);
-    a.queries = static_cast<int>(queries > 0 ? queries : 1);
-    if (queries == 0) a.group = 0;  // no rows
     a.length = static_cast<int>(length);
-    a.fresh = fresh;
+    a.group = static_cast<uint32_t>(group);
+    a.queries = static_cast<uint32_t>(queries);
+    a.fresh = fresh < length ? fresh : length;
     a.decay = decay;
-    dim3 grid(1, static_cast<unsigned>(batch * heads));
+    // one query a head, or all of a head's before the next head's: rows evenly apart
+    if (queries == 1) a.weight_query = weight_head;
+    const bool even = group == 1 || queries <= 1 || weight_head == queries * weight_query;
+    const int64_t rows = group * queries;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const int64_t cols = kWave * 16 / static_cast<int64_t>(sizeof(T));
-        grid.x = static_cast<unsigned>((length + cols - 1) / cols);
+        const dim3 grid(static_cast<unsigned>((length + cols - 1) / cols), static_cast<unsigned>(heads),
+                        static_cast<unsigned>(batch));
         const auto launch = [&](auto waves) {
             constexpr int W = decltype(waves)::value;
-            hipLaunchKernelGGL((accumulate_kernel<T, W>), grid, dim3(W * kWave), 0, static_cast<hipStream_t>(stream),
-                               a);
+            if (even)
+                hipLaunchKernelGGL((accumulate_kernel<T, W, true>), grid, dim3(W * kWave), 0,
+                                   static_cast<hipStream_t>(stream), a);
+            else
+                hipLaunchKernelGGL((accumulate_kernel<T, W, false>), grid, dim3(W * kWave), 0,
+                                   static_cast<hipStream_t>(stream), a);
             return launched();
         };
-        const int64_t rows = group * queries;
         if (rows <= 16) return launch(std::integral_constant<int, 1>{});
         if (rows <= 64) return launch(std::integral_constant<int, 4>{});
         return launch(std::integral_constant<int, 8>{});
@@ -459,17 +709,19 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
 
 int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t capacity, int64_t score_batch,
                    int64_t score_head, const int32_t *lengths, int64_t keep, int64_t first, int64_t recent,
-                   int32_t *kept, int32_t *counts, void *stream) {
+                   int32_t *kept, int32_t *counts, void *scratch, size_t scratch_bytes, void *stream) {
     SSC_TRY(check_cache(batch, heads, capacity));
     if (keep < 1 || keep > capacity || first < 0 || recent < 0 || first > keep || recent > keep - first)
         return SSC_ERR_ARG;
-    const View<3> s{{batch, heads, capacity}, {score_batch, score_head, 1}};
-    if (!s.strides_ok()) return SSC_ERR_ARG;
+    const View<3> view{{batch, heads, capacity}, {score_batch, score_head, 1}};
+    if (!view.strides_ok()) return SSC_ERR_ARG;
     if (batch > 0 && (scores == nullptr || kept == nullptr || counts == nullptr)) return SSC_ERR_ARG;
     if (!aligned(scores, 4) || !aligned(lengths, 4) || !aligned(kept, 4) || !aligned(counts, 4)) return SSC_ERR_ARG;
     const size_t rows = static_cast<size_t>(batch) * heads;
-    const Span written[] = {{kept, rows * keep * 4}, {counts, rows * 4}};
-    const Span read[] = {{scores, static_cast<size_t>(s.extent()) * 4}, {lengths, static_cast<size_t>(batch) * 4}};
+    const EvictPlan p = evict_plan(batch * heads, capacity);
+    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < p.bytes)) return SSC_ERR_SCRATCH;
+    const Span written[] = {{kept, rows * keep * 4}, {counts, rows * 4}, {scratch, p.bytes}};
+    const Span read[] = {{scores, static_cast<size_t>(view.extent()) * 4}, {lengths, static_cast<size_t>(batch) * 4}};
     if (spans_overlap(written)) return SSC_ERR_ALIAS;
     for (const Span &x : written)
         for (const Span &y : read)
@@ -488,15 +740,31 @@ int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t ca
     a.recent = static_cast<uint32_t>(recent);
     a.kept = kept;
     a.counts = counts;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.splits > 1) {
+        char *at = static_cast<char *>(scratch);
+        a.splits = p.splits;
+        a.span = p.span;
+        a.hist = reinterpret_cast<uint32_t *>(at);
+        a.found = reinterpret_cast<Threshold *>(at + p.found);
+        a.before = reinterpret_cast<uint32_t *>(at + p.before);
+        const dim3 grid(static_cast<unsigned>(heads), static_cast<unsigned>(batch), p.splits);
+        for (int pass = 0; pass < kEvictPasses; ++pass) {
+            hipLaunchKernelGGL((evict_split_kernel<false>), grid, dim3(kEvictBlock), 0, s, a, pass);
+            SSC_TRY(launched());
+        }
+        hipLaunchKernelGGL((evict_split_kernel<true>), grid, dim3(kEvictBlock), 0, s, a, kEvictPasses);
+        return launched();
+    }
     const auto launch = [&](auto items) {
-        hipLaunchKernelGGL((evict_kernel<decltype(items)::value>), dim3(static_cast<unsigned>(rows)), dim3(kEvictBlock),
-                           0, static_cast<hipStream_t>(stream), a);
+        hipLaunchKernelGGL((evict_kernel<decltype(items)::value>),
+                           dim3(static_cast<unsigned>(heads), static_cast<unsigned>(batch)), dim3(kEvictBlock), 0, s, a);
         return launched();
     };
     if (capacity <= 4 * kEvictBlock) return launch(std::integral_constant<int, 4>{});
     if (capacity <= 8 * kEvictBlock) return launch(std::integral_constant<int, 8>{});
-    if (capacity <= 32 * kEvictBlock) return launch(std::integral_constant<int, 32>{});
-    return launch(std::integral_constant<int, 0>{});
+    if (capacity <= 16 * kEvictBlock) return launch(std::integral_constant<int, 16>{});
+    return launch(std::integral_constant<int, 32>{});
 }
 
 int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t heads, int64_t capacity, int64_t width,
@@ -543,7 +811,7 @@ int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t head
     a.chunks = (a.row_bytes + bytes - 1) / bytes;
     a.cols = a.chunks;
     while (a.lg < 8 && (1 << a.lg) < a.chunks) ++a.lg;
-    dim3 grid(1, static_cast<unsigned>(batch * heads));
+    dim3 grid(1, static_cast<unsigned>(heads), static_cast<unsigned>(batch));
     if (place) {
         // few heads: their columns over several workgroups, where no two of
         // these share bytes of a row

@@ -24,7 +24,6 @@ namespace ssc {
 namespace {
 
 constexpr int kRouteBlock = 256;
-constexpr int kRouteWaves = kRouteBlock / kWave;
 constexpr int64_t kExpertsMax = 1024;
 constexpr int64_t kPerMax = 64;
 constexpr int kIndexBits = 10;
@@ -137,6 +136,7 @@ struct Key {
         }
         return x > -__builtin_inff() ? k << kIndexBits | (kIndexMask - static_cast<uint32_t>(index)) : 0u;
     }
+    __device__ static __forceinline__ K none() { return 0u; }
     __device__ static __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
     __device__ static __forceinline__ K smaller(K a, K b) { return a > b ? b : a; }
     __device__ static __forceinline__ bool expert(K k) { return k > kIndexMask; }
@@ -160,6 +160,7 @@ struct Key<float> {
         const uint64_t k = static_cast<uint64_t>(o) << kIndexBits | (kIndexMask - static_cast<uint32_t>(index));
         return __longlong_as_double(static_cast<long long>(x > -__builtin_inff() ? kBase | k : kBase));
     }
+    __device__ static __forceinline__ K none() { return 0x1p52; }
     // no key is NaN, so the instructions are used as they are
     __device__ static __forceinline__ K larger(K a, K b) {
         K r;
@@ -181,44 +182,61 @@ struct Key<float> {
     }
 };
 
-// The N keys of a lane, largest first, by merging of odd and even places
-// (63 exchanges for 16).
-template <class Q, int N>
+// a where mask is 0, b where it is all ones (a choice by a condition between
+// two elements of an array becomes an index into it, and that sixteen selects)
+__device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return a ^ ((a ^ b) & mask); }
+__device__ __forceinline__ double pick(uint32_t mask, double a, double b) {
+    const uint64_t x = static_cast<uint64_t>(__double_as_longlong(a)), y = static_cast<uint64_t>(__double_as_longlong(b));
+    const uint32_t lo = pick(mask, static_cast<uint32_t>(x), static_cast<uint32_t>(y));
+    const uint32_t hi = pick(mask, static_cast<uint32_t>(x >> 32), static_cast<uint32_t>(y >> 32));
+    return __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(hi) << 32 | lo));
+}
+
+template <class Q>
+__device__ __forceinline__ void exchange(typename Q::K &a, typename Q::K &b) {
+    const auto big = Q::larger(a, b);
+    b = Q::smaller(a, b);
+    a = big;
+}
+
+// The TOP largest keys of a lane's N, largest first, in its first places: by
+// merging of odd and even places (63 exchanges for 16), for 8 of more in runs of
+// 8, of two of which the larger half is kept and put in order (19 an run, 8
+// maxima and 12 a merge: 108 instructions for 8 of 16 against 126).
+template <class Q, int N, int TOP>
 __device__ __forceinline__ void sort_keys(typename Q::K (&k)[N]) {
 #pragma unroll
-    for (int p = 1; p < N; p *= 2) {
+    for (int run = 0; run < N; run += TOP) {
 #pragma unroll
-        for (int h = p; h >= 1; h /= 2) {
+        for (int p = 1; p < TOP; p *= 2) {
 #pragma unroll
-            for (int j = h % p; j + h < N; j += 2 * h) {
+            for (int h = p; h >= 1; h /= 2) {
 #pragma unroll
-                for (int i = 0; i < h; ++i) {
-                    const int a = j + i, b = j + i + h;
-                    if (b < N && a / (2 * p) == b / (2 * p)) {
-                        const auto big = Q::larger(k[a], k[b]);
-                        k[b] = Q::smaller(k[a], k[b]);
-                        k[a] = big;
+                for (int j = h % p; j + h < TOP; j += 2 * h) {
+#pragma unroll
+                    for (int i = 0; i < h; ++i) {
+                        const int a = j + i, b = j + i + h;
+                        if (b < TOP && a / (2 * p) == b / (2 * p)) exchange<Q>(k[run + a], k[run + b]);
                     }
                 }
             }
         }
+        if (run == 0) continue;
+#pragma unroll
+        for (int i = 0; i < TOP; ++i) k[i] = Q::larger(k[i], k[run + TOP - 1 - i]);
+#pragma unroll
+        for (int h = TOP / 2; h >= 1; h /= 2) {
+#pragma unroll
+            for (int i = 0; i < TOP; ++i)
+                if ((i & h) == 0) exchange<Q>(k[i], k[i + h]);
+        }
     }
 }
 
-// exp(d) for d <= 0, by 2^(d log2(e)) with what the product's rounding loses put
-// back to first order; below -200 it is 0.
-__device__ __forceinline__ float exp_of(float d) {
-    constexpr float kHi = 1.44269504088896340736f;
-    constexpr float kLo = static_cast<float>(1.44269504088896340736 - static_cast<double>(kHi));
-    d = fmaxf(d, -200.0f);
-    const float a = d * kHi;
-    const float r = __builtin_fmaf(d, kLo, __builtin_fmaf(d, kHi, -a));
-    const float e = __builtin_amdgcn_exp2f(a);
-    return __builtin_fmaf(e, r * 0.69314718055994530942f, e);
-}
-
-// A row of logits as exponentials of their distance from the largest. Beside one
-// of +infinity no other counts. A row without experts has none (sum 0).
+// A row of logits as exponentials of their distance from the largest: 2^((x -
+// top) log2(e)), off by 2.3 |x - top| half steps of fp32 for the difference,
+// the product and the constant, and by 2 for the exponential. Beside a logit of
+// +infinity no other counts. A row without experts has none (sum 0).
 template <int G, int N>
 struct Softmax {
     float top, sum, inv;
@@ -227,17 +245,21 @@ struct Softmax {
     __device__ __forceinline__ float lifted(float x) const {
         return lift ? (x == __builtin_inff() ? 0.0f : -__builtin_inff()) : x;
     }
+    // x as lifted: the largest is finite, and -infinity gives 0
     __device__ __forceinline__ float weight(float x) const {
-        const float y = lifted(x);
-        return y > -__builtin_inff() ? exp_of(y - top) : 0.0f;
+        return __builtin_amdgcn_exp2f((x - top) * 1.44269504088896340736f);
     }
-    __device__ __forceinline__ void make(const float (&x)[N], float (&e)[N]) {
+    __device__ __forceinline__ void make(float (&x)[N], float (&e)[N]) {
         float m = x[0];
 #pragma unroll
         for (int j = 1; j < N; ++j) m = fmaxf(m, x[j]);
-        top = group_max<G>(m);
+        top = fmaxf(group_max<G>(m), -0x1.fffffep127f);
         lift = top == __builtin_inff();
-        if (lift) top = 0.0f;
+        if (__builtin_expect(ballot(lift) != 0, 0)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = lifted(x[j]);
+            if (lift) top = 0.0f;
+        }
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -265,20 +287,27 @@ struct RouteArgs {
     uint32_t *done;
 };
 
-template <class T, int G, int N, bool BALANCE>
-__global__ __launch_bounds__(kRouteBlock) void route_kernel(RouteArgs a) {
+// With the balance a workgroup adds up its tokens' softmax, so it is larger and
+// there are fewer: as many threads as the registers of N logits allow.
+template <int N, bool BALANCE>
+constexpr int kThreads = !BALANCE ? kRouteBlock : (N > 16 ? 512 : 1024);
+
+// TOP: of the lane's logits, how many may be chosen (8 where `per` is no more).
+template <class T, int G, int N, int TOP, bool BALANCE>
+__global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs a) {
     using H = Held<T, G, N>;
     using Q = Key<T>;
     using K = typename Q::K;
-    constexpr int kTokens = kRouteBlock / G;       // of a workgroup at a time
-    constexpr int kRounds = N < 64 / G ? N : 64 / G;  // of G places among the chosen
+    constexpr int kBlock = kThreads<N, BALANCE>;
+    constexpr int kTokens = kBlock / G;  // of a workgroup at a time
+    constexpr int kHalf = kBlock / kWave / 2;
     __shared__ uint32_t s_count[BALANCE ? G * N + 1 : 1];
-    __shared__ float s_share[BALANCE ? kRouteWaves : 1][BALANCE ? G * N : 1];
+    __shared__ float s_share[BALANCE ? kHalf : 1][BALANCE ? G * N : 1];
     const int lane = lane_id();
     const int sub = lane & (G - 1);
     float share[N];
     if constexpr (BALANCE) {
-        for (int e = threadIdx.x; e <= G * N; e += kRouteBlock) s_count[e] = 0;
+        for (int e = threadIdx.x; e <= G * N; e += kBlock) s_count[e] = 0;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < N; ++j) share[j] = 0.0f;
@@ -302,29 +331,32 @@ __global__ __launch_bounds__(kRouteBlock) void route_kernel(RouteArgs a) {
         K key[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) key[j] = Q::make(x[j], H::at(sub, j));
-        sort_keys<Q, N>(key);
-        float e[kRounds], chosen = 0.0f;
-        int id[kRounds];
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            e[r] = 0.0f;
-            id[r] = -1;
-            const int most = a.per - r * G < G ? a.per - r * G : G;
+        sort_keys<Q, N, TOP>(key);
+        // G places a round, one to a lane; exponentials wait for their sum where
+        // they will be read again: in a register, or in the weights if there are more
+        float e = 0.0f, chosen = 0.0f;
+        for (int r = 0; r < a.per; r += G) {
+            const int most = a.per - r < G ? a.per - r : G;
+            K place = Q::none();
             for (int k = 0; k < most; ++k) {
                 const K best = over_group<G>(key[0], Q::larger);
-                const bool mine = best == key[0];
+                const uint32_t mine = best == key[0] ? ~0u : 0u;
 #pragma unroll
-                for (int j = 0; j + 1 < N; ++j) key[j] = mine ? key[j + 1] : key[j];
-                if (mine) key[N - 1] = Q::make(-__builtin_inff(), 0);
-                if (sub == k && Q::expert(best)) {
-                    const float w = sm.weight(Q::value(best));
-                    if (sm.lifted(Q::value(best)) > -__builtin_inff()) {
-                        id[r] = Q::index(best);
-                        e[r] = w;
-                    }
-                }
+                for (int j = 0; j + 1 < TOP; ++j) key[j] = pick(mine, key[j], key[j + 1]);
+                key[TOP - 1] = pick(mine, key[TOP - 1], Q::none());
+                place = pick(sub == k ? ~0u : 0u, place, best);
             }
-            chosen += e[r];
+            const float v = Q::value(place);
+            const bool expert = Q::expert(place);
+            const int id = expert ? Q::index(place) : -1;
+            e = expert ? sm.weight(v) : 0.0f;
+            chosen += e;
+            if (inside && sub < most) {
+                a.ids[t * a.per + r + sub] = id;
+                if (a.per > G) a.weights[t * a.per + r + sub] = e;
+                if (BALANCE && id >= 0)
+                    __hip_atomic_fetch_add(&s_count[id], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
         }
         float inv = sm.inv;
         if (a.normalize) {
@@ -332,32 +364,33 @@ __global__ __launch_bounds__(kRouteBlock) void route_kernel(RouteArgs a) {
             inv = chosen > 0.0f ? 1.0f / chosen : 0.0f;
         }
         if (inside) {
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) {
-                const int k = r * G + sub;
-                if (k < a.per) {
-                    a.ids[t * a.per + k] = id[r];
-                    a.weights[t * a.per + k] = e[r] * inv;
-                    if (BALANCE && id[r] >= 0)
-                        __hip_atomic_fetch_add(&s_count[id[r]], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                }
+            float *w = a.weights + t * a.per;
+            if (a.per <= G) {
+                if (sub < a.per) w[sub] = e * inv;
+            } else {
+                for (int k = sub; k < a.per; k += G) w[k] *= inv;
             }
         }
     }
     if constexpr (BALANCE) {
+        const int w = static_cast<int>(uniform(threadIdx.x / kWave));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
 #pragma unroll
             for (int off = G; off < kWave; off *= 2) share[j] += __shfl_xor(share[j], off);
-            if (lane < G) s_share[threadIdx.x / kWave][H::at(sub, j)] = share[j];
+            if (w >= kHalf && lane < G) s_share[w - kHalf][H::at(sub, j)] = share[j];
         }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (w < kHalf && lane < G) s_share[w][H::at(sub, j)] += share[j];
         __syncthreads();
         float *to = a.part_share + static_cast<int64_t>(blockIdx.x) * a.experts;
         int32_t *count = a.part_count + static_cast<int64_t>(blockIdx.x) * (a.experts + 1);
-        for (int i = threadIdx.x; i < a.experts; i += kRouteBlock) {
+        for (int i = threadIdx.x; i < a.experts; i += kBlock) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kRouteWaves; ++w) s += s_share[w][i];
+            for (int v = 0; v < kHalf; ++v) s += s_share[v][i];
             to[i] = s;
             count[i] = static_cast<int32_t>(s_count[i]);
         }
@@ -369,12 +402,13 @@ __global__ __launch_bounds__(kRouteBlock) void route_kernel(RouteArgs a) {
 // expert, in fp64. The workgroup that is done last adds the loss.
 constexpr int kJoinCols = 16;
 constexpr int kJoinRows = kRouteBlock / kJoinCols;
+constexpr int kJoinWaves = kRouteBlock / kWave;
 
 __global__ __launch_bounds__(kRouteBlock) void route_join_kernel(RouteArgs a, int blocks, int32_t *__restrict__ counts,
                                                                 float *__restrict__ share, float *__restrict__ loss) {
     __shared__ double s_p[kJoinRows][kJoinCols + 1];
     __shared__ int32_t s_c[kJoinRows][kJoinCols + 1];
-    __shared__ int32_t s_live[kRouteWaves];
+    __shared__ int32_t s_live[kJoinWaves];
     __shared__ double s_loss[kJoinCols];
     __shared__ uint32_t s_last;
     const int col = threadIdx.x % kJoinCols, row = threadIdx.x / kJoinCols;
@@ -398,7 +432,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_join_kernel(RouteArgs a, in
     s_c[row][col] = c;
     __syncthreads();
     n = 0;
-    for (int w = 0; w < kRouteWaves; ++w) n += s_live[w];
+    for (int w = 0; w < kJoinWaves; ++w) n += s_live[w];
     if (row == 0) {
         p = 0.0;
         c = 0;
@@ -450,7 +484,6 @@ template <class T, int G, int N>
 __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a) {
     using H = Held<T, G, N>;
     constexpr int kTokens = kRouteBlock / G;
-    constexpr int kRounds = N < 64 / G ? N : 64 / G;
     __shared__ float s_add[kRouteBlock * N];
     const int lane = lane_id();
     const int sub = lane & (G - 1);
@@ -471,37 +504,44 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
         const bool inside = t < a.tokens;
         const bool live = inside && (a.live == nullptr || a.live[t] != 0);
         const T *row = static_cast<const T *>(a.logits) + (live ? t : 0) * a.stride;
-        int id[kRounds];
-        float d[kRounds], y[kRounds];
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int k = r * G + sub;
-            const bool has = live && k < a.per && a.dweights != nullptr;
-            id[r] = has ? a.ids[t * a.per + k] : -1;
-            if (id[r] >= a.experts || id[r] < 0) id[r] = -1;
-            d[r] = id[r] >= 0 ? a.dweights[t * a.per + k] : 0.0f;
-            y[r] = id[r] >= 0 ? fmaxf(static_cast<float>(row[id[r]]), -__builtin_inff()) : -__builtin_inff();
-        }
+        // this lane's place of a round of G among the chosen
+        struct Chosen {
+            int id;
+            float d, x;
+        };
+        const auto chosen = [&](int k) -> Chosen {
+            if (!live || k >= a.per || a.dweights == nullptr) return {-1, 0.0f, -__builtin_inff()};
+            const int id = a.ids[t * a.per + k];
+            const float d = a.dweights[t * a.per + k];
+            if (id < 0 || id >= a.experts) return {-1, 0.0f, -__builtin_inff()};
+            return {id, d, fmaxf(static_cast<float>(row[id]), -__builtin_inff())};  // NaN as -infinity
+        };
+        const Chosen first = chosen(sub);
         float x[N], p[N];
         H::load(row, sub, live ? a.experts : 0, x);
         Softmax<G, N> sm;
         sm.make(x, p);
-        float w = 0.0f, wd = 0.0f;
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            y[r] = sm.weight(y[r]);
-            w += y[r];
-            wd += y[r] > 0.0f ? y[r] * d[r] : 0.0f;
+        const float y = sm.weight(sm.lifted(first.x));
+        float w = y, wd = y > 0.0f ? y * first.d : 0.0f;
+        for (int k = G + sub; k - sub < a.per; k += G) {
+            const Chosen c = chosen(k);
+            const float z = sm.weight(sm.lifted(c.x));
+            w += z;
+            wd += z > 0.0f ? z * c.d : 0.0f;
         }
         w = group_sum<G>(w);
         wd = group_sum<G>(wd);
         const float inv = a.normalize ? (w > 0.0f ? 1.0f / w : 0.0f) : sm.inv;
-        const float mean = wd * inv;
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            if (y[r] > 0.0f)
-                __hip_atomic_fetch_add(&add[id[r]], y[r] * inv * (a.normalize ? d[r] - mean : d[r]), __ATOMIC_RELAXED,
+        const float mean = wd * inv, less = a.normalize ? mean : 0.0f;
+        const auto hand = [&](const Chosen &c, float z) {
+            if (z > 0.0f)
+                __hip_atomic_fetch_add(&add[c.id], z * inv * (c.d - less), __ATOMIC_RELAXED,
                                        __HIP_MEMORY_SCOPE_WORKGROUP);
+        };
+        hand(first, y);
+        for (int k = G + sub; k - sub < a.per; k += G) {
+            const Chosen c = chosen(k);
+            hand(c, sm.weight(sm.lifted(c.x)));
         }
         float s = 0.0f;
 #pragma unroll
@@ -516,9 +556,11 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
         for (int j = 0; j < N; ++j)
             p[j] = sm.sum > 0.0f ? __builtin_fmaf(p[j], even[j] - s, add[H::at(sub, j)]) : 0.0f;
         wave_lds_order();
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if (id[r] >= 0) add[id[r]] = 0.0f;
+        if (first.id >= 0) add[first.id] = 0.0f;
+        for (int k = G + sub; k < a.per; k += G) {
+            const Chosen c = chosen(k);
+            if (c.id >= 0) add[c.id] = 0.0f;
+        }
         wave_lds_order();
         if (inside) H::store(static_cast<T *>(a.dlogits) + t * a.experts, sub, a.experts, p);
     }
@@ -526,26 +568,27 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
 
 // ============================================================ host side ---
 // Calls f with the lanes of a row and the logits of a lane: as few lanes as
-// hold it with 16 each.
+// hold it with 16 each, or 24.
 template <class F>
 int with_row(int64_t experts, F f) {
-    const auto of = [&](auto g, auto n) { return f(g, n); };
     using std::integral_constant;
-    if (experts <= 8) return of(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    if (experts <= 16) return of(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-    if (experts <= 32) return of(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    if (experts <= 64) return of(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    if (experts <= 128) return of(integral_constant<int, 8>{}, integral_constant<int, 16>{});
-    if (experts <= 256) return of(integral_constant<int, 16>{}, integral_constant<int, 16>{});
-    if (experts <= 512) return of(integral_constant<int, 32>{}, integral_constant<int, 16>{});
-    return of(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+    if (experts <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    if (experts <= 16) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+    if (experts <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    if (experts <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (experts <= 128) return f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    if (experts <= 192) return f(integral_constant<int, 8>{}, integral_constant<int, 24>{});
+    if (experts <= 256) return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    if (experts <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
+    return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
-int lanes_of(int64_t experts) {
-    return experts <= 128 ? 8 : experts <= 256 ? 16 : experts <= 512 ? 32 : 64;
+// Tokens of a workgroup at a time, with the balance.
+int64_t balance_tokens(int64_t experts) {
+    return experts <= 128 ? 128 : (experts <= 192 ? 64 : (experts <= 256 ? 64 : (experts <= 512 ? 32 : 16)));
 }
 
-// Workgroups of a pass with the balance: two a compute unit, and more where a
+// Workgroups of a pass with the balance: one a compute unit, and more where a
 // lane would add over 64 rows, one after another in fp32.
 struct RoutePlan {
     int64_t blocks;
@@ -554,9 +597,9 @@ struct RoutePlan {
 
 RoutePlan route_plan(int64_t tokens, int64_t experts) {
     RoutePlan p{};
-    const int64_t each = kRouteBlock / lanes_of(experts);
+    const int64_t each = balance_tokens(experts);
     const int64_t all = (tokens + each - 1) / each;
-    p.blocks = all < 1 ? 1 : (all < 512 ? all : 512);
+    p.blocks = all < 1 ? 1 : (all < 256 ? all : 256);
     if (p.blocks < (all + 63) / 64) p.blocks = (all + 63) / 64;
     p.loss = 16;
     p.share = p.loss + 8 * ((experts + kJoinCols - 1) / kJoinCols);
@@ -639,14 +682,20 @@ int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t expert
         using T = decltype(t);
         return with_row(experts, [&](auto g, auto n) {
             constexpr int G = decltype(g)::value, N = decltype(n)::value;
-            const int64_t all = (tokens + kRouteBlock / G - 1) / (kRouteBlock / G);
-            if (balance)
-                hipLaunchKernelGGL((route_kernel<T, G, N, true>), dim3(static_cast<unsigned>(p.blocks)),
-                                   dim3(kRouteBlock), 0, s, a);
-            else
-                hipLaunchKernelGGL((route_kernel<T, G, N, false>), dim3(static_cast<unsigned>(all < 8192 ? all : 8192)),
-                                   dim3(kRouteBlock), 0, s, a);
-            return launched();
+            const auto launch = [&](auto top) {
+                constexpr int TOP = decltype(top)::value;
+                const int64_t all = (tokens + kRouteBlock / G - 1) / (kRouteBlock / G);
+                if (balance)
+                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, true>), dim3(static_cast<unsigned>(p.blocks)),
+                                       dim3((kThreads<N, true>)), 0, s, a);
+                else
+                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, false>),
+                                       dim3(static_cast<unsigned>(all < 8192 ? all : 8192)),
+                                       dim3((kThreads<N, false>)), 0, s, a);
+                return launched();
+            };
+            if (N > 8 && per <= 8) return launch(std::integral_constant<int, (N > 8 ? 8 : N)>{});
+            return launch(std::integral_constant<int, N>{});
         });
     }));
     if (!balance) return SSC_OK;

@@ -1,11 +1,13 @@
 """ssc_route_rows and its gradient on the GPU against the definition in 64 bits.
 
 Ids and counts are equal. Steps below are half steps of fp32, 2^-24 of a value.
-An exponential is of a difference d of two fp32 logits (|d| of them of its value,
-where the difference is rounded) and itself within 4; a row's sum is added up in
-at most 16 + 6 steps, another such sum normalizes, and products and quotients
-round 4 times: a weight is within 60 + 2 max |d| of them. A mean adds up to 64
-rows a lane, 4 wavefronts and 3 lane steps in fp32, and the rest in fp64."""
+An exponential is 2 to the power of a difference d of two fp32 logits times log2(e):
+the difference, the product and the constant are off by 2.3 |d| of them, |d| being
+110 at most where anything is left, and it is itself within 4. A row's sum is added up
+in at most 24 + 6 steps, and products and quotients round 4 times: under 60 + 2 |d| in
+all, for 0.3 |d| is at most 22 of what 60 leaves. A mean adds up to 64 rows a
+lane, 3 lane steps and 9 of the wavefronts in fp32, and the rest in fp64: with
+the 38 + 2.3 |d| of a softmax below the 135 + 2 |d| allowed."""
 from __future__ import annotations
 
 import numpy as np

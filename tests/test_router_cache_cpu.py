@@ -22,15 +22,21 @@ def _call(name, defaults, **kw):
 def test_scratch_sizes():
     # one count of workgroups done, a loss for each 16 experts, shares and counts of each workgroup
     assert ssc.route_scratch_bytes(0, 8) == 16 + 8 + 8 * 4 + 9 * 4
-    assert ssc.route_scratch_bytes(100, 128) == 16 + 8 * 8 + 4 * (128 + 129) * 4
-    assert ssc.route_scratch_bytes(65_536, 128) == 16 + 8 * 8 + 512 * (128 + 129) * 4
-    # at most 64 rows of a lane: 8 rows of 512 experts to a workgroup at a time
-    assert ssc.route_scratch_bytes(2 ** 20, 512) == 16 + 8 * 32 + 2048 * (512 + 513) * 4
+    assert ssc.route_scratch_bytes(100, 128) == 16 + 8 * 8 + (128 + 129) * 4
+    assert ssc.route_scratch_bytes(65_536, 128) == 16 + 8 * 8 + 256 * (128 + 129) * 4
+    # at most 64 rows of a lane: 32 rows of 512 experts to a workgroup at a time
+    assert ssc.route_scratch_bytes(2 ** 20, 512) == 16 + 8 * 32 + 512 * (512 + 513) * 4
     assert ssc.route_scratch_bytes(-1, 8) == ssc.route_scratch_bytes(8, 0) == ssc.route_scratch_bytes(8, 1025) == 0
     assert ssc.route_scratch_bytes(BIG, 8) == 0
     assert ssc.verify_scratch_bytes(0, 100) == ssc.verify_scratch_bytes(4, 0) == 0
     assert ssc.verify_scratch_bytes(65_536, 10) == ssc.verify_scratch_bytes(1, 2 ** 22 + 1) == 0
     assert ssc.verify_scratch_bytes(3, 1025) == 32 + 3 * 2 * 8
+    # two tables of 2048 counts a split, three thresholds a head, one number a split
+    assert ssc.evict_scratch_bytes(1, 8, 16_384) == ssc.evict_scratch_bytes(40, 8, 32_768) == 0
+    assert ssc.evict_scratch_bytes(1, 8, 131_072) == 8 * 16 * 16_384 + 8 * 48 + 8 * 16 * 4
+    assert ssc.evict_scratch_bytes(40, 8, 131_072) == 320 * (4 * 16_384 + 48 + 4 * 4)
+    assert ssc.evict_scratch_bytes(1, 1, 2 ** 24) == 64 * 16_384 + 48 + 64 * 4
+    assert ssc.evict_scratch_bytes(1, 0, 100) == ssc.evict_scratch_bytes(-1, 1, 100) == ssc.evict_scratch_bytes(0, 1, 2 ** 20) == 0
 
 
 def test_route_refusals():
@@ -141,7 +147,7 @@ def test_accumulate_refusals():
 
 def test_evict_refusals():
     d = dict(scores=A, batch=2, heads=3, capacity=100, sb=300, sh=100, lengths=B, keep=50, first=4, recent=10, kept=C,
-             counts=D, stream=None)
+             counts=D, scratch=S, sbytes=1 << 24, stream=None)
     name = "ssc_evict_rows"
     assert _call(name, d, keep=0) == ARG
     assert _call(name, d, keep=101) == ARG
@@ -158,6 +164,11 @@ def test_evict_refusals():
     assert _call(name, d, kept=A + 2396) == ALIAS
     assert _call(name, d, counts=B + 4) == ALIAS
     assert _call(name, d, counts=C + 1196) == ALIAS
+    long = dict(d, capacity=40_000, sh=40_000, sb=120_000)
+    assert _call(name, long, scratch=None) == SCRATCH
+    assert _call(name, long, scratch=S + 8) == SCRATCH
+    assert _call(name, long, sbytes=ssc.evict_scratch_bytes(2, 3, 40_000) - 1) == SCRATCH
+    assert _call(name, long, scratch=A + 112) == ALIAS
 
 
 def test_move_refusals():
