@@ -33,46 +33,79 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
 
 // Which logits of a row a lane holds: chunks of kC consecutive ones, a group's
-// chunks side by side, so that its lanes read consecutive addresses.
+// chunks side by side, so that its lanes read consecutive addresses. Chunks of
+// 16 bytes that the row ends in start early, so that every load is whole and
+// none waits behind a branch; what they share with the chunk before is not
+// theirs.
 template <class T, int G, int N>
 struct Held {
     static constexpr int kC = N < 16 / static_cast<int>(sizeof(T)) ? N : 16 / static_cast<int>(sizeof(T));
-    __device__ static __forceinline__ int at(int sub, int j) { return ((j / kC) * G + sub) * kC + j % kC; }
+    static constexpr int kChunks = N / kC;
+    static constexpr bool kWide = kC * sizeof(T) == 16;  // of rows of at least that many logits
+    typedef T V __attribute__((ext_vector_type(kC)));
+    struct Narrow {
+        T e[kC];
+    };
+    using Raw = std::conditional_t<kWide, u32x4, Narrow>;
+    int n, sub, start[kChunks];
 
-    // a logit that is no number is as one of -infinity
-    __device__ static __forceinline__ void load(const T *row, int sub, int n, float (&x)[N]) {
+    __device__ __forceinline__ Held(int sub, int n) : n(n), sub(sub) {
 #pragma unroll
-        for (int c = 0; c < N / kC; ++c) {
-            const int i = at(sub, c * kC);
-            if (kC * sizeof(T) == 16 && i + kC <= n) {
-                typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
-                const u32x4 r = *reinterpret_cast<const u32x4_any *>(row + i);
-                const V v = __builtin_bit_cast(V, r);
+        for (int c = 0; c < kChunks; ++c) start[c] = kWide && at(c) > n - kC ? n - kC : at(c);
+    }
+    __device__ __forceinline__ int at(int c) const { return (c * G + sub) * kC; }
+    // the expert of logit j, and whether it is this lane's
+    __device__ __forceinline__ int index(int j) const { return start[j / kC] + j % kC; }
+    __device__ __forceinline__ bool own(int j) const {
+        const int i = index(j);
+        return kWide ? i >= at(j / kC) : i < n;
+    }
+    // every lane's chunk lies inside the row (the same in all lanes)
+    __device__ __forceinline__ bool whole(int c) const { return (c + 1) * G * kC <= n; }
+
+    __device__ __forceinline__ void fetch(const T *row, Raw (&raw)[kChunks]) const {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if constexpr (kWide) {
+                raw[c] = *reinterpret_cast<const u32x4_any *>(row + start[c]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kC; ++e) raw[c].e[e] = row[start[c] + e < n ? start[c] + e : n - 1];
+            }
+        }
+    }
+    // a logit that is no number, or not this lane's, is as one of -infinity, and -0 as 0
+    __device__ __forceinline__ void unpack(const Raw (&raw)[kChunks], float (&x)[N]) const {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if constexpr (kWide) {
+                const V v = __builtin_bit_cast(V, raw[c]);
 #pragma unroll
                 for (int e = 0; e < kC; ++e) x[c * kC + e] = static_cast<float>(v[e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < kC; ++e)
-                    x[c * kC + e] = i + e < n ? static_cast<float>(row[i + e]) : -__builtin_inff();
+                for (int e = 0; e < kC; ++e) x[c * kC + e] = static_cast<float>(raw[c].e[e]);
+            }
+            if (!whole(c)) {
+#pragma unroll
+                for (int j = c * kC; j < (c + 1) * kC; ++j) x[j] = own(j) ? x[j] : -__builtin_inff();
             }
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = fmaxf(x[j], -__builtin_inff());
+        for (int j = 0; j < N; ++j) x[j] = fmaxf(x[j] + 0.0f, -__builtin_inff());
     }
-    __device__ static __forceinline__ void store(T *row, int sub, int n, const float (&x)[N]) {
+    __device__ __forceinline__ void store(T *row, const float (&x)[N]) const {
 #pragma unroll
-        for (int c = 0; c < N / kC; ++c) {
-            const int i = at(sub, c * kC);
-            if (kC * sizeof(T) == 16 && i + kC <= n) {
-                typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
+        for (int c = 0; c < kChunks; ++c) {
+            if (kWide && start[c] == at(c)) {
                 V v;
 #pragma unroll
                 for (int e = 0; e < kC; ++e) v[e] = static_cast<T>(x[c * kC + e]);
-                *reinterpret_cast<u32x4_any *>(row + i) = __builtin_bit_cast(u32x4, v);
+                if constexpr (kWide) *reinterpret_cast<u32x4_any *>(row + start[c]) = __builtin_bit_cast(u32x4, v);
             } else {
 #pragma unroll
-                for (int e = 0; e < kC; ++e)
-                    if (i + e < n) row[i + e] = static_cast<T>(x[c * kC + e]);
+                for (int j = c * kC; j < (c + 1) * kC; ++j)
+                    if (own(j)) row[index(j)] = static_cast<T>(x[j]);
             }
         }
     }
@@ -88,6 +121,10 @@ __device__ __forceinline__ uint32_t partner(uint32_t v) {
     if constexpr (STEP == 4) return dpp_move<0x141, 0xf>(v);
     if constexpr (STEP == 8) return dpp_move<0x140, 0xf>(v);
     return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), STEP));
+}
+template <int STEP>
+__device__ __forceinline__ int32_t partner(int32_t v) {
+    return static_cast<int32_t>(partner<STEP>(static_cast<uint32_t>(v)));
 }
 template <int STEP>
 __device__ __forceinline__ float partner(float v) {
@@ -113,54 +150,72 @@ template <int G>
 __device__ __forceinline__ float group_sum(float v) {
     return over_group<G>(v, [](float a, float b) { return a + b; });
 }
+// Sum over the groups of a wavefront, lane by lane.
+template <int G>
+__device__ __forceinline__ float over_groups(float v) {
+    if constexpr (G <= 8) v += __uint_as_float(dpp_move<0x128, 0xf>(__float_as_uint(v)));  // 8 lanes on in each 16
+    if constexpr (G <= 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (G <= 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
+}
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
     return over_group<G>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// A logit and its expert in one number that is largest for the largest logit,
-// the lowest expert of equal ones; a key of value 0 is no expert. 16-bit logits
-// fit with their index into 32 bits, fp32 ones into the fraction of a double
-// (2^52 above them keeps it normal), whose maximum is one instruction.
+// A logit (no NaN, no -0) and its expert in one number that is largest for the
+// largest logit, the lowest expert of equal ones. A 16-bit logit's fp32 bits end in
+// 13 zeros or more, which take the index; as signed integers, those of negative
+// ones inverted but for the sign, they are in order.
 template <class T>
 struct Key {
-    using K = uint32_t;
-    __device__ static __forceinline__ K make(float x, int index) {
-        const uint32_t b = __float_as_uint(x + 0.0f) >> 16;
-        uint32_t k;
-        if constexpr (std::is_same_v<T, _Float16>) {
-            const uint32_t h = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x + 0.0f));
-            k = h & 0x8000u ? ~h & 0xffffu : h | 0x8000u;
-        } else {
-            k = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
-        }
-        return x > -__builtin_inff() ? k << kIndexBits | (kIndexMask - static_cast<uint32_t>(index)) : 0u;
+    using K = int32_t;
+    static constexpr uint32_t kInf = 0x7f800000u;
+    __device__ static __forceinline__ uint32_t ordered(uint32_t b) {
+        return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) & 0x7fffffffu);
     }
-    __device__ static __forceinline__ K none() { return 0u; }
+    __device__ static __forceinline__ K make(float x, int index) {
+        return static_cast<K>((ordered(__float_as_uint(x)) & ~kIndexMask) | (kIndexMask - static_cast<uint32_t>(index)));
+    }
+    __device__ static __forceinline__ K none() { return INT32_MIN; }
     __device__ static __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
     __device__ static __forceinline__ K smaller(K a, K b) { return a > b ? b : a; }
-    __device__ static __forceinline__ bool expert(K k) { return k > kIndexMask; }
-    __device__ static __forceinline__ int index(K k) { return static_cast<int>(kIndexMask - (k & kIndexMask)); }
+    // above those of -infinity, which end in other bits than 0
+    __device__ static __forceinline__ bool expert(K k) { return k >= static_cast<K>(0x80800000u); }
+    __device__ static __forceinline__ int index(K k) {
+        return static_cast<int>(kIndexMask - (static_cast<uint32_t>(k) & kIndexMask));
+    }
     __device__ static __forceinline__ float value(K k) {
-        const uint32_t o = k >> kIndexBits, b = o & 0x8000u ? o & 0x7fffu : ~o & 0xffffu;
-        if constexpr (std::is_same_v<T, _Float16>)
-            return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b)));
-        else
-            return __uint_as_float(b << 16);
+        return __uint_as_float(ordered(static_cast<uint32_t>(k)) & ~kIndexMask);
     }
 };
+// An fp32 logit is the high half of a double, which orders such halves as floats
+// (none reaches the exponent of NaN: that of infinity is 0x7f8 of 0x7ff), with the
+// index behind it, inverted where the sign inverts the order. Maxima are one
+// instruction.
 template <>
 struct Key<float> {
     using K = double;
-    static constexpr uint64_t kBase = 0x4330000000000000ull;
-    __device__ static __forceinline__ uint64_t bits(K k) { return static_cast<uint64_t>(__double_as_longlong(k)); }
-    __device__ static __forceinline__ K make(float x, int index) {
-        const uint32_t b = __float_as_uint(x + 0.0f);
-        const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-        const uint64_t k = static_cast<uint64_t>(o) << kIndexBits | (kIndexMask - static_cast<uint32_t>(index));
-        return __longlong_as_double(static_cast<long long>(x > -__builtin_inff() ? kBase | k : kBase));
+    __device__ static __forceinline__ uint32_t high(K k) {
+        return static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(k)) >> 32);
     }
-    __device__ static __forceinline__ K none() { return 0x1p52; }
+    __device__ static __forceinline__ uint32_t low(K k) {
+        return static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(k)));
+    }
+    __device__ static __forceinline__ K of(uint32_t hi, uint32_t lo) {
+        return __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(hi) << 32 | lo));
+    }
+    __device__ static __forceinline__ K make(float x, int index) {
+        const uint32_t b = __float_as_uint(x);
+        return of(b, ~static_cast<uint32_t>(index) ^ static_cast<uint32_t>(static_cast<int32_t>(b) >> 31));
+    }
+    __device__ static __forceinline__ K none() { return of(0xff800000u, ~0u); }
     // no key is NaN, so the instructions are used as they are
     __device__ static __forceinline__ K larger(K a, K b) {
         K r;
@@ -172,19 +227,19 @@ struct Key<float> {
         asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
         return r;
     }
-    __device__ static __forceinline__ bool expert(K k) { return bits(k) - kBase > kIndexMask; }
+    __device__ static __forceinline__ bool expert(K k) { return high(k) != 0xff800000u; }
     __device__ static __forceinline__ int index(K k) {
-        return static_cast<int>(kIndexMask - (static_cast<uint32_t>(bits(k)) & kIndexMask));
+        return static_cast<int>(~(low(k) ^ static_cast<uint32_t>(static_cast<int32_t>(high(k)) >> 31)));
     }
-    __device__ static __forceinline__ float value(K k) {
-        const uint32_t o = static_cast<uint32_t>((bits(k) - kBase) >> kIndexBits);
-        return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
-    }
+    __device__ static __forceinline__ float value(K k) { return __uint_as_float(high(k)); }
 };
 
 // a where mask is 0, b where it is all ones (a choice by a condition between
 // two elements of an array becomes an index into it, and that sixteen selects)
 __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return a ^ ((a ^ b) & mask); }
+__device__ __forceinline__ int32_t pick(uint32_t mask, int32_t a, int32_t b) {
+    return static_cast<int32_t>(pick(mask, static_cast<uint32_t>(a), static_cast<uint32_t>(b)));
+}
 __device__ __forceinline__ double pick(uint32_t mask, double a, double b) {
     const uint64_t x = static_cast<uint64_t>(__double_as_longlong(a)), y = static_cast<uint64_t>(__double_as_longlong(b));
     const uint32_t lo = pick(mask, static_cast<uint32_t>(x), static_cast<uint32_t>(y));
@@ -199,10 +254,26 @@ __device__ __forceinline__ void exchange(typename Q::K &a, typename Q::K &b) {
     a = big;
 }
 
-// The TOP largest keys of a lane's N, largest first, in its first places: by
-// merging of odd and even places (63 exchanges for 16), for 8 of more in runs of
-// 8, of two of which the larger half is kept and put in order (19 an run, 8
-// maxima and 12 a merge: 108 instructions for 8 of 16 against 126).
+// Of two runs of TOP keys, largest first, the larger half, again in order.
+template <class Q, int TOP, class F>
+__device__ __forceinline__ void merge_keys(typename Q::K *k, F other) {
+#pragma unroll
+    for (int i = 0; i < TOP / 2; ++i) {
+        const auto a = Q::larger(k[i], other(TOP - 1 - i)), b = Q::larger(k[TOP - 1 - i], other(i));
+        k[i] = a;
+        k[TOP - 1 - i] = b;
+    }
+#pragma unroll
+    for (int h = TOP / 2; h >= 1; h /= 2) {
+#pragma unroll
+        for (int i = 0; i < TOP; ++i)
+            if ((i & h) == 0) exchange<Q>(k[i], k[i + h]);
+    }
+}
+
+// The TOP largest keys of a lane's N, largest first, in its first places: runs
+// of TOP sorted by merging of odd and even places, and merged (8 of 16: 2 x 19
+// exchanges, 8 maxima and 12 exchanges).
 template <class Q, int N, int TOP>
 __device__ __forceinline__ void sort_keys(typename Q::K (&k)[N]) {
 #pragma unroll
@@ -221,15 +292,19 @@ __device__ __forceinline__ void sort_keys(typename Q::K (&k)[N]) {
                 }
             }
         }
-        if (run == 0) continue;
+        if (run > 0) merge_keys<Q, TOP>(k, [&](int i) { return k[run + i]; });
+    }
+}
+
+// The TOP largest of the group's, largest first, in every lane of it.
+template <class Q, int G, int TOP, int STEP = 1>
+__device__ __forceinline__ void merge_group(typename Q::K *k) {
+    if constexpr (STEP < G) {
+        typename Q::K other[TOP];
 #pragma unroll
-        for (int i = 0; i < TOP; ++i) k[i] = Q::larger(k[i], k[run + TOP - 1 - i]);
-#pragma unroll
-        for (int h = TOP / 2; h >= 1; h /= 2) {
-#pragma unroll
-            for (int i = 0; i < TOP; ++i)
-                if ((i & h) == 0) exchange<Q>(k[i], k[i + h]);
-        }
+        for (int i = 0; i < TOP; ++i) other[i] = partner<STEP>(k[i]);
+        merge_keys<Q, TOP>(k, [&](int i) { return other[i]; });
+        merge_group<Q, G, TOP, 2 * STEP>(k);
     }
 }
 
@@ -292,8 +367,10 @@ struct RouteArgs {
 template <int N, bool BALANCE>
 constexpr int kThreads = !BALANCE ? kRouteBlock : (N > 16 ? 512 : 1024);
 
-// TOP: of the lane's logits, how many may be chosen (8 where `per` is no more).
-template <class T, int G, int N, int TOP, bool BALANCE>
+// MERGE: up to TOP are chosen, 4 or 8, and the lanes' runs of them are merged
+// (48 instructions a step for 8 of fp32); otherwise TOP = N, and each is found by a
+// maximum over the heads of the lanes' runs, and taken off its run (32 and more).
+template <class T, int G, int N, int TOP, bool MERGE, bool BALANCE>
 __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs a) {
     using H = Held<T, G, N>;
     using Q = Key<T>;
@@ -305,6 +382,7 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
     __shared__ float s_share[BALANCE ? kHalf : 1][BALANCE ? G * N : 1];
     const int lane = lane_id();
     const int sub = lane & (G - 1);
+    const H held(sub, a.experts);
     float share[N];
     if constexpr (BALANCE) {
         for (int e = threadIdx.x; e <= G * N; e += kBlock) s_count[e] = 0;
@@ -313,13 +391,30 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
         for (int j = 0; j < N; ++j) share[j] = 0.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     }
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTokens; base < a.tokens;
-         base += static_cast<int64_t>(gridDim.x) * kTokens) {
+    // a row's loads are on their way while the one before it is worked on, where
+    // the registers hold both
+    constexpr bool kAhead = MERGE || !BALANCE;
+    typename H::Raw raw[H::kChunks];
+    bool live;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+    const auto fetch = [&](int64_t t) {
+        const int64_t row = t < a.tokens ? t : a.tokens - 1;
+        held.fetch(static_cast<const T *>(a.logits) + row * a.stride, raw);
+        live = t < a.tokens && (a.live == nullptr || a.live[row] != 0);
+    };
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * kTokens;
+    if (kAhead && begin < a.tokens) fetch(begin + threadIdx.x / G);
+    for (int64_t base = begin; base < a.tokens; base += step) {
         const int64_t t = base + threadIdx.x / G;
         const bool inside = t < a.tokens;
-        const bool live = inside && (a.live == nullptr || a.live[t] != 0);
         float x[N], p[N];
-        H::load(static_cast<const T *>(a.logits) + (live ? t : 0) * a.stride, sub, live ? a.experts : 0, x);
+        if (!kAhead) fetch(t);
+        held.unpack(raw, x);
+        if (__builtin_expect(ballot(!live) != 0, 0)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = live ? x[j] : -__builtin_inff();
+        }
+        if (kAhead && base + step < a.tokens) fetch(t + step);
         Softmax<G, N> sm;
         sm.make(x, p);
         if constexpr (BALANCE) {
@@ -330,32 +425,42 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
         }
         K key[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) key[j] = Q::make(x[j], H::at(sub, j));
+        for (int j = 0; j < N; ++j) key[j] = Q::make(x[j], held.index(j));
         sort_keys<Q, N, TOP>(key);
         // G places a round, one to a lane; exponentials wait for their sum where
         // they will be read again: in a register, or in the weights if there are more
         float e = 0.0f, chosen = 0.0f;
-        for (int r = 0; r < a.per; r += G) {
-            const int most = a.per - r < G ? a.per - r : G;
-            K place = Q::none();
-            for (int k = 0; k < most; ++k) {
-                const K best = over_group<G>(key[0], Q::larger);
-                const uint32_t mine = best == key[0] ? ~0u : 0u;
-#pragma unroll
-                for (int j = 0; j + 1 < TOP; ++j) key[j] = pick(mine, key[j], key[j + 1]);
-                key[TOP - 1] = pick(mine, key[TOP - 1], Q::none());
-                place = pick(sub == k ? ~0u : 0u, place, best);
-            }
-            const float v = Q::value(place);
+        const auto take = [&](K place, int r, int most) {
             const bool expert = Q::expert(place);
             const int id = expert ? Q::index(place) : -1;
-            e = expert ? sm.weight(v) : 0.0f;
+            e = expert ? sm.weight(Q::value(place)) : 0.0f;
             chosen += e;
             if (inside && sub < most) {
                 a.ids[t * a.per + r + sub] = id;
                 if (a.per > G) a.weights[t * a.per + r + sub] = e;
                 if (BALANCE && id >= 0)
                     __hip_atomic_fetch_add(&s_count[id], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+        };
+        if constexpr (MERGE) {
+            merge_group<Q, G, TOP>(key);
+            K place = Q::none();
+#pragma unroll
+            for (int i = 0; i < TOP; ++i) place = pick(sub == i && i < a.per ? ~0u : 0u, place, key[i]);
+            take(place, 0, a.per);
+        } else {
+            for (int r = 0; r < a.per; r += G) {
+                const int most = a.per - r < G ? a.per - r : G;
+                K place = Q::none();
+                for (int k = 0; k < most; ++k) {
+                    const K best = over_group<G>(key[0], Q::larger);
+                    const uint32_t mine = best == key[0] ? ~0u : 0u;
+#pragma unroll
+                    for (int j = 0; j + 1 < N; ++j) key[j] = pick(mine, key[j], key[j + 1]);
+                    key[N - 1] = pick(mine, key[N - 1], Q::none());
+                    place = pick(sub == k ? ~0u : 0u, place, best);
+                }
+                take(place, r, most);
             }
         }
         float inv = sm.inv;
@@ -376,14 +481,13 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
         const int w = static_cast<int>(uniform(threadIdx.x / kWave));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-#pragma unroll
-            for (int off = G; off < kWave; off *= 2) share[j] += __shfl_xor(share[j], off);
-            if (w >= kHalf && lane < G) s_share[w - kHalf][H::at(sub, j)] = share[j];
+            share[j] = over_groups<G>(share[j]);
+            if (w >= kHalf && lane < G && held.own(j)) s_share[w - kHalf][held.index(j)] = share[j];
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (w < kHalf && lane < G) s_share[w][H::at(sub, j)] += share[j];
+            if (w < kHalf && lane < G && held.own(j)) s_share[w][held.index(j)] += share[j];
         __syncthreads();
         float *to = a.part_share + static_cast<int64_t>(blockIdx.x) * a.experts;
         int32_t *count = a.part_count + static_cast<int64_t>(blockIdx.x) * (a.experts + 1);
@@ -398,71 +502,79 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
     }
 }
 
-// The workgroups' sums joined: 16 experts to a workgroup, sixteen threads to an
-// expert, in fp64. The workgroup that is done last adds the loss.
+// The workgroups' sums joined, in fp64: 16 experts to a workgroup, 64 threads
+// to an expert. The workgroup that is done last adds the loss.
+constexpr int kJoinBlock = 1024;
 constexpr int kJoinCols = 16;
-constexpr int kJoinRows = kRouteBlock / kJoinCols;
-constexpr int kJoinWaves = kRouteBlock / kWave;
+constexpr int kJoinRows = kJoinBlock / kJoinCols;
+constexpr int kJoinWaves = kJoinBlock / kWave;
 
-__global__ __launch_bounds__(kRouteBlock) void route_join_kernel(RouteArgs a, int blocks, int32_t *__restrict__ counts,
+__global__ __launch_bounds__(kJoinBlock) void route_join_kernel(RouteArgs a, int blocks, int32_t *__restrict__ counts,
                                                                 float *__restrict__ share, float *__restrict__ loss) {
-    __shared__ double s_p[kJoinRows][kJoinCols + 1];
-    __shared__ int32_t s_c[kJoinRows][kJoinCols + 1];
+    __shared__ double s_p[kJoinWaves][kJoinCols];
+    __shared__ int32_t s_c[kJoinWaves][kJoinCols];
     __shared__ int32_t s_live[kJoinWaves];
-    __shared__ double s_loss[kJoinCols];
-    __shared__ uint32_t s_last;
-    const int col = threadIdx.x % kJoinCols, row = threadIdx.x / kJoinCols;
-    const int e = blockIdx.x * kJoinCols + col;
-    int32_t n = 0;
-    for (int b = threadIdx.x; b < blocks; b += kRouteBlock)
-        n += a.part_count[static_cast<int64_t>(b) * (a.experts + 1) + a.experts];
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off);
-    if (lane_id() == 0) s_live[threadIdx.x / kWave] = n;
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    const int col = lane % kJoinCols;
+    const int e = static_cast<int>(blockIdx.x) * kJoinCols + col;
+    const int at = e < a.experts ? e : a.experts - 1;
     double p = 0.0;
-    int32_t c = 0;
-    if (e < a.experts) {
-#pragma unroll 8
-        for (int b = row; b < blocks; b += kJoinRows) {
-            p += static_cast<double>(a.part_share[static_cast<int64_t>(b) * a.experts + e]);
-            c += a.part_count[static_cast<int64_t>(b) * (a.experts + 1) + e];
-        }
+    int32_t c = 0, n = 0;
+#pragma unroll 4
+    for (int b = static_cast<int>(threadIdx.x) / kJoinCols; b < blocks; b += kJoinRows) {
+        p += static_cast<double>(a.part_share[static_cast<int64_t>(b) * a.experts + at]);
+        c += a.part_count[static_cast<int64_t>(b) * (a.experts + 1) + at];
+        n += a.part_count[static_cast<int64_t>(b) * (a.experts + 1) + a.experts];
     }
-    s_p[row][col] = p;
-    s_c[row][col] = c;
+#pragma unroll
+    for (int off = kJoinCols; off < kWave; off *= 2) {
+        p += __shfl_xor(p, off);
+        c += __shfl_xor(c, off);
+        n += __shfl_xor(n, off);
+    }
+    if (lane < kJoinCols) {
+        s_p[w][col] = p;
+        s_c[w][col] = c;
+        s_live[w] = n;
+    }
     __syncthreads();
+    if (w > 0) return;
+    p = 0.0;
+    c = 0;
     n = 0;
-    for (int w = 0; w < kJoinWaves; ++w) n += s_live[w];
-    if (row == 0) {
-        p = 0.0;
-        c = 0;
-        for (int r = 0; r < kJoinRows; ++r) {
-            p += s_p[r][col];
-            c += s_c[r][col];
-        }
-        p = n > 0 ? p / n : 0.0;
-        if (e < a.experts) {
-            share[e] = static_cast<float>(p);
-            counts[e] = c;
-        }
-        s_loss[col] = e < a.experts ? p * c : 0.0;
+#pragma unroll
+    for (int v = 0; v < kJoinWaves; ++v) {
+        p += s_p[v][col];
+        c += s_c[v][col];
+        n += s_live[v];
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < kJoinCols; ++i) s += s_loss[i];
+    p = n > 0 ? p / n : 0.0;
+    if (lane < kJoinCols && e < a.experts) {
+        share[e] = static_cast<float>(p);
+        counts[e] = c;
+    }
+    double s = e < a.experts ? p * c : 0.0;
+#pragma unroll
+    for (int off = 1; off < kJoinCols; off *= 2) s += __shfl_xor(s, off);
+    uint32_t before = 0;
+    if (lane == 0) {
+        if (blockIdx.x == 0) counts[a.experts] = n;
         __hip_atomic_store(a.part_loss + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        // acknowledged before the workgroup counts as done
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        before = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) counts[a.experts] = n;
-    __syncthreads();
-    if (s_last == gridDim.x - 1 && threadIdx.x == 0) {
-        double s = 0.0;
-        for (uint32_t b = 0; b < gridDim.x; ++b)
-            s += __hip_atomic_load(a.part_loss + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *loss = static_cast<float>(n > 0 ? s * a.experts / (static_cast<double>(n) * a.per) : 0.0);
-    }
+    if (uniform(before) != gridDim.x - 1) return;
+    // up to 64 workgroups, a lane each, added in one order
+    s = lane < static_cast<int>(gridDim.x)
+            ? __hip_atomic_load(a.part_loss + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+            : 0.0;
+#pragma unroll
+    for (int off = 1; off < kWave; off *= 2) s += __shfl_xor(s, off);
+    if (lane == 0) *loss = static_cast<float>(n > 0 ? s * a.experts / (static_cast<double>(n) * a.per) : 0.0);
 }
+static_assert(kExpertsMax / kJoinCols <= kWave, "a lane a workgroup");
 
 // The gradient. What a chosen expert adds is computed by the lane that holds
 // its place among the chosen and handed to the lane that holds its logit
@@ -488,39 +600,75 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
     const int lane = lane_id();
     const int sub = lane & (G - 1);
     float *add = s_add + (threadIdx.x / G) * (G * N);  // of this token
+    const H held(sub, a.experts);
     float even[N];
-    const int64_t n = a.counts != nullptr ? a.counts[a.experts] : 0;
-    const double each = n > 0 ? static_cast<double>(*a.dloss) * a.experts / (static_cast<double>(n) * n * a.per) : 0.0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int e = H::at(sub, j);
-        even[j] = n > 0 && e < a.experts ? static_cast<float>(each * a.counts[e]) : 0.0f;
+        even[j] = 0.0f;
         add[sub + j * G] = 0.0f;
     }
+    if (a.counts != nullptr) {
+        const int64_t n = a.counts[a.experts];
+        const float each = static_cast<float>(
+            n > 0 ? static_cast<double>(*a.dloss) * a.experts / (static_cast<double>(n) * n * a.per) : 0.0);
+        int32_t c[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            c[j] = a.counts[H::kWide || held.index(j) < a.experts ? held.index(j) : a.experts - 1];
+#pragma unroll
+        for (int j = 0; j < N; ++j) even[j] = each * static_cast<float>(c[j]);
+    }
     wave_lds_order();
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTokens; base < a.tokens;
-         base += static_cast<int64_t>(gridDim.x) * kTokens) {
+    // this lane's place of a round of G among the chosen
+    struct Chosen {
+        int id;
+        float d, x;
+    };
+    // A row's loads, and those of its first G chosen, are on their way while the
+    // one before it is worked on; none waits behind a branch: what is not wanted
+    // is read all the same.
+    typename H::Raw raw[H::kChunks];
+    int next_id = -1;
+    float next_d = 0.0f;
+    bool next_live;
+    const auto fetch = [&](int64_t t) {
+        const int64_t in = t < a.tokens ? t : a.tokens - 1;
+        if (a.dweights != nullptr) {
+            const int64_t at = in * a.per + (sub < a.per ? sub : a.per - 1);
+            next_id = a.ids[at];
+            next_d = a.dweights[at];
+        }
+        held.fetch(static_cast<const T *>(a.logits) + in * a.stride, raw);
+        next_live = t < a.tokens && (a.live == nullptr || a.live[in] != 0);
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+    fetch(static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / G);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kTokens; base < a.tokens; base += step) {
         const int64_t t = base + threadIdx.x / G;
         const bool inside = t < a.tokens;
-        const bool live = inside && (a.live == nullptr || a.live[t] != 0);
-        const T *row = static_cast<const T *>(a.logits) + (live ? t : 0) * a.stride;
-        // this lane's place of a round of G among the chosen
-        struct Chosen {
-            int id;
-            float d, x;
-        };
+        const bool live = next_live;
+        const T *row = static_cast<const T *>(a.logits) + (inside ? t : a.tokens - 1) * a.stride;
+        Chosen first{-1, 0.0f, -__builtin_inff()};
+        if (sub < a.per && next_id >= 0 && next_id < a.experts && live) first = {next_id, next_d, 0.0f};
+        // in a cache by now
+        const float first_x = static_cast<float>(row[first.id >= 0 ? first.id : 0]);
         const auto chosen = [&](int k) -> Chosen {
             if (!live || k >= a.per || a.dweights == nullptr) return {-1, 0.0f, -__builtin_inff()};
             const int id = a.ids[t * a.per + k];
             const float d = a.dweights[t * a.per + k];
             if (id < 0 || id >= a.experts) return {-1, 0.0f, -__builtin_inff()};
-            return {id, d, fmaxf(static_cast<float>(row[id]), -__builtin_inff())};  // NaN as -infinity
+            return {id, d, fmaxf(static_cast<float>(row[id]), -__builtin_inff())};
         };
-        const Chosen first = chosen(sub);
         float x[N], p[N];
-        H::load(row, sub, live ? a.experts : 0, x);
+        held.unpack(raw, x);
+        if (__builtin_expect(ballot(!live) != 0, 0)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = live ? x[j] : -__builtin_inff();
+        }
+        if (base + step < a.tokens) fetch(t + step);
         Softmax<G, N> sm;
         sm.make(x, p);
+        if (first.id >= 0) first.x = fmaxf(first_x, -__builtin_inff());  // NaN as -infinity
         const float y = sm.weight(sm.lifted(first.x));
         float w = y, wd = y > 0.0f ? y * first.d : 0.0f;
         for (int k = G + sub; k - sub < a.per; k += G) {
@@ -553,8 +701,11 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
         if (!a.normalize) s += mean;
         wave_lds_order();
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            p[j] = sm.sum > 0.0f ? __builtin_fmaf(p[j], even[j] - s, add[H::at(sub, j)]) : 0.0f;
+        for (int j = 0; j < N; ++j) p[j] = __builtin_fmaf(p[j], even[j] - s, add[held.index(j)]);
+        if (__builtin_expect(ballot(!(sm.sum > 0.0f)) != 0, 0)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) p[j] = sm.sum > 0.0f ? p[j] : 0.0f;
+        }
         wave_lds_order();
         if (first.id >= 0) add[first.id] = 0.0f;
         for (int k = G + sub; k < a.per; k += G) {
@@ -562,7 +713,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_grad_kernel(RouteGradArgs a
             if (c.id >= 0) add[c.id] = 0.0f;
         }
         wave_lds_order();
-        if (inside) H::store(static_cast<T *>(a.dlogits) + t * a.experts, sub, a.experts, p);
+        if (inside) held.store(static_cast<T *>(a.dlogits) + t * a.experts, p);
     }
 }
 
@@ -682,25 +833,29 @@ int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t expert
         using T = decltype(t);
         return with_row(experts, [&](auto g, auto n) {
             constexpr int G = decltype(g)::value, N = decltype(n)::value;
-            const auto launch = [&](auto top) {
+            const auto launch = [&](auto top, auto merge) {
                 constexpr int TOP = decltype(top)::value;
+                constexpr bool M = decltype(merge)::value;
                 const int64_t all = (tokens + kRouteBlock / G - 1) / (kRouteBlock / G);
                 if (balance)
-                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, true>), dim3(static_cast<unsigned>(p.blocks)),
+                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, M, true>), dim3(static_cast<unsigned>(p.blocks)),
                                        dim3((kThreads<N, true>)), 0, s, a);
                 else
-                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, false>),
+                    hipLaunchKernelGGL((route_kernel<T, G, N, TOP, M, false>),
                                        dim3(static_cast<unsigned>(all < 8192 ? all : 8192)),
                                        dim3((kThreads<N, false>)), 0, s, a);
                 return launched();
             };
-            if (N > 8 && per <= 8) return launch(std::integral_constant<int, (N > 8 ? 8 : N)>{});
-            return launch(std::integral_constant<int, N>{});
+            if constexpr (N >= 8) {
+                if (per <= 4) return launch(std::integral_constant<int, 4>{}, std::true_type{});
+                if (per <= 8) return launch(std::integral_constant<int, 8>{}, std::true_type{});
+            }
+            return launch(std::integral_constant<int, N>{}, std::false_type{});
         });
     }));
     if (!balance) return SSC_OK;
     hipLaunchKernelGGL(route_join_kernel, dim3(static_cast<unsigned>((experts + kJoinCols - 1) / kJoinCols)),
-                       dim3(kRouteBlock), 0, s, a, static_cast<int>(p.blocks), counts, share, loss);
+                       dim3(kJoinBlock), 0, s, a, static_cast<int>(p.blocks), counts, share, loss);
     return launched();
 }
 
@@ -744,7 +899,7 @@ int ssc_route_rows_grad(const void *logits, int dtype, int64_t tokens, int64_t e
         return with_row(experts, [&](auto g, auto n) {
             constexpr int G = decltype(g)::value, N = decltype(n)::value;
             const int64_t all = (tokens + kRouteBlock / G - 1) / (kRouteBlock / G);
-            hipLaunchKernelGGL((route_grad_kernel<T, G, N>), dim3(static_cast<unsigned>(all < 2048 ? all : 2048)),
+            hipLaunchKernelGGL((route_grad_kernel<T, G, N>), dim3(static_cast<unsigned>(all < 1024 ? all : 1024)),
                                dim3(kRouteBlock), 0, static_cast<hipStream_t>(stream), a);
             return launched();
         });
