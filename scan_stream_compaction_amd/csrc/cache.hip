@@ -171,13 +171,6 @@ struct EvictArgs {
     uint32_t *hist;         // [2][rows][splits][bins] of this pass and the one before
 };
 
-// The score as an integer of the same order; NaN as the lowest, -0 as 0.
-__device__ __forceinline__ uint32_t score_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return x == x ? k : 0u;
-}
-
 __device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : (pass == 1 ? 10 : 0); }
 __device__ __forceinline__ uint32_t digit_bins(int pass) { return pass == 2 ? 1024u : 2048u; }
 
@@ -185,12 +178,11 @@ __device__ __forceinline__ uint32_t digit_bins(int pass) { return pass == 2 ? 10
 struct Head {
     const float *scores;
     int32_t *kept;
-    uint32_t len, begin, end, need;
+    uint32_t len, begin, end;
 
     __device__ __forceinline__ Head(const EvictArgs &a, int64_t h, int64_t b) {
-        const int64_t bh = b * a.heads + h;
         scores = a.scores + b * a.score_batch + h * a.score_head;
-        kept = a.kept + bh * a.keep;
+        kept = a.kept + (b * a.heads + h) * a.keep;
         len = a.capacity;
         if (a.lengths != nullptr) {
             const int32_t l = a.lengths[b];
@@ -198,15 +190,32 @@ struct Head {
         }
         begin = a.first;
         end = len - a.recent;  // used where len > keep
-        need = a.keep - a.first - a.recent;
     }
-    __device__ __forceinline__ Threshold start() const { return {need == 0 ? ~0u : 0u, 0u, need, need == 0}; }
-    __device__ __forceinline__ bool open(uint32_t i) const { return i >= begin && i < end; }
-    __device__ __forceinline__ bool always(uint32_t i) const { return i < begin || (i >= end && i < len); }
     // up to `keep` positions: all stay; by `stride` threads
-    __device__ __forceinline__ void keep_all(const EvictArgs &a, int64_t bh, uint32_t thread, uint32_t stride) const {
+    __device__ __forceinline__ void keep_all(const EvictArgs &a, int32_t *count, uint32_t thread, uint32_t stride) const {
         for (uint32_t s = thread; s < a.keep; s += stride) kept[s] = s < len ? static_cast<int32_t>(s) : -1;
-        if (thread == 0) a.counts[bh] = static_cast<int32_t>(len);
+        if (thread == 0) *count = static_cast<int32_t>(len);
+    }
+    // The scores at base, base + 64, ... as integers of the same order. Positions
+    // that stay in any case are above all, NaN is below all scores, -0 as 0, and
+    // positions at or past `to` are below that.
+    template <int ITEMS>
+    __device__ __forceinline__ void load(uint32_t base, uint32_t to, uint32_t (&key)[ITEMS]) const {
+        float x[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t i = base + j * kWave;
+            x[j] = scores[i < len ? i : len - 1u];
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t i = base + j * kWave;
+            const uint32_t b = __float_as_uint(x[j] + 0.0f);
+            uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+            k = x[j] == x[j] ? k : 1u;
+            k = i - begin < end - begin ? k : ~0u;
+            key[j] = i < to ? k : 0u;
+        }
     }
 };
 
@@ -217,19 +226,31 @@ struct EvictShared {
     uint32_t digit, above, inside, before;
 };
 
-// Many scores may be equal (0 above all): the lanes that share the first active
-// lane's digit are counted by one add.
+// Counts a wavefront's digits, where they count. Many scores may be equal (0
+// above all): the lanes that share the first one's digit are counted by one add.
 __device__ __forceinline__ void count_digit(uint32_t *hist, uint32_t d, bool counts) {
     const uint64_t active = ballot(counts);
     if (active == 0) return;
     const int leader = __builtin_ctzll(active);
     const uint32_t common = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(d), leader));
-    const uint64_t same = ballot(counts && d == common);
-    if (lane_id() == leader)
-        __hip_atomic_fetch_add(&hist[common], static_cast<uint32_t>(__builtin_popcountll(same)), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_WORKGROUP);
-    else if (counts && d != common)
-        __hip_atomic_fetch_add(&hist[d], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    const bool same = d == common;
+    const uint32_t many = static_cast<uint32_t>(__builtin_popcountll(ballot(same) & active));
+    const bool leads = lane_id() == leader;
+    if ((counts && !same) || leads)
+        __hip_atomic_fetch_add(&hist[d], leads ? many : 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+template <int ITEMS>
+__device__ __forceinline__ void count_digits(uint32_t *hist, const uint32_t (&key)[ITEMS], const Threshold &t, int pass) {
+    if (pass == 0) {
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) count_digit(hist, key[j] >> 21, true);
+    } else {
+        const uint32_t bins = digit_bins(pass);
+        const int shift = digit_shift(pass);
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) count_digit(hist, (key[j] >> shift) & (bins - 1u), (key[j] & t.fixed) == t.low);
+    }
 }
 
 // The digit that the need-th largest falls into; c0 and c1 are the counts of this
@@ -260,78 +281,86 @@ __device__ __forceinline__ void find_digit(EvictShared &sh, uint32_t c0, uint32_
     t.all = t.need == sh.inside;
 }
 
-__device__ __forceinline__ bool better(const Threshold &t, uint32_t k) { return t.all ? k >= t.low : k > t.low; }
+// This wavefront's keys that stay, by item: those better than the threshold, and
+// those equal to it where not all of them stay.
+template <int ITEMS>
+struct Staying {
+    bool sure[ITEMS], equal[ITEMS];
+    uint32_t sures, equals;
+
+    __device__ __forceinline__ Staying(const uint32_t (&key)[ITEMS], const Threshold &t) : sures(0), equals(0) {
+        const uint32_t from = t.all ? t.low : t.low + 1u;  // no threshold that others are equal to is the largest
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            sure[j] = key[j] >= from;
+            equal[j] = key[j] == t.low && !t.all;
+            sures += static_cast<uint32_t>(__builtin_popcountll(ballot(sure[j])));
+            equals += static_cast<uint32_t>(__builtin_popcountll(ballot(equal[j])));
+        }
+    }
+    // their positions, base + 64 j, from slot `at` on; of the equal ones, of which
+    // `run` came before, the first `need` of all
+    __device__ __forceinline__ void emit(const EvictArgs &a, const Head &head, uint32_t base, uint32_t at, uint32_t run,
+                                         uint32_t need) const {
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint64_t same = ballot(equal[j]);
+            bool yes = sure[j];
+            if (same != 0) {
+                yes = yes || (equal[j] && run + mbcnt64(same) < need);
+                run += static_cast<uint32_t>(__builtin_popcountll(same));
+            }
+            const uint64_t all = ballot(yes);
+            const uint32_t slot = at + mbcnt64(all);
+            if (yes && slot < a.keep) head.kept[slot] = static_cast<int32_t>(base + j * kWave);
+            at += static_cast<uint32_t>(__builtin_popcountll(all));
+        }
+    }
+};
+
+// Sums over the wavefronts of what their lane 0 put into LDS: of those before
+// wavefront w, and of all.
+__device__ __forceinline__ uint32_t waves_before(const uint32_t *values, int w, uint32_t &all) {
+    const uint32_t v = wave_inclusive_scan<SumU32>(lane_id() < kEvictWaves ? values[lane_id()] : 0u);
+    all = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), kEvictWaves - 1));
+    return w == 0 ? 0u : static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), w - 1));
+}
+
+__device__ __forceinline__ uint32_t least(uint32_t x, uint32_t y) { return x < y ? x : y; }
 
 template <int ITEMS>
 __global__ __launch_bounds__(kEvictBlock) void evict_kernel(EvictArgs a) {
     __shared__ EvictShared sh;
-    const int64_t bh = static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
     const Head head(a, blockIdx.x, blockIdx.y);
+    int32_t *count = a.counts + static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
     if (head.len <= a.keep) {
-        head.keep_all(a, bh, threadIdx.x, kEvictBlock);
+        head.keep_all(a, count, threadIdx.x, kEvictBlock);
         return;
     }
-    const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const uint32_t base = static_cast<uint32_t>(w) * ITEMS * kWave + lane;
+    const uint32_t base = static_cast<uint32_t>(w) * ITEMS * kWave + lane_id();
     uint32_t key[ITEMS];
-    {
-        float x[ITEMS];
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            const uint32_t i = base + j * kWave;
-            x[j] = head.open(i) ? head.scores[i] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) key[j] = score_key(x[j]);
-    }
-    Threshold t = head.start();
+    head.load(base, head.len, key);
+    Threshold t{0u, 0u, a.keep, 0u};
     for (int pass = 0; pass < kEvictPasses && !t.all; ++pass) {
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j)
-            count_digit(sh.hist, (key[j] >> digit_shift(pass)) & (digit_bins(pass) - 1u),
-                        head.open(base + j * kWave) && (key[j] & t.fixed) == t.low);
+        count_digits(sh.hist, key, t, pass);
         __syncthreads();
         const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
         find_digit(sh, sh.hist[top], sh.hist[top - 1u], pass, t);
     }
-    // the wavefront's share: those that stay in any case, and those equal
-    uint32_t sure = 0, equal = 0;
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        const uint32_t i = base + j * kWave;
-        const bool open = head.open(i);
-        sure += static_cast<uint32_t>(__builtin_popcountll(ballot(head.always(i) || (open && better(t, key[j])))));
-        equal += static_cast<uint32_t>(__builtin_popcountll(ballot(open && !t.all && key[j] == t.low)));
+    const Staying<ITEMS> stay(key, t);
+    __syncthreads();
+    if (lane_id() == 0) {
+        sh.wave[w] = stay.sures;
+        sh.wave_equal[w] = stay.equals;
     }
     __syncthreads();
-    if (lane == 0) {
-        sh.wave[w] = sure;
-        sh.wave_equal[w] = equal;
-    }
-    __syncthreads();
-    uint32_t at = 0, equals = 0;
-    for (int v = 0; v < w; ++v) {
-        at += sh.wave[v];
-        equals += sh.wave_equal[v];
-    }
-    at += equals < t.need ? equals : t.need;
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        const uint32_t i = base + j * kWave;
-        const bool open = head.open(i);
-        const bool same = open && !t.all && key[j] == t.low;
-        const uint64_t sames = ballot(same);
-        const bool yes = head.always(i) || (open && better(t, key[j])) || (same && equals + mbcnt64(sames) < t.need);
-        equals += static_cast<uint32_t>(__builtin_popcountll(sames));
-        const uint64_t yeses = ballot(yes);
-        const uint32_t slot = at + mbcnt64(yeses);
-        if (yes && slot < a.keep) head.kept[slot] = static_cast<int32_t>(i);
-        at += static_cast<uint32_t>(__builtin_popcountll(yeses));
-    }
-    if (threadIdx.x == 0) a.counts[bh] = static_cast<int32_t>(a.keep);
+    uint32_t all;
+    const uint32_t run = waves_before(sh.wave_equal, w, all);
+    stay.emit(a, head, base, waves_before(sh.wave, w, all) + least(run, t.need), run, t.need);
+    if (threadIdx.x == 0) *count = static_cast<int32_t>(a.keep);
 }
 
 // ---- by several workgroups ----
@@ -341,13 +370,13 @@ constexpr uint32_t kEvictTile = kEvictItems * kEvictBlock;
 // The counts of pass - 1 joined over the splits: the digit, and how many scores of
 // earlier splits stay for it (`equals`: of those that share the digits found, where
 // not all of them do).
-__device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh, int64_t bh, int pass, Threshold &t,
-                                            uint32_t &before, uint32_t &equals) {
+__device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh, int64_t bh, int64_t rows, int pass,
+                                            Threshold &t, uint32_t &before, uint32_t &equals) {
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
-    const uint32_t *hist = a.hist + ((static_cast<int64_t>((pass - 1) & 1) * gridDim.x * gridDim.y + bh) * a.splits) * kEvictBins;
+    const uint32_t *hist = a.hist + ((((pass - 1) & 1) * rows + bh) * a.splits) * kEvictBins;
     uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t s = 0; s < a.splits; ++s) {
         const uint2 c = *reinterpret_cast<const uint2 *>(hist + static_cast<int64_t>(s) * kEvictBins + top - 1u);
         c0 += c.y;
@@ -363,7 +392,9 @@ __device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh,
     if (top == d) sh.before = b0;
     if (top - 1u == d) sh.before = b1;
     __syncthreads();
-    for (int v = 0; v < kEvictWaves; ++v) before += sh.wave_equal[v];
+    uint32_t all;
+    waves_before(sh.wave_equal, 0, all);
+    before += all;
     equals = t.all ? 0u : sh.before;
     if (t.all) before += sh.before;
     __syncthreads();
@@ -375,110 +406,56 @@ __global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, i
     __shared__ EvictShared sh;
     const uint32_t split = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
+    const int64_t rows = static_cast<int64_t>(gridDim.x) * gridDim.y;
     const Head head(a, blockIdx.x, blockIdx.y);
     if (head.len <= a.keep) {
-        if (LAST) head.keep_all(a, bh, split * kEvictBlock + threadIdx.x, a.splits * kEvictBlock);
+        if (LAST) head.keep_all(a, a.counts + bh, split * kEvictBlock + threadIdx.x, a.splits * kEvictBlock);
         return;
     }
-    const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t from = split * a.span;
-    const uint32_t to = head.len - (from < head.len ? from : head.len) < a.span ? head.len : from + a.span;
-    const int64_t rows = static_cast<int64_t>(gridDim.x) * gridDim.y;
-    Threshold t = head.start();
+    const uint32_t to = head.len - least(from, head.len) < a.span ? head.len : from + a.span;
+    Threshold t{0u, 0u, a.keep, 0u};
     uint32_t before = 0, equals = 0;
     if (pass > 0) {
         if (pass > 1) {
             t = a.found[bh * kEvictPasses + pass - 2];
             before = a.before[bh * a.splits + split];
         }
-        if (!t.all) join_splits(a, sh, bh, pass, t, before, equals);
+        if (!t.all) join_splits(a, sh, bh, rows, pass, t, before, equals);
         if (!LAST && threadIdx.x == 0) {
             if (split == 0) a.found[bh * kEvictPasses + pass - 1] = t;
             a.before[bh * a.splits + split] = before;
         }
     }
-    const auto load = [&](uint32_t base, uint32_t(&key)[kEvictItems]) {
-        float x[kEvictItems];
-#pragma unroll
-        for (int j = 0; j < kEvictItems; ++j) {
-            const uint32_t i = base + j * kWave;
-            x[j] = i < to && head.open(i) ? head.scores[i] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kEvictItems; ++j) key[j] = score_key(x[j]);
-    };
     if constexpr (!LAST) {
         if (t.all) return;
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
         __syncthreads();
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
-            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane;
             uint32_t key[kEvictItems];
-            load(base, key);
-#pragma unroll
-            for (int j = 0; j < kEvictItems; ++j) {
-                const uint32_t i = base + j * kWave;
-                count_digit(sh.hist, (key[j] >> digit_shift(pass)) & (digit_bins(pass) - 1u),
-                            i < to && head.open(i) && (key[j] & t.fixed) == t.low);
-            }
+            head.load(tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id(), to, key);
+            count_digits(sh.hist, key, t, pass);
         }
         __syncthreads();
-        uint32_t *hist =
-            a.hist + ((static_cast<int64_t>(pass & 1) * rows + bh) * a.splits + split) * kEvictBins;
+        uint32_t *hist = a.hist + (((pass & 1) * rows + bh) * a.splits + split) * kEvictBins;
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) hist[i] = sh.hist[i];
     } else {
-        // slots before this split: positions that stay in any case, better scores, and equal ones
-        uint32_t at = before + (from < head.begin ? from : head.begin) + (from > head.end ? from - head.end : 0u);
-        at += equals < t.need ? equals : t.need;
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
-            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane;
+            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id();
             uint32_t key[kEvictItems];
-            load(base, key);
-            uint32_t sure = 0, equal = 0;
-#pragma unroll
-            for (int j = 0; j < kEvictItems; ++j) {
-                const uint32_t i = base + j * kWave;
-                const bool in = i < to, open = in && head.open(i);
-                sure += static_cast<uint32_t>(
-                    __builtin_popcountll(ballot((in && head.always(i)) || (open && better(t, key[j])))));
-                equal += static_cast<uint32_t>(__builtin_popcountll(ballot(open && !t.all && key[j] == t.low)));
-            }
-            if (lane == 0) {
-                sh.wave[w] = sure;
-                sh.wave_equal[w] = equal;
+            head.load(base, to, key);
+            const Staying<kEvictItems> stay(key, t);
+            if (lane_id() == 0) {
+                sh.wave[w] = stay.sures;
+                sh.wave_equal[w] = stay.equals;
             }
             __syncthreads();
-            const uint32_t tile_equals = equals;
-            uint32_t mine = at - (tile_equals < t.need ? tile_equals : t.need), all_sure = 0, all_equal = 0;
-            uint32_t run = tile_equals;
-            for (int v = 0; v < kEvictWaves; ++v) {
-                const uint32_t s = sh.wave[v], e = sh.wave_equal[v];
-                if (v < w) {
-                    mine += s;
-                    run += e;
-                }
-                all_sure += s;
-                all_equal += e;
-            }
-            mine += run < t.need ? run : t.need;
-#pragma unroll
-            for (int j = 0; j < kEvictItems; ++j) {
-                const uint32_t i = base + j * kWave;
-                const bool in = i < to, open = in && head.open(i);
-                const bool same = open && !t.all && key[j] == t.low;
-                const uint64_t sames = ballot(same);
-                const bool yes = (in && head.always(i)) || (open && better(t, key[j])) ||
-                                 (same && run + mbcnt64(sames) < t.need);
-                run += static_cast<uint32_t>(__builtin_popcountll(sames));
-                const uint64_t yeses = ballot(yes);
-                const uint32_t slot = mine + mbcnt64(yeses);
-                if (yes && slot < a.keep) head.kept[slot] = static_cast<int32_t>(i);
-                mine += static_cast<uint32_t>(__builtin_popcountll(yeses));
-            }
-            at += all_sure - (tile_equals < t.need ? tile_equals : t.need);
-            equals += all_equal;
-            at += equals < t.need ? equals : t.need;
+            uint32_t all_sures, all_equals;
+            const uint32_t run = equals + waves_before(sh.wave_equal, w, all_equals);
+            stay.emit(a, head, base, before + waves_before(sh.wave, w, all_sures) + least(run, t.need), run, t.need);
+            before += all_sures;
+            equals += all_equals;
             __syncthreads();
         }
         if (split == 0 && threadIdx.x == 0) a.counts[bh] = static_cast<int32_t>(a.keep);
