@@ -18,7 +18,7 @@ namespace {
 
 // ---------------------------------------------------- weights added up ---
 // A lane holds 16 bytes of columns of the weights and adds up its rows (the
-// queries of the heads that share a cache head), eight in flight; the
+// queries of the heads that share a cache head), sixteen in flight; the
 // wavefronts of a workgroup take every WAVES-th row and are joined in LDS.
 struct AccumulateArgs {
     float *scores;
@@ -36,7 +36,7 @@ struct AccumulateArgs {
 template <class T, int WAVES, bool EVEN>
 __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs a) {
     constexpr int kN = 16 / static_cast<int>(sizeof(T));
-    constexpr int kFlight = 8;
+    constexpr int kFlight = 16;
     typedef T V __attribute__((ext_vector_type(kN)));
     typedef uint32_t Raw __attribute__((ext_vector_type(4)));
     typedef uint32_t RawAny __attribute__((ext_vector_type(4), aligned(2), may_alias));
@@ -94,6 +94,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
             r += C * WAVES;
         };
         while (r + (kFlight - 1) * WAVES < rows) some(std::integral_constant<int, kFlight>{});
+        if (r + 7 * WAVES < rows) some(std::integral_constant<int, 8>{});
         if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
         while (r < rows) some(std::integral_constant<int, 1>{});
     } else if (first < a.length) {
@@ -415,6 +416,10 @@ __global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, i
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t from = split * a.span;
     const uint32_t to = head.len - least(from, head.len) < a.span ? head.len : from + a.span;
+    // the first tile's scores are on their way while the splits' counts are joined
+    const uint32_t mine = static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id();
+    uint32_t key[kEvictItems];
+    head.load(from + mine, to, key);
     Threshold t{0u, 0u, a.keep, 0u};
     uint32_t before = 0, equals = 0;
     if (pass > 0) {
@@ -433,8 +438,7 @@ __global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, i
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
         __syncthreads();
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
-            uint32_t key[kEvictItems];
-            head.load(tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id(), to, key);
+            if (tile != from) head.load(tile + mine, to, key);
             count_digits(sh.hist, key, t, pass);
         }
         __syncthreads();
@@ -442,9 +446,7 @@ __global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, i
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) hist[i] = sh.hist[i];
     } else {
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
-            const uint32_t base = tile + static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id();
-            uint32_t key[kEvictItems];
-            head.load(base, to, key);
+            if (tile != from) head.load(tile + mine, to, key);
             const Staying<kEvictItems> stay(key, t);
             if (lane_id() == 0) {
                 sh.wave[w] = stay.sures;
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, i
             __syncthreads();
             uint32_t all_sures, all_equals;
             const uint32_t run = equals + waves_before(sh.wave_equal, w, all_equals);
-            stay.emit(a, head, base, before + waves_before(sh.wave, w, all_sures) + least(run, t.need), run, t.need);
+            stay.emit(a, head, tile + mine, before + waves_before(sh.wave, w, all_sures) + least(run, t.need), run, t.need);
             before += all_sures;
             equals += all_equals;
             __syncthreads();
@@ -556,28 +558,46 @@ __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) 
     const int rows = kPlaceBlock >> a.lg;
     const int lane_col = static_cast<int>(threadIdx.x) & ((1 << a.lg) - 1);
     const int c0 = static_cast<int>(blockIdx.x) * a.cols, c1 = c0 + a.cols < a.chunks ? c0 + a.cols : a.chunks;
-    for (int64_t set = 0; set < a.keep; set += rows * kMoveFlight) {
-        int64_t pos[kMoveFlight];
-        const int64_t first = set + (threadIdx.x >> a.lg);
+    const int64_t step = static_cast<int64_t>(rows) * kMoveFlight;
+    // a slot's position, -1 for none: one that stays where it is needs no move, one
+    // that lies before its slot is none of evict_rows
+    int32_t pos[kMoveFlight], next[kMoveFlight];
+    const auto positions = [&](int64_t set, int32_t(&p)[kMoveFlight]) {
 #pragma unroll
         for (int j = 0; j < kMoveFlight; ++j) {
-            const int64_t s = first + j * rows;
-            pos[j] = s < a.keep ? kept[s] : -1;
-            // a row that stays where it is needs no move; one that lies before its slot is none of evict_rows
-            if (pos[j] >= a.capacity || pos[j] <= s) pos[j] = -1;
+            const int64_t s = set + (threadIdx.x >> a.lg) + j * rows;
+            const int32_t k = kept[s < a.keep ? s : a.keep - 1];
+            p[j] = s < a.keep && k < a.capacity && k > s ? k : -1;
         }
+    };
+    typename P::V v[kMoveFlight];
+    const auto load = [&](int base, const int32_t(&p)[kMoveFlight]) {
+        const int c = base + lane_col;
+        const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
+#pragma unroll
+        for (int j = 0; j < kMoveFlight; ++j)
+            if (p[j] >= 0 && c < c1) v[j] = P::load_stream(rows_at + static_cast<int64_t>(p[j]) * a.to_row + at);
+    };
+    positions(0, pos);
+    load(c0, pos);
+    for (int64_t set = 0; set < a.keep; set += step) {
+        if (set + step < a.keep) positions(set + step, next);
         for (int base = c0; base < c1; base += 1 << a.lg) {
+            __syncthreads();  // all of this set's pieces have been read
             const int c = base + lane_col;
             const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
-            typename P::V v[kMoveFlight];
+            const int64_t first = set + (threadIdx.x >> a.lg);
 #pragma unroll
             for (int j = 0; j < kMoveFlight; ++j)
-                if (pos[j] >= 0 && c < c1) v[j] = P::load(rows_at + pos[j] * a.to_row + at);
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kMoveFlight; ++j)
-                if (pos[j] >= 0 && c < c1) P::store(rows_at + (first + j * rows) * a.to_row + at, v[j]);
+                if (pos[j] >= 0 && c < c1) P::store_stream(rows_at + (first + j * rows) * a.to_row + at, v[j]);
+            // the next pieces are on their way while these are stored
+            if (base + (1 << a.lg) < c1)
+                load(base + (1 << a.lg), pos);
+            else if (set + step < a.keep)
+                load(c0, next);
         }
+#pragma unroll
+        for (int j = 0; j < kMoveFlight; ++j) pos[j] = next[j];
     }
 }
 
@@ -793,7 +813,7 @@ int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t head
         // few heads: their columns over several workgroups, where no two of
         // these share bytes of a row
         int parts = 1;
-        while (a.row_bytes % bytes == 0 && batch * heads * parts < 256 && a.chunks / (parts * 2) >= 4 &&
+        while (a.row_bytes % bytes == 0 && batch * heads * parts < 512 && a.chunks / (parts * 2) >= 4 &&
                a.chunks % (parts * 2) == 0)
             parts *= 2;
         a.cols = a.chunks / parts;

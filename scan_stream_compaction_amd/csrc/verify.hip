@@ -103,33 +103,45 @@ struct Weights {
         }
     }
     __device__ static __forceinline__ double weight(double w) { return w > 0.0 && w < __builtin_inf() ? w : 0.0; }
+
+    // kN values of each row, as they lie in memory
+    struct Pair {
+        Raw x, y;
+    };
+    // [i, i + kN), which the row holds all of
+    __device__ __forceinline__ Pair fetch(int i) const {
+        Pair r;
+        r.x = *reinterpret_cast<const RawAny *>(p + i);
+        r.y = q != nullptr ? static_cast<Raw>(*reinterpret_cast<const RawAny *>(q + i)) : Raw{0, 0, 0, 0};
+        return r;
+    }
+    __device__ __forceinline__ void unpack(const Pair &r, int i, double (&w)[kN]) const {
+        const V x = __builtin_bit_cast(V, r.x), y = __builtin_bit_cast(V, r.y);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const double a = static_cast<float>(x[e]), b = static_cast<float>(y[e]);
+            w[e] = weight(a - b);
+        }
+        if (without >= 0) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) w[e] = i + e == without ? 0.0 : w[e];
+        }
+    }
     // weights [i, i + kN); past the end 0
     __device__ __forceinline__ void load(int i, double (&w)[kN]) const {
         if (i + kN <= n) {
-            const V x = __builtin_bit_cast(V, static_cast<Raw>(*reinterpret_cast<const RawAny *>(p + i)));
-            if (q != nullptr) {
-                const V y = __builtin_bit_cast(V, static_cast<Raw>(*reinterpret_cast<const RawAny *>(q + i)));
-#pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    w[e] = weight(static_cast<double>(static_cast<float>(x[e])) -
-                                  static_cast<double>(static_cast<float>(y[e])));
-            } else {
-#pragma unroll
-                for (int e = 0; e < kN; ++e) w[e] = weight(static_cast<double>(static_cast<float>(x[e])));
-            }
+            unpack(fetch(i), i, w);
         } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 double v = 0.0;
-                if (i + e < n) {
+                if (i + e < n && i + e != without) {
                     v = static_cast<float>(p[i + e]);
                     if (q != nullptr) v -= static_cast<double>(static_cast<float>(q[i + e]));
                 }
                 w[e] = weight(v);
             }
         }
-#pragma unroll
-        for (int e = 0; e < kN; ++e) w[e] = i + e == without ? 0.0 : w[e];
     }
 };
 
@@ -166,17 +178,45 @@ __device__ __forceinline__ double segment_sum(const Weights<T> &w, int seg) {
     return wave_scan_f64(s);
 }
 
+// A segment that the row holds all of is on its way while the one before it is
+// added up.
 template <class T, class I>
 __global__ __launch_bounds__(kSumBlock) void verify_sum_kernel(VerifyArgs a) {
+    using W = Weights<T>;
+    constexpr int kN = W::kN, kParts = kEach / kN;
     const int64_t b = blockIdx.y;
     const VerifyState s = drafts_that_stand<T, I>(a, b);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.state[b] = s;
-    const Weights<T> w(a, b, s, static_cast<const I *>(a.ids));
+    const W w(a, b, s, static_cast<const I *>(a.ids));
     const int step = static_cast<int>(gridDim.x) * kSumWaves;
-    for (int seg = static_cast<int>(blockIdx.x) * kSumWaves + static_cast<int>(uniform(threadIdx.x / kWave));
-         seg < a.segs; seg += step) {
+    const int lane = lane_id();
+    const int whole = a.vocab / kSeg;
+    int seg = static_cast<int>(blockIdx.x) * kSumWaves + static_cast<int>(uniform(threadIdx.x / kWave));
+    typename W::Pair raw[kParts];
+    const auto fetch = [&](int at) {
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) raw[j] = w.fetch(at * kSeg + (j * kWave + lane) * kN);
+    };
+    if (seg < whole) fetch(seg);
+    for (; seg < whole; seg += step) {
+        typename W::Pair now[kParts];
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) now[j] = raw[j];
+        if (seg + step < whole) fetch(seg + step);
+        double sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+            double v[kN];
+            w.unpack(now[j], seg * kSeg + (j * kWave + lane) * kN, v);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) sum += v[e];
+        }
+        sum = wave_scan_f64(sum);
+        if (lane == kWave - 1) a.sums[b * a.segs + seg] = sum;
+    }
+    if (seg < a.segs) {  // the last, in part
         const double sum = segment_sum(w, seg);
-        if (lane_id() == kWave - 1) a.sums[b * a.segs + seg] = sum;
+        if (lane == kWave - 1) a.sums[b * a.segs + seg] = sum;
     }
 }
 
@@ -375,7 +415,10 @@ int verify_impl(const void *probs, int dtype, int64_t rows, int64_t drafts, int6
     a.state = static_cast<VerifyState *>(scratch);
     a.sums = reinterpret_cast<double *>(static_cast<char *>(scratch) + plan.sums);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int blocks = (plan.segs + kSumWaves - 1) / kSumWaves;
+    // a segment to a wavefront, or several where there are more than the chip holds
+    int64_t each = rows * plan.segs / 6144;
+    each = each < 1 ? 1 : (each > 8 ? 8 : each);
+    const int64_t blocks = (plan.segs + kSumWaves * each - 1) / (kSumWaves * each);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         hipLaunchKernelGGL((verify_sum_kernel<T, I>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(rows)),
