@@ -940,6 +940,30 @@ def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor
 
 
 # ---- the router before the grouping ---------------------------------------
+# The calls below check a tensor by what it should be first, and by what is wrong
+# with it only where that fails: 0.3 us of host time for each against 0.7.
+
+
+def _given(t, name: str, like: torch.Tensor, device: int, dtype: torch.dtype, numel: int) -> torch.Tensor:
+    """_need for one dtype, `device` being like's."""
+    if (type(t) is _Tensor and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and t.numel() >= numel):
+        return t
+    return _need(t, name, like, (dtype,), numel)
+
+
+def _exactly(t, name: str, like: torch.Tensor, device: int, dtype: torch.dtype, numel: int, what: str):
+    """_given for a tensor of one value for each of something; None stays None."""
+    if t is not None and _given(t, name, like, device, dtype, numel).numel() != numel:
+        raise ValueError(f"{name} holds one value a {what}")
+    return t
+
+
+def _result(t, name: str, like: torch.Tensor, device: int, dtype: torch.dtype, *shape) -> torch.Tensor:
+    """A new tensor for a result, or the given one in the result's shape."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _shaped(_given(t, name, like, device, dtype, math.prod(shape)), *shape)
 
 
 def _view(t, name: str, dims: int, dtypes, like: torch.Tensor | None = None) -> torch.Tensor:
@@ -955,18 +979,25 @@ def _view(t, name: str, dims: int, dtypes, like: torch.Tensor | None = None) -> 
         raise TypeError(f"{name} must be of dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} has {dims} dimensions, not {t.dim()}")
-    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1:
+    if t.stride(dims - 1) != 1 and t.size(dims - 1) > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return t
 
 
-def _live(live, like: torch.Tensor, tokens: int) -> torch.Tensor | None:
-    if live is None:
-        return None
-    _need(live, "live", like, (torch.bool, torch.uint8), tokens)
-    if live.numel() != tokens:
-        raise ValueError("live holds one value a token")
-    return live
+def _logits(logits: torch.Tensor) -> tuple[int, int, int]:
+    """(tokens, experts, stride) of the router's logits."""
+    _view(logits, "logits", 2, DTYPE)
+    tokens, experts = logits.shape
+    stride = logits.stride(0) if tokens > 1 else max(experts, 1)
+    if stride < experts:
+        raise ValueError("rows of logits do not overlap")
+    return tokens, experts, stride
+
+
+def _live(live, like: torch.Tensor, device: int, tokens: int) -> torch.Tensor | None:
+    if live is not None and live.dtype is torch.uint8:
+        return _exactly(live, "live", like, device, torch.uint8, tokens, "token")
+    return _exactly(live, "live", like, device, torch.bool, tokens, "token")
 
 
 def route_scratch_bytes(tokens: int, experts: int) -> int:
@@ -986,25 +1017,21 @@ def route_rows(logits: torch.Tensor, per: int, *, normalize: bool = True, live: 
     counts (experts + 1; int32) holds each expert's assignments and, last, the
     number n of tokens with an expert; share (experts; float32) the mean softmax
     over these; loss (1; float32) experts * sum of counts / (per * n) * share, 1
-    where tokens fall evenly. The rows may lie apart. No result carries autograd
-    history: route_rows_grad is the gradient."""
-    _view(logits, "logits", 2, DTYPE)
-    tokens, experts = logits.shape
-    stride = logits.stride(0) if tokens > 1 else max(experts, 1)
-    if stride < experts:
-        raise ValueError("rows of logits do not overlap")
+    where tokens fall evenly. The rows may lie apart; there are up to 1024 experts,
+    and up to 64 of them a token. No result carries autograd history:
+    route_rows_grad is the gradient."""
+    tokens, experts, stride = _logits(logits)
+    device = logits.get_device()
     if not 1 <= per <= experts:
         raise ValueError(f"per must be in [1, {experts}], not {per}")
-    live = _live(live, logits, tokens)
-    ids = (logits.new_empty((tokens, per), dtype=torch.int32) if ids is None
-           else _shaped(_need(ids, "ids", logits, (torch.int32,), tokens * per), tokens, per))
-    weights = (logits.new_empty((tokens, per), dtype=torch.float32) if weights is None
-               else _shaped(_need(weights, "weights", logits, (torch.float32,), tokens * per), tokens, per))
+    if live is not None:
+        _live(live, logits, device, tokens)
+    ids = _result(ids, "ids", logits, device, torch.int32, tokens, per)
+    weights = _result(weights, "weights", logits, device, torch.float32, tokens, per)
     if balance:
-        counts, share, loss = (
-            logits.new_empty(n, dtype=dt) if t is None else _shaped(_need(t, name, logits, (dt,), n), n)
-            for t, name, dt, n in ((counts, "counts", torch.int32, experts + 1), (share, "share", torch.float32, experts),
-                                   (loss, "loss", torch.float32, 1)))
+        counts = _result(counts, "counts", logits, device, torch.int32, experts + 1)
+        share = _result(share, "share", logits, device, torch.float32, experts)
+        loss = _result(loss, "loss", logits, device, torch.float32, 1)
         scratch = _work_bytes(scratch, logits, route_scratch_bytes(tokens, experts))
     elif counts is not None or share is not None or loss is not None:
         raise ValueError("counts, share and loss come with balance=True")
@@ -1020,37 +1047,35 @@ def route_rows_grad(logits: torch.Tensor, ids: torch.Tensor | None, dweights: to
                     dloss: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of route_rows with respect to the logits, (tokens, experts) of
     their type: of the weights by dweights (tokens, per; float32; None for 0) with
-    the ids that route_rows gave, and of the loss by dloss (1; float32; None for 0)
-    with its counts, which are constants, and may be those of several calls added
-    up. normalize and live as in route_rows."""
-    _view(logits, "logits", 2, DTYPE)
-    tokens, experts = logits.shape
-    stride = logits.stride(0) if tokens > 1 else max(experts, 1)
-    if stride < experts:
-        raise ValueError("rows of logits do not overlap")
+    the ids that route_rows gave (needed without dweights, too, where dloss is
+    given: the loss counts tokens * per assignments), and of the loss by dloss (1;
+    float32; None for 0) with its counts, which are constants, and may be those of
+    several calls added up. normalize and live as in route_rows."""
+    tokens, experts, stride = _logits(logits)
+    device = logits.get_device()
     per = 1
     if ids is not None:
-        _need(ids, "ids", logits, (torch.int32,), 0)
-        if ids.dim() != 2 or ids.shape[0] != tokens:
+        _given(ids, "ids", logits, device, torch.int32, 0)
+        if ids.dim() != 2 or ids.size(0) != tokens:
             raise ValueError("ids is (tokens, per)")
-        per = ids.shape[1]
-    elif dweights is not None:
-        raise ValueError("dweights comes with ids")
+        per = ids.size(1)
+    elif dweights is not None or dloss is not None:
+        raise ValueError("dweights and dloss come with ids")
     if dweights is not None:
-        _need(dweights, "dweights", logits, (torch.float32,), 0)
-        if dweights.shape != ids.shape:
+        _given(dweights, "dweights", logits, device, torch.float32, 0)
+        if dweights.dim() != 2 or dweights.size(0) != tokens or dweights.size(1) != per:
             raise ValueError("one gradient per weight")
     if (counts is None) != (dloss is None):
         raise ValueError("dloss comes with counts")
     if counts is not None:
-        _need(counts, "counts", logits, (torch.int32,), experts + 1)
-        if counts.numel() != experts + 1:
+        if _given(counts, "counts", logits, device, torch.int32, experts + 1).numel() != experts + 1:
             raise ValueError("counts holds experts + 1 values")
-        _need(dloss, "dloss", logits, (torch.float32,), 1)
-    out = (logits.new_empty((tokens, experts)) if out is None
-           else _shaped(_need(out, "out", logits, (logits.dtype,), tokens * experts), tokens, experts))
-    _row_call("ssc_route_rows_grad", logits, logits, DTYPE[logits.dtype], tokens, experts, stride,
-              _live(live, logits, tokens), ids, per, int(normalize), dweights, counts, dloss, out)
+        _given(dloss, "dloss", logits, device, torch.float32, 1)
+    if live is not None:
+        _live(live, logits, device, tokens)
+    out = _result(out, "out", logits, device, logits.dtype, tokens, experts)
+    _row_call("ssc_route_rows_grad", logits, logits, DTYPE[logits.dtype], tokens, experts, stride, live, ids, per,
+              int(normalize), dweights, counts, dloss, out)
     return out
 
 
@@ -1075,47 +1100,38 @@ def verify_rows(probs: torch.Tensor, drafted: torch.Tensor, u: torch.Tensor, dra
     include/ssc.h states the rules."""
     _view(probs, "probs", 3, DTYPE)
     rows, places, vocab = probs.shape
+    device = probs.get_device()
     drafts = places - 1
     if drafts < 0:
         raise ValueError("probs holds one row more than there are drafts")
-    name = "ssc_verify_rows_" + _ids(drafted, "drafted") if isinstance(drafted, torch.Tensor) else ""
-    _need(drafted, "drafted", probs, None, 0)
-    if drafted.shape != (rows, drafts):
+    if not isinstance(drafted, torch.Tensor):
+        raise TypeError("drafted must be a torch tensor")
+    name = "ssc_verify_rows_" + _ids(drafted, "drafted")
+    _given(drafted, "drafted", probs, device, drafted.dtype, 0)
+    if drafted.dim() != 2 or drafted.size(0) != rows or drafted.size(1) != drafts:
         raise ValueError(f"drafted is {(rows, drafts)}, not {tuple(drafted.shape)}")
-    _need(u, "u", probs, (torch.float32,), 0)
-    if u.shape != (rows, places):
+    _given(u, "u", probs, device, torch.float32, 0)
+    if u.dim() != 2 or u.size(0) != rows or u.size(1) != places:
         raise ValueError(f"u is {(rows, places)}, not {tuple(u.shape)}")
-    strides = 0, 0
+    by_row = by_place = 0
     if draft_probs is not None:
         _view(draft_probs, "draft_probs", 3, (probs.dtype,), probs)
-        if draft_probs.shape != (rows, drafts, vocab):
+        if draft_probs.size(0) != rows or draft_probs.size(1) != drafts or draft_probs.size(2) != vocab:
             raise ValueError(f"draft_probs is {(rows, drafts, vocab)}, not {tuple(draft_probs.shape)}")
-        strides = draft_probs.stride(0), draft_probs.stride(1)
+        by_row, by_place = draft_probs.stride(0), draft_probs.stride(1)
         if drafts == 0:
             draft_probs = None
     if lengths is not None:
-        _need(lengths, "lengths", probs, (torch.int32,), rows)
-        if lengths.numel() != rows:
-            raise ValueError("lengths holds one value a row")
-    tokens = (probs.new_empty((rows, places), dtype=torch.int32) if tokens is None
-              else _shaped(_need(tokens, "tokens", probs, (torch.int32,), rows * places), rows, places))
-    accepted = (probs.new_empty(rows, dtype=torch.int32) if accepted is None
-                else _shaped(_need(accepted, "accepted", probs, (torch.int32,), rows), rows))
+        _exactly(lengths, "lengths", probs, device, torch.int32, rows, "row")
+    tokens = _result(tokens, "tokens", probs, device, torch.int32, rows, places)
+    accepted = _result(accepted, "accepted", probs, device, torch.int32, rows)
     scratch = _work_bytes(scratch, probs, verify_scratch_bytes(rows, vocab))
     _row_call(name, probs, probs, DTYPE[probs.dtype], rows, drafts, vocab, probs.stride(0), probs.stride(1), drafted,
-              draft_probs, *strides, u, lengths, tokens, accepted, scratch, _numel(scratch))
+              draft_probs, by_row, by_place, u, lengths, tokens, accepted, scratch, _numel(scratch))
     return tokens, accepted
 
 
 # ---- a cache cut to the rows that were attended to most --------------------
-
-
-def _lengths(lengths, like: torch.Tensor, batch: int) -> torch.Tensor | None:
-    if lengths is not None:
-        _need(lengths, "lengths", like, (torch.int32,), batch)
-        if lengths.numel() != batch:
-            raise ValueError("lengths holds one value a sequence")
-    return lengths
 
 
 def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: torch.Tensor | None = None,
@@ -1130,14 +1146,16 @@ def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: 
     _view(scores, "scores", 3, (torch.float32,))
     _view(weights, "weights", 4, DTYPE, scores)
     batch, heads, capacity = scores.shape
-    count, length = weights.shape[1], weights.shape[3]
-    if weights.shape[0] != batch or heads < 1 or count < 1 or count % heads or length > capacity:
+    sequences, count, queries, length = weights.shape
+    if sequences != batch or heads < 1 or count < 1 or count % heads or length > capacity:
         raise ValueError("weights is (batch, heads * group, queries, up to capacity)")
     if fresh < 0:
         raise ValueError("fresh is not negative")
+    if lengths is not None:
+        _exactly(lengths, "lengths", scores, scores.get_device(), torch.int32, batch, "sequence")
     _row_call("ssc_accumulate_weights", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
-              weights, DTYPE[weights.dtype], count // heads, weights.shape[2], length, weights.stride(0),
-              weights.stride(1), weights.stride(2), _lengths(lengths, scores, batch), fresh, float(decay))
+              weights, DTYPE[weights.dtype], count // heads, queries, length, weights.stride(0), weights.stride(1),
+              weights.stride(2), lengths, min(fresh, capacity), float(decay))
     return scores
 
 
@@ -1157,17 +1175,18 @@ def evict_rows(scores: torch.Tensor, keep: int, *, first: int = 0, recent: int =
     dimension. move_rows takes a cache's rows, and the scores, there."""
     _view(scores, "scores", 3, (torch.float32,))
     batch, heads, capacity = scores.shape
+    device = scores.get_device()
     if not 1 <= keep <= capacity:
         raise ValueError(f"keep must be in [1, {capacity}], not {keep}")
     if first < 0 or recent < 0 or first + recent > keep:
         raise ValueError("first and recent are not negative, and keep holds both")
-    kept = (scores.new_empty((batch, heads, keep), dtype=torch.int32) if kept is None
-            else _shaped(_need(kept, "kept", scores, (torch.int32,), batch * heads * keep), batch, heads, keep))
-    counts = (scores.new_empty((batch, heads), dtype=torch.int32) if counts is None
-              else _shaped(_need(counts, "counts", scores, (torch.int32,), batch * heads), batch, heads))
+    if lengths is not None:
+        _exactly(lengths, "lengths", scores, device, torch.int32, batch, "sequence")
+    kept = _result(kept, "kept", scores, device, torch.int32, batch, heads, keep)
+    counts = _result(counts, "counts", scores, device, torch.int32, batch, heads)
     scratch = _work_bytes(scratch, scores, evict_scratch_bytes(batch, heads, capacity))
     _row_call("ssc_evict_rows", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
-              _lengths(lengths, scores, batch), keep, first, recent, kept, counts, scratch, _numel(scratch))
+              lengths, keep, first, recent, kept, counts, scratch, _numel(scratch))
     return kept, counts
 
 
@@ -1180,16 +1199,16 @@ def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | No
     lie apart; scores move as scores.unsqueeze(3)."""
     _view(cache, "cache", 4, None)
     batch, heads, capacity, width = cache.shape
-    _need(kept, "kept", cache, (torch.int32,), 0)
-    if kept.dim() != 3 or kept.shape[0] != batch or kept.shape[1] != heads:
+    _given(kept, "kept", cache, cache.get_device(), torch.int32, 0)
+    if kept.dim() != 3 or kept.size(0) != batch or kept.size(1) != heads:
         raise ValueError("kept is (batch, heads, keep)")
-    keep = kept.shape[2]
+    keep = kept.size(2)
     to = cache
     if out is not None:
-        to = out = _view(out, "out", 4, (cache.dtype,), cache)
-        if out.shape[0] != batch or out.shape[1] != heads or out.shape[3] != width or out.shape[2] < keep:
+        to = _view(out, "out", 4, (cache.dtype,), cache)
+        if out.size(0) != batch or out.size(1) != heads or out.size(3) != width or out.size(2) < keep:
             raise ValueError("out is (batch, heads, at least keep, width)")
-        if out.shape[2] != keep:
+        if out.size(2) != keep:
             out = out[:, :, :keep]
     _row_call("ssc_move_rows", cache, cache, cache.element_size(), batch, heads, capacity, width, cache.stride(0),
               cache.stride(1), cache.stride(2), kept, keep, to, to.stride(0), to.stride(1), to.stride(2))
