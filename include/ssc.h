@@ -544,7 +544,8 @@ int ssc_route_rows_grad(const void *logits, int dtype, int64_t tokens, int64_t e
  * After the choice of tokens: drafts verified. */
 
 /* Scratch bytes of ssc_verify_rows: about 8 for each 1024 tokens of the
- * vocabulary and row. */
+ * vocabulary and row; 0 up to 65,536 tokens, and for 160 rows or more up to
+ * 131,072. */
 size_t ssc_verify_scratch_bytes(int64_t rows, int64_t vocab);
 
 /* Drafted tokens held against the probabilities of the model that they were

@@ -693,9 +693,12 @@ def _row_call(name: str, like: torch.Tensor, *args) -> None:
     repeated by a prepared call."""
     fn = getattr(_lib or lib(), name)
     device = like.get_device()
-    if _recording is not None or device != _current_device():
-        fn = _on_device(fn, device)
-    _call(name, fn, *args, _stream(like))
+    if _recording is None and device == _current_device():
+        rc = fn(*[a if type(a) is int else a.data_ptr() if isinstance(a, _Tensor) else a for a in args], _stream(like))
+        if rc != 0:
+            _check(name, rc)
+        return
+    _call(name, _on_device(fn, device), *args, _stream(like))
 
 
 def _work_bytes(scratch, like: torch.Tensor, nbytes: int) -> torch.Tensor | None:
@@ -995,7 +998,7 @@ def _logits(logits: torch.Tensor) -> tuple[int, int, int]:
 
 
 def _live(live, like: torch.Tensor, device: int, tokens: int) -> torch.Tensor | None:
-    if live is not None and live.dtype is torch.uint8:
+    if getattr(live, "dtype", None) is torch.uint8:
         return _exactly(live, "live", like, device, torch.uint8, tokens, "token")
     return _exactly(live, "live", like, device, torch.bool, tokens, "token")
 

@@ -8,11 +8,13 @@
 // u_last times their sum. The tokens then come as from p alone. Of the (drafts
 // + 1) rows of a sequence one is read, beside 2 * drafts single values.
 //
-// Two launches: every wavefront finds a (a few dependent loads) and sums
-// segments of 1024 weights; then a workgroup a sequence finds the segment by a
-// scan of the sums, and the token in it by reading it again. Sums are fp64, in
-// an order that the sizes fix: a border of u that fp32 sums would miss once in
-// some hundred rows (131,072 borders, 1e-8 of the sum each) is met.
+// Every wavefront finds a (a few dependent loads) and sums segments of 1024
+// weights; then a workgroup a sequence finds the segment by a scan of the sums,
+// and the token in it by reading it again: in one launch, or in two where few
+// long rows would leave the chip empty. Sums are fp64, in an order that the sizes
+// fix: a border of u that fp32 sums would miss once in some hundred rows (131,072
+// borders, 1e-8 of the sum each) is met. Bound by HBM for many rows (192 of
+// 131,072 bf16, p and q: 20 us a call, 5.0 TB/s), by latency for few.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,6 +30,16 @@ constexpr int kEach = kSeg / kWave;
 constexpr int kSumBlock = 256;
 constexpr int kSumWaves = kSumBlock / kWave;
 constexpr int kDrawBlock = 256;
+// The form in one launch, a row to a workgroup: for rows of up to 64 segments, and
+// of up to 128 where there are enough to fill the chip. us a call (repeated by
+// prepared), one launch against two, fp32:
+//   rows of        32,768                     65,536                      131,072
+//   1        12.6 16.7 ( 7.9  7.1)     12.5 16.7 (10.4  6.9)     15.5 16.7 (15.4  6.8)
+//   64       12.6 16.7 ( 9.0  7.7)     12.7 16.7 (11.6  9.4)     19.0 16.4 (19.0 15.2)
+//   192      12.5 16.8 (10.9 12.3)     17.3 18.4 (17.3 18.1)     27.2 28.9 (27.1 28.8)
+constexpr int kRowBlock = 1024;
+constexpr int kRowSegs = 128;
+constexpr int kRowMany = 160;
 constexpr int64_t kVerifyVocabMax = int64_t{1} << 22;
 constexpr int kSegsMax = static_cast<int>(kVerifyVocabMax / kSeg);
 
@@ -178,25 +190,21 @@ __device__ __forceinline__ double segment_sum(const Weights<T> &w, int seg) {
     return wave_scan_f64(s);
 }
 
-// A segment that the row holds all of is on its way while the one before it is
-// added up.
-template <class T, class I>
-__global__ __launch_bounds__(kSumBlock) void verify_sum_kernel(VerifyArgs a) {
+// Sums of the segments first, first + step, ... into sums, by a wavefront. One
+// that the row holds all of is on its way while the one before it is added up.
+template <class T>
+__device__ __forceinline__ void segment_sums(const VerifyArgs &a, const Weights<T> &w, int first, int step,
+                                             double *sums) {
     using W = Weights<T>;
     constexpr int kN = W::kN, kParts = kEach / kN;
-    const int64_t b = blockIdx.y;
-    const VerifyState s = drafts_that_stand<T, I>(a, b);
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.state[b] = s;
-    const W w(a, b, s, static_cast<const I *>(a.ids));
-    const int step = static_cast<int>(gridDim.x) * kSumWaves;
     const int lane = lane_id();
     const int whole = a.vocab / kSeg;
-    int seg = static_cast<int>(blockIdx.x) * kSumWaves + static_cast<int>(uniform(threadIdx.x / kWave));
     typename W::Pair raw[kParts];
     const auto fetch = [&](int at) {
 #pragma unroll
         for (int j = 0; j < kParts; ++j) raw[j] = w.fetch(at * kSeg + (j * kWave + lane) * kN);
     };
+    int seg = first;
     if (seg < whole) fetch(seg);
     for (; seg < whole; seg += step) {
         typename W::Pair now[kParts];
@@ -212,51 +220,58 @@ __global__ __launch_bounds__(kSumBlock) void verify_sum_kernel(VerifyArgs a) {
             for (int e = 0; e < kN; ++e) sum += v[e];
         }
         sum = wave_scan_f64(sum);
-        if (lane == kWave - 1) a.sums[b * a.segs + seg] = sum;
+        if (lane == kWave - 1) sums[seg] = sum;
     }
     if (seg < a.segs) {  // the last, in part
         const double sum = segment_sum(w, seg);
-        if (lane == kWave - 1) a.sums[b * a.segs + seg] = sum;
+        if (lane == kWave - 1) sums[seg] = sum;
     }
 }
 
-// Where the running sum of n values first exceeds goal (-1: nowhere), and the
-// sum before that place; by a workgroup. A value that adds nothing is no place.
-constexpr int kDrawWaves = kDrawBlock / kWave;
+template <class T, class I>
+__global__ __launch_bounds__(kSumBlock) void verify_sum_kernel(VerifyArgs a) {
+    const int64_t b = blockIdx.y;
+    const VerifyState s = drafts_that_stand<T, I>(a, b);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.state[b] = s;
+    const Weights<T> w(a, b, s, static_cast<const I *>(a.ids));
+    segment_sums(a, w, static_cast<int>(blockIdx.x) * kSumWaves + static_cast<int>(uniform(threadIdx.x / kWave)),
+                 static_cast<int>(gridDim.x) * kSumWaves, a.sums + b * a.segs);
+}
 
+// The token of a row from the sums of its segments, by a workgroup: where their
+// running sum first exceeds the goal, then where that of the segment's weights
+// does. What weighs nothing is no place. Writes the row's results.
+template <int BLOCK>
 struct DrawShared {
-    double sums[kSegsMax];
-    double wave[kDrawWaves];
-    int first[kDrawWaves];
+    double wave[BLOCK / kWave];
+    int first[BLOCK / kWave];
 };
 
-template <class T, class I>
-__global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
-    __shared__ DrawShared sh;
-    const int64_t b = blockIdx.x;
+template <int BLOCK, class T, class I>
+__device__ __forceinline__ void draw(const VerifyArgs &a, int64_t b, const VerifyState &s, Weights<T> &weights,
+                                     double *sums, DrawShared<BLOCK> &sh) {
+    constexpr int kWaves = BLOCK / kWave;
     const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const VerifyState s = a.state[b];
-    Weights<T> weights(a, b, s, static_cast<const I *>(a.ids));
     const double u = unit(a.u[b * (a.drafts + 1) + a.drafts]);
-    for (int i = threadIdx.x; i < a.segs; i += kDrawBlock) sh.sums[i] = a.sums[b * a.segs + i];
-    __syncthreads();
     // a thread runs over consecutive segments
-    const int each = (a.segs + kDrawBlock - 1) / kDrawBlock;
+    const int each = (a.segs + BLOCK - 1) / BLOCK;
     const int begin = static_cast<int>(threadIdx.x) * each;
     const int end = begin + each < a.segs ? begin + each : a.segs;
     double own, incl, before, total;
     const auto scan = [&]() {
         own = 0.0;
-        for (int i = begin; i < end; ++i) own += sh.sums[i];
+        for (int i = begin; i < end; ++i) own += sums[i];
         incl = wave_scan_f64(own);
         if (lane == kWave - 1) sh.wave[w] = incl;
         __syncthreads();
         before = 0.0;
         total = 0.0;
-        for (int v = 0; v < kDrawWaves; ++v) {
-            if (v < w) before += sh.wave[v];
-            total += sh.wave[v];
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const double x = sh.wave[v];
+            before += v < w ? x : 0.0;
+            total += x;
         }
     };
     scan();
@@ -264,10 +279,7 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
         weights.q = nullptr;
         weights.without = -1;
         __syncthreads();
-        for (int seg = w; seg < a.segs; seg += kDrawWaves) {
-            const double sum = segment_sum(weights, seg);
-            if (lane == kWave - 1) sh.sums[seg] = sum;
-        }
+        segment_sums(a, weights, w, kWaves, sums);
         __syncthreads();
         scan();
     }
@@ -277,7 +289,7 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
     double run = before + incl - own;
     int seg = -1, last = -1;
     for (int i = begin; i < end; ++i) {
-        const double v = sh.sums[i];
+        const double v = sums[i];
         run += v;
         if (v > 0.0) last = i;
         if (seg < 0 && v > 0.0 && run > goal) seg = i;
@@ -293,7 +305,8 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
     }
     __syncthreads();
     int at = -1, fallback = -1;
-    for (int v = 0; v < kDrawWaves; ++v) {
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) {
         const int f = sh.first[v];
         if (f >= 0 && at < 0) at = f;
         if (f < -1) fallback = -2 - f;
@@ -301,16 +314,14 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
     if (at < 0) at = fallback;
     int32_t token = -1;
     if (at >= 0) {
-        // the sum before the segment, added up as the search did
-        const int owner = at / each;
-        double base = 0.0;
-        if (static_cast<int>(threadIdx.x) == owner) {
-            base = before + incl - own;
-            for (int i = begin; i < at; ++i) base += sh.sums[i];
-            sh.wave[0] = base;  // the waves' totals have been read: a barrier lies between
+        // the sum before the segment, added up as the search did; the wavefronts'
+        // totals have been read by now
+        if (static_cast<int>(threadIdx.x) == at / each) {
+            double base = before + incl - own;
+            for (int i = begin; i < at; ++i) base += sums[i];
+            sh.wave[0] = base;
         }
         __syncthreads();
-        base = sh.wave[0];
         if (w == 0) {
             constexpr int kN = Weights<T>::kN;
             double v[kEach / kN][kN], sum = 0.0;
@@ -321,7 +332,7 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e) sum += v[j][e];
             }
-            double r = base + wave_scan_f64(sum) - sum;
+            double r = sh.wave[0] + wave_scan_f64(sum) - sum;
             int first = -1, any = -1;
 #pragma unroll
             for (int j = 0; j < kEach / kN; ++j) {
@@ -349,6 +360,31 @@ __global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
     }
 }
 
+template <class T, class I>
+__global__ __launch_bounds__(kDrawBlock) void verify_draw_kernel(VerifyArgs a) {
+    __shared__ double s_sums[kSegsMax];
+    __shared__ DrawShared<kDrawBlock> sh;
+    const int64_t b = blockIdx.x;
+    for (int i = threadIdx.x; i < a.segs; i += kDrawBlock) s_sums[i] = a.sums[b * a.segs + i];
+    const VerifyState s = a.state[b];
+    Weights<T> weights(a, b, s, static_cast<const I *>(a.ids));
+    __syncthreads();
+    draw<kDrawBlock, T, I>(a, b, s, weights, s_sums, sh);
+}
+
+// A row by one workgroup, in one launch.
+template <class T, class I>
+__global__ __launch_bounds__(kRowBlock) void verify_row_kernel(VerifyArgs a) {
+    __shared__ double s_sums[kRowSegs];
+    __shared__ DrawShared<kRowBlock> sh;
+    const int64_t b = blockIdx.x;
+    const VerifyState s = drafts_that_stand<T, I>(a, b);
+    Weights<T> weights(a, b, s, static_cast<const I *>(a.ids));
+    segment_sums(a, weights, static_cast<int>(uniform(threadIdx.x / kWave)), kRowBlock / kWave, s_sums);
+    __syncthreads();
+    draw<kRowBlock, T, I>(a, b, s, weights, s_sums, sh);
+}
+
 // ============================================================ host side ---
 struct VerifyPlan {
     int segs;
@@ -357,6 +393,7 @@ struct VerifyPlan {
 VerifyPlan verify_plan(int64_t rows, int64_t vocab) {
     VerifyPlan p{};
     p.segs = static_cast<int>((vocab + kSeg - 1) / kSeg);
+    if (p.segs <= kRowSegs / 2 || (p.segs <= kRowSegs && rows >= kRowMany)) return p;
     p.sums = (static_cast<size_t>(rows) * sizeof(VerifyState) + 15) / 16 * 16;
     p.bytes = p.sums + static_cast<size_t>(rows) * p.segs * sizeof(double);
     return p;
@@ -383,7 +420,7 @@ int verify_impl(const void *probs, int dtype, int64_t rows, int64_t drafts, int6
         !aligned(lengths, 4) || !aligned(tokens, 4) || !aligned(accepted, 4))
         return SSC_ERR_ARG;
     const VerifyPlan plan = verify_plan(rows, vocab);
-    if (rows > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < plan.bytes)) return SSC_ERR_SCRATCH;
+    if (plan.bytes > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < plan.bytes)) return SSC_ERR_SCRATCH;
     const size_t n = static_cast<size_t>(rows);
     const Span written[] = {{tokens, n * (drafts + 1) * 4}, {accepted, n * 4}, {scratch, plan.bytes}};
     const Span read[] = {{probs, static_cast<size_t>(p.extent()) * es},
@@ -415,6 +452,12 @@ int verify_impl(const void *probs, int dtype, int64_t rows, int64_t drafts, int6
     a.state = static_cast<VerifyState *>(scratch);
     a.sums = reinterpret_cast<double *>(static_cast<char *>(scratch) + plan.sums);
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (plan.bytes == 0)
+        return with_dtype(dtype, [&](auto t) {
+            using T = decltype(t);
+            hipLaunchKernelGGL((verify_row_kernel<T, I>), dim3(static_cast<unsigned>(rows)), dim3(kRowBlock), 0, s, a);
+            return launched();
+        });
     // a segment to a wavefront, or several where there are more than the chip holds
     int64_t each = rows * plan.segs / 6144;
     each = each < 1 ? 1 : (each > 8 ? 8 : each);

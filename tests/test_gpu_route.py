@@ -124,6 +124,21 @@ def test_masked_and_special_logits(dtype, experts):
     check_forward(x, 2, live=torch.zeros(14, dtype=torch.bool, device=DEV))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("experts", [7, 30, 100, 150, 300])
+def test_logits_of_the_last_bits(dtype, experts):
+    """Subnormal logits of both signs beside zeros, and neighbours of one step."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(experts)
+    small = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    x = (torch.randint(-3, 4, (40, experts), device=DEV, generator=g).double() * small).to(dtype)
+    for per in (1, 4, 7):
+        check_forward(x, per)
+    near = (1.0 + torch.randint(0, 5, (40, experts), device=DEV, generator=g).double() * torch.finfo(dtype).eps).to(dtype)
+    for sign in (1, -1):
+        check_forward(near * sign, 5)
+
+
 def gradient(logits, ids, dweights, normalize, live, counts, dloss):
     """(gradient, bound): the formula in 64 bits, and what |g| bounds its roundings by."""
     per = ids.shape[1]

@@ -76,7 +76,7 @@ def inputs(seed, rows, drafts, vocab, dtype, near=0.5, ids=torch.int32):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("vocab", [1, 2, 7, 9, 1000, 1023, 1024, 1025, 4097, 50_001, 131_072])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 9, 1000, 1023, 1024, 1025, 4097, 50_001, 65_536, 65_537, 131_072])
 @pytest.mark.parametrize("drafts", [1, 4])
 def test_sizes(drafts, vocab, dtype):
     p, x, u, q, g = inputs(vocab + drafts, 13, drafts, vocab, dtype, ids=torch.int64 if vocab % 2 else torch.int32)
@@ -103,8 +103,9 @@ def test_the_largest_vocabulary(dtype):
     check(p, x, u, q)
 
 
-def test_many_rows():
-    p, x, u, q, _ = inputs(4, 65_535, 2, 5, torch.float32)
+@pytest.mark.parametrize("rows,vocab", [(65_535, 5), (159, 70_000), (160, 70_000)])
+def test_many_rows(rows, vocab):
+    p, x, u, q, _ = inputs(4, rows, 2, vocab, torch.float32)
     check(p, x, u, q)
 
 
@@ -128,9 +129,10 @@ def test_borders_met_exactly():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_rows_that_leave_nothing_and_special_values(dtype):
+@pytest.mark.parametrize("vocab", [3000, 70_000])
+def test_rows_that_leave_nothing_and_special_values(vocab, dtype):
     inf, nan = float("inf"), float("nan")
-    p, x, u, q, _ = inputs(5, 16, 2, 3000, dtype)
+    p, x, u, q, _ = inputs(5, 16, 2, vocab, dtype)
     u[:, 0] = 0.9999999
     p[0] = 0
     p[1] = nan
@@ -143,7 +145,7 @@ def test_rows_that_leave_nothing_and_special_values(dtype):
     q[7, :, 100:] = nan
     q[8] = inf
     x[9] = -1
-    x[10] = 3000
+    x[10] = vocab
     x[11] = 2 ** 31 - 1
     x[12] = -2 ** 31
     p[13, :, :-1] = 0
@@ -174,16 +176,17 @@ def test_the_distribution_of_the_tokens():
     assert bool(((share - p.double()).abs() <= 2.0 / m).all())
 
 
-def test_strides_outputs_and_repeats():
-    p, x, u, q, g = inputs(6, 7, 3, 1003, torch.bfloat16)
-    wide = torch.zeros(7, 9, 1100, device=DEV, dtype=torch.bfloat16)
-    wide[:, 1:8:2, 13:1016] = p
-    qt = torch.zeros(3, 7, 1003, device=DEV, dtype=torch.bfloat16).copy_(q.transpose(0, 1)).transpose(0, 1)
-    view = wide[:, 1:8:2, 13:1016]
+@pytest.mark.parametrize("vocab", [1003, 66_001])
+def test_strides_outputs_and_repeats(vocab):
+    p, x, u, q, g = inputs(6, 7, 3, vocab, torch.bfloat16)
+    wide = torch.zeros(7, 9, vocab + 97, device=DEV, dtype=torch.bfloat16)
+    wide[:, 1:8:2, 13:vocab + 13] = p
+    qt = torch.zeros(3, 7, vocab, device=DEV, dtype=torch.bfloat16).copy_(q.transpose(0, 1)).transpose(0, 1)
+    view = wide[:, 1:8:2, 13:vocab + 13]
     assert not view.is_contiguous() and not qt.is_contiguous()
     want = check(p, x, u, q)
     buf = torch.full((2, 40), -9, dtype=torch.int32, device=DEV)
-    scratch = torch.full((ssc.verify_scratch_bytes(7, 1003),), 255, dtype=torch.uint8, device=DEV)
+    scratch = torch.full((ssc.verify_scratch_bytes(7, vocab),), 255, dtype=torch.uint8, device=DEV)
     for _ in range(3):
         got = ssc.verify_rows(view, x, u, qt, tokens=buf[0, 5:33], accepted=buf[1, 5:12], scratch=scratch)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
@@ -192,8 +195,9 @@ def test_strides_outputs_and_repeats():
     assert empty[0].shape == (0, 4) and empty[1].shape == (0,)
 
 
-def test_graph_replays_and_streams():
-    p, x, u, q, g = inputs(7, 20, 4, 5000, torch.float32)
+@pytest.mark.parametrize("vocab", [5000, 70_000])
+def test_graph_replays_and_streams(vocab):
+    p, x, u, q, g = inputs(7, 20, 4, vocab, torch.float32)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -211,7 +215,7 @@ def test_graph_replays_and_streams():
 
 
 def test_two_calls_at_once():
-    ins = [inputs(40 + i, 30, 3, 40_000, torch.bfloat16)[:4] for i in range(2)]
+    ins = [inputs(40 + i, 30, 3, 70_000, torch.bfloat16)[:4] for i in range(2)]
     want = [ssc.verify_rows(*a) for a in ins]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in ins]

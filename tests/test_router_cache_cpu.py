@@ -30,7 +30,9 @@ def test_scratch_sizes():
     assert ssc.route_scratch_bytes(BIG, 8) == 0
     assert ssc.verify_scratch_bytes(0, 100) == ssc.verify_scratch_bytes(4, 0) == 0
     assert ssc.verify_scratch_bytes(65_536, 10) == ssc.verify_scratch_bytes(1, 2 ** 22 + 1) == 0
-    assert ssc.verify_scratch_bytes(3, 1025) == 32 + 3 * 2 * 8
+    assert ssc.verify_scratch_bytes(3, 65_536) == ssc.verify_scratch_bytes(160, 131_072) == 0
+    assert ssc.verify_scratch_bytes(3, 65_537) == 32 + 3 * 65 * 8
+    assert ssc.verify_scratch_bytes(160, 131_073) == 160 * 8 + 160 * 129 * 8
     # two tables of 2048 counts a split, three thresholds a head, one number a split
     assert ssc.evict_scratch_bytes(1, 8, 16_384) == ssc.evict_scratch_bytes(40, 8, 32_768) == 0
     assert ssc.evict_scratch_bytes(1, 8, 131_072) == 8 * 16 * 16_384 + 8 * 48 + 8 * 16 * 4
@@ -108,15 +110,17 @@ def test_verify_refusals(name):
     assert _call(name, d, probs=A + 1) == ARG
     assert _call(name, d, drafted=B + 2) == ARG
     assert _call(name, d, u=D + 1) == ARG
-    assert _call(name, d, scratch=None) == SCRATCH
-    assert _call(name, d, sbytes=ssc.verify_scratch_bytes(5, 1000) - 1) == SCRATCH
+    long = dict(d, vocab=70_000, place=70_000, row=280_000, dplace=70_000, drow=210_000)
+    assert _call(name, long, scratch=None) == SCRATCH
+    assert _call(name, long, scratch=S + 8) == SCRATCH
+    assert _call(name, long, sbytes=ssc.verify_scratch_bytes(5, 70_000) - 1) == SCRATCH
+    assert _call(name, long, scratch=C) == ALIAS
     assert _call(name, d, tokens=A + 39_996) == ALIAS
     assert _call(name, d, tokens=C + 29_996) == ALIAS
     assert _call(name, d, accepted=F + 76) == ALIAS
     assert _call(name, d, accepted=B) == ALIAS
     assert _call(name, d, tokens=D) == ALIAS
     assert _call(name, d, accepted=E + 16) == ALIAS
-    assert _call(name, d, scratch=C) == ALIAS
 
 
 def test_accumulate_refusals():
