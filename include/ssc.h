@@ -505,7 +505,8 @@ int ssc_sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, 
  * elements, stride >= experts). 1 <= experts <= 1024, 1 <= per <= experts and
  * per <= 64. */
 
-/* Scratch bytes of ssc_route_rows with its balance (0 without). */
+/* Scratch bytes of ssc_route_rows with its balance (0 without, and for up to 64
+ * tokens, up to 512 of fewer than 129 experts). */
 size_t ssc_route_scratch_bytes(int64_t tokens, int64_t experts);
 
 /* The experts of each token: ids[t, :] (tokens x per) are the experts of its
@@ -587,6 +588,11 @@ int ssc_verify_rows_i64(const void *probs, int dtype, int64_t rows, int64_t draf
  * lengths[b] (nullable: all) is the number of positions in use, held to what there
  * is. */
 
+/* Scratch bytes of ssc_accumulate_weights: sums of the parts that many rows of a
+ * few short heads are added up in, 0 otherwise. */
+size_t ssc_accumulate_scratch_bytes(int64_t batch, int64_t heads, int64_t group, int64_t queries,
+                                    int64_t length, int dtype);
+
 /* The attention weights that each cached position got, added up: for i <
  * min(length, lengths[b])
  *   scores[b, h, i] = decay * scores[b, h, i] + sum of weights[b, g, q, i]
@@ -599,10 +605,11 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
                            int dtype, int64_t group, int64_t queries, int64_t length,
                            int64_t weight_stride_batch, int64_t weight_stride_head,
                            int64_t weight_stride_query, const int32_t *lengths, int64_t fresh,
-                           float decay, void *stream);
+                           float decay, void *scratch, size_t scratch_bytes, void *stream);
 
-/* Scratch bytes of ssc_evict_rows (0 for up to 16,384 positions): 16 KiB for each
- * 8192 positions of a few heads, or each 32,768 of many. */
+/* Scratch bytes of ssc_evict_rows (0 for up to 16,384 positions, and up to 32,768
+ * of many heads): 4 for each position, and 16 KiB for each 8192 positions of a few
+ * heads, or each 32,768 of many. */
 size_t ssc_evict_scratch_bytes(int64_t batch, int64_t heads, int64_t capacity);
 
 /* The positions that stay when every head is cut to `keep` rows: kept (batch x
@@ -617,6 +624,10 @@ int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t ca
                    int64_t keep, int64_t first, int64_t recent, int32_t *kept, int32_t *counts,
                    void *scratch, size_t scratch_bytes, void *stream);
 
+/* Scratch bytes of ssc_move_rows in place: the rows it moves, where a few long
+ * heads go by way of it; 0 otherwise, and for a move to another cache. */
+size_t ssc_move_scratch_bytes(int elem_bytes, int64_t batch, int64_t heads, int64_t keep, int64_t width);
+
 /* Rows of a cache moved together: out[b, h, s, :] = cache[b, h, kept[b, h, s], :]
  * for s < keep, bit for bit, for elements of 1, 2, 4 or 8 bytes. Slots whose position
  * lies outside [0, capacity) are not written. out may be the cache itself (the same
@@ -626,7 +637,7 @@ int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t head
                   int64_t width, int64_t cache_stride_batch, int64_t cache_stride_head,
                   int64_t cache_stride_row, const int32_t *kept, int64_t keep, void *out,
                   int64_t out_stride_batch, int64_t out_stride_head, int64_t out_stride_row,
-                  void *stream);
+                  void *scratch, size_t scratch_bytes, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *ssc_status_str(int status);

@@ -89,10 +89,12 @@ SIGNATURES = {
     "ssc_verify_scratch_bytes": (_SZ, [_I64, _I64]),
     "ssc_verify_rows_i32": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "ssc_verify_rows_i64": (_INT, [_P, _INT] + [_I64] * 5 + [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
-    "ssc_accumulate_weights": (_INT, [_P] + [_I64] * 5 + [_P, _INT] + [_I64] * 6 + [_P, _I64, _F32, _P]),
+    "ssc_accumulate_weights": (_INT, [_P] + [_I64] * 5 + [_P, _INT] + [_I64] * 6 + [_P, _I64, _F32, _P, _SZ, _P]),
+    "ssc_accumulate_scratch_bytes": (_SZ, [_I64] * 5 + [_INT]),
     "ssc_evict_scratch_bytes": (_SZ, [_I64, _I64, _I64]),
     "ssc_evict_rows": (_INT, [_P] + [_I64] * 5 + [_P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
-    "ssc_move_rows": (_INT, [_P, _INT] + [_I64] * 7 + [_P, _I64, _P] + [_I64] * 3 + [_P]),
+    "ssc_move_rows": (_INT, [_P, _INT] + [_I64] * 7 + [_P, _I64, _P] + [_I64] * 3 + [_P, _SZ, _P]),
+    "ssc_move_scratch_bytes": (_SZ, [_INT] + [_I64] * 4),
     "ssc_status_str": (ctypes.c_char_p, [_INT]),
     "ssc_last_hip_error": (_INT, []),
 }
@@ -1137,8 +1139,12 @@ def verify_rows(probs: torch.Tensor, drafted: torch.Tensor, u: torch.Tensor, dra
 # ---- a cache cut to the rows that were attended to most --------------------
 
 
+def accumulate_scratch_bytes(batch: int, heads: int, group: int, queries: int, length: int, dtype: torch.dtype) -> int:
+    return int(lib().ssc_accumulate_scratch_bytes(batch, heads, group, queries, length, DTYPE[dtype]))
+
+
 def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: torch.Tensor | None = None,
-                       fresh: int = 0, decay: float = 1.0) -> torch.Tensor:
+                       fresh: int = 0, decay: float = 1.0, scratch: torch.Tensor | None = None) -> torch.Tensor:
     """Adds to scores (batch, heads, capacity; float32, in place, and returned) the
     attention weights that each cached position got: weights (batch, heads * group,
     queries, length) of any row type, summed over the queries and over the group of
@@ -1156,9 +1162,11 @@ def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: 
         raise ValueError("fresh is not negative")
     if lengths is not None:
         _exactly(lengths, "lengths", scores, scores.get_device(), torch.int32, batch, "sequence")
+    group = count // heads
+    scratch = _work_bytes(scratch, scores, accumulate_scratch_bytes(batch, heads, group, queries, length, weights.dtype))
     _row_call("ssc_accumulate_weights", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
-              weights, DTYPE[weights.dtype], count // heads, queries, length, weights.stride(0), weights.stride(1),
-              weights.stride(2), lengths, min(fresh, capacity), float(decay))
+              weights, DTYPE[weights.dtype], group, queries, length, weights.stride(0), weights.stride(1),
+              weights.stride(2), lengths, min(fresh, capacity), float(decay), scratch, _numel(scratch))
     return scores
 
 
@@ -1193,7 +1201,12 @@ def evict_rows(scores: torch.Tensor, keep: int, *, first: int = 0, recent: int =
     return kept, counts
 
 
-def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | None = None) -> torch.Tensor:
+def move_scratch_bytes(elem_bytes: int, batch: int, heads: int, keep: int, width: int) -> int:
+    return int(lib().ssc_move_scratch_bytes(elem_bytes, batch, heads, keep, width))
+
+
+def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | None = None,
+              scratch: torch.Tensor | None = None) -> torch.Tensor:
     """out[b, h, s] = cache[b, h, kept[b, h, s]]: the rows of a cache (batch, heads,
     capacity, width; elements of 1, 2, 4 or 8 bytes) that evict_rows keeps, moved
     together. Without out in place, and the cache is returned; otherwise the part
@@ -1207,6 +1220,10 @@ def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | No
         raise ValueError("kept is (batch, heads, keep)")
     keep = kept.size(2)
     to = cache
+    if out is None or out.data_ptr() == cache.data_ptr():
+        scratch = _work_bytes(scratch, cache, move_scratch_bytes(cache.element_size(), batch, heads, keep, width))
+    else:
+        scratch = None
     if out is not None:
         to = _view(out, "out", 4, (cache.dtype,), cache)
         if out.size(0) != batch or out.size(1) != heads or out.size(3) != width or out.size(2) < keep:
@@ -1214,5 +1231,6 @@ def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | No
         if out.size(2) != keep:
             out = out[:, :, :keep]
     _row_call("ssc_move_rows", cache, cache, cache.element_size(), batch, heads, capacity, width, cache.stride(0),
-              cache.stride(1), cache.stride(2), kept, keep, to, to.stride(0), to.stride(1), to.stride(2))
+              cache.stride(1), cache.stride(2), kept, keep, to, to.stride(0), to.stride(1), to.stride(2),
+              scratch, _numel(scratch))
     return cache if out is None else out

@@ -30,6 +30,9 @@ struct AccumulateArgs {
     uint32_t group, queries;
     int64_t fresh;
     float decay;
+    // few long columns: the rows in `splits` parts, their sums in scratch
+    uint32_t splits, col_blocks;
+    float *part;  // [splits][batch][heads][length]
 };
 
 // EVEN: the rows of a cache head lie evenly apart (queries of one head)
@@ -46,7 +49,8 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     const int64_t h = blockIdx.y, b = blockIdx.z;
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int lane = lane_id();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kWave * kN + lane * kN;
+    const uint32_t split = blockIdx.x / a.col_blocks;
+    const int64_t first = static_cast<int64_t>(blockIdx.x - split * a.col_blocks) * kWave * kN + lane * kN;
     const T *from = static_cast<const T *>(a.weights) + b * a.weight_batch + h * a.weight_group + first;
     float *to = a.scores + b * a.score_batch + h * a.score_head + first;
     int64_t len = a.length;
@@ -59,7 +63,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     // the earlier scores are on their way while the weights are read
     const int64_t old = len - a.fresh;  // positions with an earlier score
     Score before[kN / 4];
-    const bool vector = first + kN <= len && first + kN <= old && w == 0;
+    const bool vector = first + kN <= len && first + kN <= old && w == 0 && a.splits == 1;
 #pragma unroll
     for (int i = 0; i < kN / 4; ++i) {
         before[i] = Score{0.0f, 0.0f, 0.0f, 0.0f};
@@ -68,7 +72,9 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     float sum[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) sum[e] = 0.0f;
-    const uint32_t rows = a.group * a.queries;
+    const uint32_t all = a.group * a.queries, share = (all + a.splits - 1) / a.splits;
+    const uint32_t begin = split * share < all ? split * share : all;  // the last parts may be empty
+    const uint32_t rows = all - begin < share ? all : begin + share;
     // a weight that is no number (of a query whose mask left nothing) adds nothing
     const auto add = [&](const V &v) {
 #pragma unroll
@@ -82,7 +88,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
         return from + (r / a.queries) * a.weight_head + (r % a.queries) * a.weight_query;
     };
     if (whole) {
-        uint32_t r = w;
+        uint32_t r = begin + w;
         const auto some = [&](auto count) {
             constexpr int C = decltype(count)::value;
             Raw raw[C];
@@ -98,7 +104,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
         if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
         while (r < rows) some(std::integral_constant<int, 1>{});
     } else if (first < a.length) {
-        for (uint32_t r = w; r < rows; r += WAVES) {
+        for (uint32_t r = begin + w; r < rows; r += WAVES) {
             const T *p = row(r);
             V v;
 #pragma unroll
@@ -118,7 +124,12 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
             for (int e = 0; e < kN; ++e) sum[e] += s_sum[v][e * kWave + lane];
         }
     }
-    if (vector) {
+    if (a.splits > 1) {
+        float *part = a.part + ((static_cast<int64_t>(split) * gridDim.z + b) * gridDim.y + h) * a.length + first;
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+            if (first + e < len) part[e] = sum[e];
+    } else if (vector) {
 #pragma unroll
         for (int i = 0; i < kN / 4; ++i) {
             Score s;
@@ -135,6 +146,26 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     }
 }
 
+// The parts' sums joined, in their order.
+__global__ __launch_bounds__(256) void accumulate_join_kernel(AccumulateArgs a) {
+    const int64_t h = blockIdx.y, b = blockIdx.z;
+    int64_t len = a.length;
+    if (a.lengths != nullptr) {
+        const int64_t l = a.lengths[b];
+        len = l < len ? l : len;
+    }
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= len) return;
+    float *to = a.scores + b * a.score_batch + h * a.score_head + i;
+    const float old = i < len - a.fresh ? *to : 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.z) * gridDim.y * a.length;
+    const float *part = a.part + (b * gridDim.y + h) * a.length + i;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (uint32_t s = 0; s < a.splits; ++s) sum += part[s * step];
+    *to = i < len - a.fresh ? __builtin_fmaf(old, a.decay, sum) : sum;
+}
+
 // ------------------------------------------------------- which rows stay ---
 // The threshold is the `need`-th largest score, found by its leading 11, 11 and
 // 10 bits: counts by digit in LDS, a scan from the largest digit down, then the
@@ -144,8 +175,9 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
 //
 // Up to 32,768 positions a workgroup does all of a head, its scores in
 // registers. Longer heads, and those of a few that leave the chip empty, go over
-// several workgroups (splits) and four launches: a count by each digit, which
-// first joins the splits' counts of the one before, and the output.
+// several workgroups (splits) and three launches: counts by the first digit;
+// these joined, counts by the second and a list of the scores that share the
+// first; those joined, the third digit from the lists, and the output.
 constexpr int kEvictBlock = 1024;
 constexpr int kEvictWaves = kEvictBlock / kWave;
 constexpr int kEvictBins = 2048;
@@ -167,9 +199,11 @@ struct EvictArgs {
     int32_t *kept, *counts;
     // of the splits
     uint32_t splits, span;  // and positions of one, a multiple of kEvictTile
-    Threshold *found;       // [rows][passes]
-    uint32_t *before;       // [rows][splits] scores of earlier splits that stay, as far as known
-    uint32_t *hist;         // [2][rows][splits][bins] of this pass and the one before
+    Threshold *found;       // [rows] by the first digit
+    uint32_t *before;       // [rows][splits] scores of earlier splits that stay for it
+    uint32_t *hist;         // [2][rows][splits][bins] of the first two digits
+    uint32_t *listed;       // [rows][splits] scores that share the first digit,
+    uint32_t *list;         // [rows][splits][span] and they, in no order
 };
 
 __device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : (pass == 1 ? 10 : 0); }
@@ -368,24 +402,12 @@ __global__ __launch_bounds__(kEvictBlock) void evict_kernel(EvictArgs a) {
 constexpr int kEvictItems = 8;
 constexpr uint32_t kEvictTile = kEvictItems * kEvictBlock;
 
-// The counts of pass - 1 joined over the splits: the digit, and how many scores of
-// earlier splits stay for it (`equals`: of those that share the digits found, where
-// not all of them do).
-__device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh, int64_t bh, int64_t rows, int pass,
-                                            Threshold &t, uint32_t &before, uint32_t &equals) {
+// How many scores of earlier splits stay for the digit that was found: those of
+// larger ones, and its own if all of it does. Otherwise `equals` is the number
+// of its own. b0 and b1 are the earlier splits' counts of this thread's bins.
+__device__ __forceinline__ void count_before(EvictShared &sh, uint32_t top, uint32_t b0, uint32_t b1,
+                                             const Threshold &t, uint32_t &before, uint32_t &equals) {
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
-    const uint32_t *hist = a.hist + ((((pass - 1) & 1) * rows + bh) * a.splits) * kEvictBins;
-    uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
-#pragma unroll 16
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(hist + static_cast<int64_t>(s) * kEvictBins + top - 1u);
-        c0 += c.y;
-        c1 += c.x;
-        b0 += s < blockIdx.z ? c.y : 0u;
-        b1 += s < blockIdx.z ? c.x : 0u;
-    }
-    find_digit(sh, c0, c1, pass - 1, t);
     const uint32_t d = sh.digit;
     const uint32_t mine = (top > d ? b0 : 0u) + (top - 1u > d ? b1 : 0u);
     const uint32_t sum = wave_inclusive_scan<SumU32>(mine);
@@ -401,61 +423,140 @@ __device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh,
     __syncthreads();
 }
 
-// pass 0 .. 2: counts by a digit; 3: the output
-template <bool LAST>
-__global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a, int pass) {
+// The splits' counts of a pass joined.
+__device__ __forceinline__ void join_splits(const EvictArgs &a, EvictShared &sh, int64_t bh, int64_t rows, int pass,
+                                            Threshold &t, uint32_t &before, uint32_t &equals) {
+    const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
+    const uint32_t *hist = a.hist + ((pass * rows + bh) * a.splits) * kEvictBins;
+    uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
+#pragma unroll 16
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const uint2 c = *reinterpret_cast<const uint2 *>(hist + static_cast<int64_t>(s) * kEvictBins + top - 1u);
+        c0 += c.y;
+        c1 += c.x;
+        b0 += s < blockIdx.z ? c.y : 0u;
+        b1 += s < blockIdx.z ? c.x : 0u;
+    }
+    find_digit(sh, c0, c1, pass, t);
+    count_before(sh, top, b0, b1, t, before, equals);
+}
+
+// The third digit from the lists of the scores that share the first, of which a
+// wavefront reads every 16th split's.
+__device__ __forceinline__ void join_lists(const EvictArgs &a, EvictShared &sh, uint32_t *before_hist, int64_t bh,
+                                           Threshold &t, uint32_t &before, uint32_t &equals) {
+    const int lane = lane_id();
+    const int w = static_cast<int>(uniform(threadIdx.x / kWave));
+    for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) {
+        sh.hist[i] = 0;
+        before_hist[i] = 0;
+    }
+    __syncthreads();
+    for (uint32_t s = w; s < a.splits; s += kEvictWaves) {
+        const uint32_t n = least(a.listed[bh * a.splits + s], a.span);
+        const uint32_t *list = a.list + (bh * a.splits + s) * a.span;
+        for (uint32_t i = 0; i < n; i += 4 * kWave) {
+            uint32_t k[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) k[j] = list[least(i + j * kWave + lane, n - 1u)];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const bool counts = i + j * kWave + lane < n && (k[j] & t.fixed) == t.low;
+                count_digit(sh.hist, k[j] & 1023u, counts);
+                if (s < blockIdx.z) count_digit(before_hist, k[j] & 1023u, counts);
+            }
+        }
+    }
+    __syncthreads();
+    const uint32_t top = kEvictBins - 1u - 2u * threadIdx.x;
+    const uint32_t b0 = before_hist[top], b1 = before_hist[top - 1u];
+    find_digit(sh, sh.hist[top], sh.hist[top - 1u], 2, t);
+    count_before(sh, top, b0, b1, t, before, equals);
+}
+
+enum EvictStep { kFirstDigit, kSecondDigit, kOutput };
+
+template <EvictStep STEP>
+__global__ __launch_bounds__(kEvictBlock) void evict_split_kernel(EvictArgs a) {
     __shared__ EvictShared sh;
+    __shared__ uint32_t s_more[STEP == kOutput ? kEvictBins : 1];
     const uint32_t split = blockIdx.z;
     const int64_t bh = static_cast<int64_t>(blockIdx.y) * a.heads + blockIdx.x;
     const int64_t rows = static_cast<int64_t>(gridDim.x) * gridDim.y;
     const Head head(a, blockIdx.x, blockIdx.y);
     if (head.len <= a.keep) {
-        if (LAST) head.keep_all(a, a.counts + bh, split * kEvictBlock + threadIdx.x, a.splits * kEvictBlock);
+        if (STEP == kOutput) head.keep_all(a, a.counts + bh, split * kEvictBlock + threadIdx.x, a.splits * kEvictBlock);
         return;
     }
+    const int lane = lane_id();
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const uint32_t from = split * a.span;
     const uint32_t to = head.len - least(from, head.len) < a.span ? head.len : from + a.span;
     // the first tile's scores are on their way while the splits' counts are joined
-    const uint32_t mine = static_cast<uint32_t>(w) * kEvictItems * kWave + lane_id();
+    const uint32_t mine = static_cast<uint32_t>(w) * kEvictItems * kWave + lane;
     uint32_t key[kEvictItems];
     head.load(from + mine, to, key);
     Threshold t{0u, 0u, a.keep, 0u};
     uint32_t before = 0, equals = 0;
-    if (pass > 0) {
-        if (pass > 1) {
-            t = a.found[bh * kEvictPasses + pass - 2];
-            before = a.before[bh * a.splits + split];
-        }
-        if (!t.all) join_splits(a, sh, bh, rows, pass, t, before, equals);
-        if (!LAST && threadIdx.x == 0) {
-            if (split == 0) a.found[bh * kEvictPasses + pass - 1] = t;
+    if constexpr (STEP == kSecondDigit) {
+        join_splits(a, sh, bh, rows, 0, t, before, equals);
+        if (threadIdx.x == 0) {
+            if (split == 0) a.found[bh] = t;
             a.before[bh * a.splits + split] = before;
+            sh.before = 0;  // scores listed so far
         }
-    }
-    if constexpr (!LAST) {
         if (t.all) return;
+    }
+    if constexpr (STEP == kOutput) {
+        t = a.found[bh];
+        before = a.before[bh * a.splits + split];
+        if (!t.all) join_splits(a, sh, bh, rows, 1, t, before, equals);
+        if (!t.all) join_lists(a, sh, s_more, bh, t, before, equals);
+    }
+    if constexpr (STEP != kOutput) {
+        constexpr int kPass = STEP == kFirstDigit ? 0 : 1;
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) sh.hist[i] = 0;
         __syncthreads();
+        uint32_t *list = a.list + (bh * a.splits + split) * a.span;
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
             if (tile != from) head.load(tile + mine, to, key);
-            count_digits(sh.hist, key, t, pass);
+            count_digits(sh.hist, key, t, kPass);
+            if constexpr (STEP == kSecondDigit) {
+                uint32_t many = 0;
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j)
+                    many += static_cast<uint32_t>(__builtin_popcountll(ballot((key[j] & t.fixed) == t.low)));
+                uint32_t at = 0;
+                if (lane == 0 && many > 0)
+                    at = __hip_atomic_fetch_add(&sh.before, many, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                at = uniform(at);
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j) {
+                    const bool shares = (key[j] & t.fixed) == t.low;
+                    const uint64_t shared = ballot(shares);
+                    const uint32_t slot = at + mbcnt64(shared);
+                    if (shares && slot < a.span) list[slot] = key[j];
+                    at += static_cast<uint32_t>(__builtin_popcountll(shared));
+                }
+            }
         }
         __syncthreads();
-        uint32_t *hist = a.hist + (((pass & 1) * rows + bh) * a.splits + split) * kEvictBins;
+        uint32_t *hist = a.hist + ((kPass * rows + bh) * a.splits + split) * kEvictBins;
         for (uint32_t i = threadIdx.x; i < kEvictBins; i += kEvictBlock) hist[i] = sh.hist[i];
+        if (STEP == kSecondDigit && threadIdx.x == 0) a.listed[bh * a.splits + split] = sh.before;
     } else {
         for (uint32_t tile = from; tile < to; tile += kEvictTile) {
             if (tile != from) head.load(tile + mine, to, key);
             const Staying<kEvictItems> stay(key, t);
-            if (lane_id() == 0) {
+            if (lane == 0) {
                 sh.wave[w] = stay.sures;
                 sh.wave_equal[w] = stay.equals;
             }
             __syncthreads();
             uint32_t all_sures, all_equals;
             const uint32_t run = equals + waves_before(sh.wave_equal, w, all_equals);
-            stay.emit(a, head, tile + mine, before + waves_before(sh.wave, w, all_sures) + least(run, t.need), run, t.need);
+            stay.emit(a, head, tile + mine, before + waves_before(sh.wave, w, all_sures) + least(run, t.need), run,
+                      t.need);
             before += all_sures;
             equals += all_equals;
             __syncthreads();
@@ -481,6 +582,8 @@ struct MoveArgs {
     const int32_t *kept;
     int heads, capacity, keep;
     int row_bytes, chunks;
+    int moved;   // 0: every row that is kept; in place, those that lie past their slot: to scratch (1),
+                 // or from there (2), where row s is slot s's
     int lg;      // log2 of the lanes of a row
     int cols;    // chunks of a row that a workgroup moves
 };
@@ -532,8 +635,9 @@ __global__ __launch_bounds__(kMoveBlock) void move_kernel(MoveArgs a) {
 #pragma unroll
     for (int j = 0; j < kMoveFlight; ++j) {
         const int64_t s = first + j * rows;
-        pos[j] = s < a.keep ? kept[s] : -1;
-        if (pos[j] >= a.capacity) pos[j] = -1;
+        const int32_t k = s < a.keep ? kept[s] : -1;
+        const bool moves = k >= 0 && k < a.capacity && (a.moved == 0 || k > s);
+        pos[j] = moves ? (a.moved == 2 ? s : k) : -1;
     }
     for (int c = static_cast<int>(threadIdx.x) & ((1 << a.lg) - 1); c < a.chunks; c += 1 << a.lg) {
         const int at = piece_at<BYTES>(a, c);
@@ -548,34 +652,36 @@ __global__ __launch_bounds__(kMoveBlock) void move_kernel(MoveArgs a) {
 }
 
 constexpr int kPlaceBlock = 1024;
+constexpr int kPlaceFlight = 4;  // pieces of a lane at a time
 
 template <int BYTES>
 __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) {
     using P = Piece<BYTES>;
-    const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.heads + h;
+    // the columns of a head last: where the heads are a multiple of 8 they share an XCD
+    const int64_t h = blockIdx.x, b = blockIdx.y, bh = b * a.heads + h;
     char *rows_at = a.to + b * a.to_batch + h * a.to_head;
     const int32_t *kept = a.kept + bh * a.keep;
     const int rows = kPlaceBlock >> a.lg;
     const int lane_col = static_cast<int>(threadIdx.x) & ((1 << a.lg) - 1);
-    const int c0 = static_cast<int>(blockIdx.x) * a.cols, c1 = c0 + a.cols < a.chunks ? c0 + a.cols : a.chunks;
-    const int64_t step = static_cast<int64_t>(rows) * kMoveFlight;
+    const int c0 = static_cast<int>(blockIdx.z) * a.cols, c1 = c0 + a.cols < a.chunks ? c0 + a.cols : a.chunks;
+    const int64_t step = static_cast<int64_t>(rows) * kPlaceFlight;
     // a slot's position, -1 for none: one that stays where it is needs no move, one
     // that lies before its slot is none of evict_rows
-    int32_t pos[kMoveFlight], next[kMoveFlight];
-    const auto positions = [&](int64_t set, int32_t(&p)[kMoveFlight]) {
+    int32_t pos[kPlaceFlight], next[kPlaceFlight];
+    const auto positions = [&](int64_t set, int32_t(&p)[kPlaceFlight]) {
 #pragma unroll
-        for (int j = 0; j < kMoveFlight; ++j) {
+        for (int j = 0; j < kPlaceFlight; ++j) {
             const int64_t s = set + (threadIdx.x >> a.lg) + j * rows;
             const int32_t k = kept[s < a.keep ? s : a.keep - 1];
             p[j] = s < a.keep && k < a.capacity && k > s ? k : -1;
         }
     };
-    typename P::V v[kMoveFlight];
-    const auto load = [&](int base, const int32_t(&p)[kMoveFlight]) {
+    typename P::V v[kPlaceFlight];
+    const auto load = [&](int base, const int32_t(&p)[kPlaceFlight]) {
         const int c = base + lane_col;
         const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
 #pragma unroll
-        for (int j = 0; j < kMoveFlight; ++j)
+        for (int j = 0; j < kPlaceFlight; ++j)
             if (p[j] >= 0 && c < c1) v[j] = P::load_stream(rows_at + static_cast<int64_t>(p[j]) * a.to_row + at);
     };
     positions(0, pos);
@@ -588,7 +694,7 @@ __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) 
             const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
             const int64_t first = set + (threadIdx.x >> a.lg);
 #pragma unroll
-            for (int j = 0; j < kMoveFlight; ++j)
+            for (int j = 0; j < kPlaceFlight; ++j)
                 if (pos[j] >= 0 && c < c1) P::store_stream(rows_at + (first + j * rows) * a.to_row + at, v[j]);
             // the next pieces are on their way while these are stored
             if (base + (1 << a.lg) < c1)
@@ -597,7 +703,7 @@ __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) 
                 load(c0, next);
         }
 #pragma unroll
-        for (int j = 0; j < kMoveFlight; ++j) pos[j] = next[j];
+        for (int j = 0; j < kPlaceFlight; ++j) pos[j] = next[j];
     }
 }
 
@@ -607,6 +713,65 @@ int check_cache(int64_t batch, int64_t heads, int64_t capacity) {
     if (batch > INT32_MAX || heads > INT32_MAX || capacity > INT32_MAX - 4096 || batch * heads > 65535)
         return SSC_ERR_SIZE;
     return SSC_OK;
+}
+
+// Workgroups of 64 lanes' columns; and where the wavefronts of these are few
+// (under 2048) and have over 16 rows each, the rows in parts, up to 4096 wavefronts
+// in all. Two heads of 4 sequences, 456 rows of 1390 fp16: 36 us in one part.
+struct AccumulatePlan {
+    uint32_t splits, col_blocks;
+    size_t bytes;
+};
+
+AccumulatePlan accumulate_plan(int64_t heads, int64_t rows, int64_t length, int dtype) {
+    AccumulatePlan p{};
+    const int64_t cols = kWave * 16 / static_cast<int64_t>(elem_bytes(dtype));
+    p.col_blocks = static_cast<uint32_t>((length + cols - 1) / cols);
+    p.splits = 1;
+    const int64_t waves = heads * p.col_blocks * 8;
+    if (waves > 0 && waves < 2048 && rows > 128) {
+        const int64_t wanted = (4096 + waves - 1) / waves, most = (rows + 127) / 128;
+        p.splits = static_cast<uint32_t>(wanted < most ? wanted : most);
+        p.bytes = static_cast<size_t>(p.splits) * heads * length * 4;
+    }
+    return p;
+}
+
+// A move in place: directly, few heads with their columns over several
+// workgroups (no two of these share bytes of a row, nor less than 64 bytes), or
+// by way of scratch. A workgroup's set of rows takes 4.5 us one after another; the
+// scratch doubles the traffic but has no such order. Rows moved, direct against
+// scratch, us:
+//   2 heads x 20,000 of 128 bytes   84   11      4 heads x 2500 of 1024 bytes   19   13
+//   8 x 20,000 of 256               88   35      8 x 1024 of 256               5.6  9.8
+//   22 x 4382 of 192                25   18      48 x 4695 of 256               34   46
+//   32 x 2048 of 130                32   14      256 x 4096 of 256             102  188
+struct MovePlan {
+    int piece, cols;
+    size_t bytes;
+};
+
+MovePlan move_plan(int64_t heads, int64_t keep, int64_t row_bytes, int elem) {
+    MovePlan p{};
+    // pieces that overlap must all be read before one is stored
+    const bool overlap = row_bytes % 16 != 0 && row_bytes > 16 << 8;
+    p.piece = row_bytes >= 16 && !overlap ? 16 : elem;
+    const int64_t chunks = (row_bytes + p.piece - 1) / p.piece;
+    int64_t parts = 1;
+    if (row_bytes % p.piece == 0 && heads > 0) {
+        const int64_t most = chunks * p.piece / 64;
+        parts = 512 / heads;
+        parts = parts < most ? parts : most;
+        parts = parts < 1 ? 1 : parts;
+    }
+    p.cols = static_cast<int>((chunks + parts - 1) / parts);
+    int lg = 0;
+    while (lg < 8 && (1 << lg) < p.cols) ++lg;
+    const int64_t set = (kPlaceBlock >> lg) * kPlaceFlight;
+    const double sets = static_cast<double>((keep + set - 1) / set) * ((p.cols + (1 << lg) - 1) >> lg);
+    const double bytes = static_cast<double>(heads) * static_cast<double>(keep) * static_cast<double>(row_bytes);
+    if (4.5 * sets > 6.0 + 4.0 * bytes / 6.3e6) p.bytes = static_cast<size_t>(heads) * keep * row_bytes;
+    return p;
 }
 
 // Splits of a head: of 8192 positions where that gives up to 512 workgroups,
@@ -628,8 +793,8 @@ EvictPlan evict_plan(int64_t rows, int64_t capacity) {
     p.span = static_cast<uint32_t>(each * kEvictTile);
     const size_t all = static_cast<size_t>(rows) * p.splits;
     p.found = 2 * all * kEvictBins * 4;
-    p.before = p.found + static_cast<size_t>(rows) * kEvictPasses * sizeof(Threshold);
-    p.bytes = p.before + all * 4;
+    p.before = p.found + static_cast<size_t>(rows) * sizeof(Threshold);
+    p.bytes = p.before + 2 * all * 4 + all * p.span * 4;
     return p;
 }
 
@@ -640,6 +805,21 @@ using namespace ssc;
 
 extern "C" {
 
+size_t ssc_accumulate_scratch_bytes(int64_t batch, int64_t heads, int64_t group, int64_t queries, int64_t length,
+                                    int dtype) {
+    if (check_cache(batch, heads, 1) != SSC_OK || !dtype_ok(dtype) || group < 1 || queries < 0 || length < 0 ||
+        length > INT32_MAX || group > INT32_MAX || queries > INT32_MAX)
+        return 0;
+    return accumulate_plan(batch * heads, group * queries, length, dtype).bytes;
+}
+
+size_t ssc_move_scratch_bytes(int elem_bytes, int64_t batch, int64_t heads, int64_t keep, int64_t width) {
+    if (check_cache(batch, heads, 1) != SSC_OK || batch < 1 || keep < 1 || keep > INT32_MAX || width < 1 ||
+        width > (1 << 24) || elem_bytes < 1 || elem_bytes > 8)
+        return 0;
+    return move_plan(batch * heads, keep, width * elem_bytes, elem_bytes).bytes;
+}
+
 size_t ssc_evict_scratch_bytes(int64_t batch, int64_t heads, int64_t capacity) {
     if (check_cache(batch, heads, capacity) != SSC_OK) return 0;
     return evict_plan(batch * heads, capacity).bytes;
@@ -648,7 +828,8 @@ size_t ssc_evict_scratch_bytes(int64_t batch, int64_t heads, int64_t capacity) {
 int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t capacity, int64_t score_batch,
                            int64_t score_head, const void *weights, int dtype, int64_t group, int64_t queries,
                            int64_t length, int64_t weight_batch, int64_t weight_head, int64_t weight_query,
-                           const int32_t *lengths, int64_t fresh, float decay, void *stream) {
+                           const int32_t *lengths, int64_t fresh, float decay, void *scratch, size_t scratch_bytes,
+                           void *stream) {
     SSC_TRY(check_cache(batch, heads, capacity));
     if (!dtype_ok(dtype) || group < 1 || queries < 0 || length < 0 || length > capacity || fresh < 0) return SSC_ERR_ARG;
     if (group > INT32_MAX || queries > INT32_MAX || group * queries > (int64_t{1} << 30) || heads * group > INT32_MAX)
@@ -658,10 +839,15 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
     if (!s.strides_ok() || !w.strides_ok() || !s.distinct()) return SSC_ERR_ARG;
     if (batch > 0 && (scores == nullptr || (w.extent() > 0 && weights == nullptr))) return SSC_ERR_ARG;
     if (!aligned(scores, 4) || !aligned(weights, elem_bytes(dtype)) || !aligned(lengths, 4)) return SSC_ERR_ARG;
-    const size_t out = static_cast<size_t>(s.extent()) * 4;
-    if (overlap(scores, out, weights, static_cast<size_t>(w.extent()) * elem_bytes(dtype)) ||
-        overlap(scores, out, lengths, static_cast<size_t>(batch) * 4))
-        return SSC_ERR_ALIAS;
+    const AccumulatePlan p = accumulate_plan(batch * heads, group * queries, length, dtype);
+    if (p.bytes > 0 && (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < p.bytes)) return SSC_ERR_SCRATCH;
+    const Span written[] = {{scores, static_cast<size_t>(s.extent()) * 4}, {scratch, p.bytes}};
+    const Span read[] = {{weights, static_cast<size_t>(w.extent()) * elem_bytes(dtype)},
+                         {lengths, static_cast<size_t>(batch) * 4}};
+    if (spans_overlap(written)) return SSC_ERR_ALIAS;
+    for (const Span &x : written)
+        for (const Span &y : read)
+            if (overlap(x.p, x.bytes, y.p, y.bytes)) return SSC_ERR_ALIAS;
     SSC_TRY(check_device());
     if (batch == 0 || length == 0) return SSC_OK;
     AccumulateArgs a{};
@@ -683,11 +869,12 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
     if (queries == 1) a.weight_query = weight_head;
     const bool even = group == 1 || queries <= 1 || weight_head == queries * weight_query;
     const int64_t rows = group * queries;
-    return with_dtype(dtype, [&](auto t) {
+    a.splits = p.splits;
+    a.col_blocks = p.col_blocks;
+    a.part = static_cast<float *>(scratch);
+    SSC_TRY(with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        const int64_t cols = kWave * 16 / static_cast<int64_t>(sizeof(T));
-        const dim3 grid(static_cast<unsigned>((length + cols - 1) / cols), static_cast<unsigned>(heads),
-                        static_cast<unsigned>(batch));
+        const dim3 grid(p.splits * p.col_blocks, static_cast<unsigned>(heads), static_cast<unsigned>(batch));
         const auto launch = [&](auto waves) {
             constexpr int W = decltype(waves)::value;
             if (even)
@@ -701,7 +888,13 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
         if (rows <= 16) return launch(std::integral_constant<int, 1>{});
         if (rows <= 64) return launch(std::integral_constant<int, 4>{});
         return launch(std::integral_constant<int, 8>{});
-    });
+    }));
+    if (p.splits == 1) return SSC_OK;
+    hipLaunchKernelGGL(accumulate_join_kernel,
+                       dim3(static_cast<unsigned>((length + 255) / 256), static_cast<unsigned>(heads),
+                            static_cast<unsigned>(batch)),
+                       dim3(256), 0, static_cast<hipStream_t>(stream), a);
+    return launched();
 }
 
 int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t capacity, int64_t score_batch,
@@ -745,12 +938,14 @@ int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t ca
         a.hist = reinterpret_cast<uint32_t *>(at);
         a.found = reinterpret_cast<Threshold *>(at + p.found);
         a.before = reinterpret_cast<uint32_t *>(at + p.before);
+        a.listed = a.before + rows * p.splits;
+        a.list = a.listed + rows * p.splits;
         const dim3 grid(static_cast<unsigned>(heads), static_cast<unsigned>(batch), p.splits);
-        for (int pass = 0; pass < kEvictPasses; ++pass) {
-            hipLaunchKernelGGL((evict_split_kernel<false>), grid, dim3(kEvictBlock), 0, s, a, pass);
-            SSC_TRY(launched());
-        }
-        hipLaunchKernelGGL((evict_split_kernel<true>), grid, dim3(kEvictBlock), 0, s, a, kEvictPasses);
+        hipLaunchKernelGGL((evict_split_kernel<kFirstDigit>), grid, dim3(kEvictBlock), 0, s, a);
+        SSC_TRY(launched());
+        hipLaunchKernelGGL((evict_split_kernel<kSecondDigit>), grid, dim3(kEvictBlock), 0, s, a);
+        SSC_TRY(launched());
+        hipLaunchKernelGGL((evict_split_kernel<kOutput>), grid, dim3(kEvictBlock), 0, s, a);
         return launched();
     }
     const auto launch = [&](auto items) {
@@ -766,7 +961,8 @@ int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t ca
 
 int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t heads, int64_t capacity, int64_t width,
                   int64_t cache_batch, int64_t cache_head, int64_t cache_row, const int32_t *kept, int64_t keep,
-                  void *out, int64_t out_batch, int64_t out_head, int64_t out_row, void *stream) {
+                  void *out, int64_t out_batch, int64_t out_head, int64_t out_row, void *scratch, size_t scratch_bytes,
+                  void *stream) {
     SSC_TRY(check_cache(batch, heads, capacity));
     if ((elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4 && elem_bytes != 8) || width < 1 || keep < 1 ||
         keep > capacity)
@@ -786,6 +982,14 @@ int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t head
     if ((!place && overlap(out, out_bytes, cache, cache_bytes)) ||
         overlap(out, place ? cache_bytes : out_bytes, kept, static_cast<size_t>(batch) * heads * keep * 4))
         return SSC_ERR_ALIAS;
+    const MovePlan p = move_plan(batch * heads, keep, width * elem_bytes, elem_bytes);
+    const size_t need = place ? p.bytes : 0;
+    if (need > 0) {
+        if (scratch == nullptr || !aligned(scratch, 16) || scratch_bytes < need) return SSC_ERR_SCRATCH;
+        if (overlap(scratch, need, out, cache_bytes) ||
+            overlap(scratch, need, kept, static_cast<size_t>(batch) * heads * keep * 4))
+            return SSC_ERR_ALIAS;
+    }
     SSC_TRY(check_device());
     if (batch == 0) return SSC_OK;
     MoveArgs a{};
@@ -802,35 +1006,45 @@ int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t head
     a.capacity = static_cast<int>(capacity);
     a.keep = static_cast<int>(keep);
     a.row_bytes = static_cast<int>(width * elem_bytes);
-    // pieces that overlap must all be read before one is stored
-    const bool shared = place && a.row_bytes % 16 != 0 && a.row_bytes > 16 << 8;
-    const int bytes = a.row_bytes >= 16 && !shared ? 16 : elem_bytes;
+    const bool direct = place && need == 0;
+    const int bytes = direct ? p.piece : (a.row_bytes >= 16 ? 16 : elem_bytes);
     a.chunks = (a.row_bytes + bytes - 1) / bytes;
-    a.cols = a.chunks;
-    while (a.lg < 8 && (1 << a.lg) < a.chunks) ++a.lg;
-    dim3 grid(1, static_cast<unsigned>(heads), static_cast<unsigned>(batch));
-    if (place) {
-        // few heads: their columns over several workgroups, where no two of
-        // these share bytes of a row
-        int parts = 1;
-        while (a.row_bytes % bytes == 0 && batch * heads * parts < 512 && a.chunks / (parts * 2) >= 4 &&
-               a.chunks % (parts * 2) == 0)
-            parts *= 2;
-        a.cols = a.chunks / parts;
-        a.lg = 0;
-        while (a.lg < 8 && (1 << a.lg) < a.cols) ++a.lg;
-        grid.x = static_cast<unsigned>(parts);
-    } else {
-        const int64_t rows = static_cast<int64_t>(kMoveBlock >> a.lg) * kMoveFlight;
-        grid.x = static_cast<unsigned>((keep + rows - 1) / rows);
-    }
+    a.cols = direct ? p.cols : a.chunks;
+    while (a.lg < 8 && (1 << a.lg) < a.cols) ++a.lg;
+    const int64_t rows = static_cast<int64_t>(kMoveBlock >> a.lg) * kMoveFlight;
+    hipStream_t s = static_cast<hipStream_t>(stream);
     const auto launch = [&](auto piece) {
         constexpr int B = decltype(piece)::value;
-        if (place)
-            hipLaunchKernelGGL((move_in_place_kernel<B>), grid, dim3(kPlaceBlock), 0, static_cast<hipStream_t>(stream),
-                               a);
-        else
-            hipLaunchKernelGGL((move_kernel<B>), grid, dim3(kMoveBlock), 0, static_cast<hipStream_t>(stream), a);
+        if (direct) {
+            const dim3 grid(static_cast<unsigned>(heads), static_cast<unsigned>(batch),
+                            static_cast<unsigned>((a.chunks + a.cols - 1) / a.cols));
+            hipLaunchKernelGGL((move_in_place_kernel<B>), grid, dim3(kPlaceBlock), 0, s, a);
+            return launched();
+        }
+        const dim3 grid(static_cast<unsigned>((keep + rows - 1) / rows), static_cast<unsigned>(heads),
+                        static_cast<unsigned>(batch));
+        if (!place) {
+            hipLaunchKernelGGL((move_kernel<B>), grid, dim3(kMoveBlock), 0, s, a);
+            return launched();
+        }
+        MoveArgs m = a;  // to scratch, and back into place
+        m.moved = 1;
+        m.to = static_cast<char *>(scratch);
+        m.to_row = a.row_bytes;
+        m.to_head = keep * m.to_row;
+        m.to_batch = heads * m.to_head;
+        hipLaunchKernelGGL((move_kernel<B>), grid, dim3(kMoveBlock), 0, s, m);
+        SSC_TRY(launched());
+        m.moved = 2;
+        m.from = m.to;
+        m.from_row = m.to_row;
+        m.from_head = m.to_head;
+        m.from_batch = m.to_batch;
+        m.to = a.to;
+        m.to_row = a.to_row;
+        m.to_head = a.to_head;
+        m.to_batch = a.to_batch;
+        hipLaunchKernelGGL((move_kernel<B>), grid, dim3(kMoveBlock), 0, s, m);
         return launched();
     };
     switch (bytes) {

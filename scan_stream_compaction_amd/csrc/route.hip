@@ -360,6 +360,9 @@ struct RouteArgs {
     int32_t *part_count;
     double *part_loss;
     uint32_t *done;
+    // the results, where one workgroup has all of the tokens
+    int32_t *counts;
+    float *share, *loss;
 };
 
 // With the balance a workgroup adds up its tokens' softmax, so it is larger and
@@ -389,7 +392,7 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < N; ++j) share[j] = 0.0f;
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0 && a.counts == nullptr) *a.done = 0;
     }
     // a row's loads are on their way while the one before it is worked on, where
     // the registers hold both
@@ -489,6 +492,30 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
         for (int j = 0; j < N; ++j)
             if (w < kHalf && lane < G && held.own(j)) s_share[w][held.index(j)] += share[j];
         __syncthreads();
+        if (a.counts != nullptr) {
+            __shared__ double s_loss[kBlock / kWave];
+            const uint32_t n = s_count[G * N];
+            double sum = 0.0;
+            for (int i = threadIdx.x; i < a.experts; i += kBlock) {
+                double p = 0.0;
+#pragma unroll
+                for (int v = 0; v < kHalf; ++v) p += static_cast<double>(s_share[v][i]);
+                p = n > 0 ? p / n : 0.0;
+                a.share[i] = static_cast<float>(p);
+                a.counts[i] = static_cast<int32_t>(s_count[i]);
+                sum += p * s_count[i];
+            }
+#pragma unroll
+            for (int off = 1; off < kWave; off *= 2) sum += __shfl_xor(sum, off);
+            if (lane == 0) s_loss[w] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                a.counts[a.experts] = static_cast<int32_t>(n);
+                for (int v = 1; v < kBlock / kWave; ++v) sum += s_loss[v];
+                *a.loss = static_cast<float>(n > 0 ? sum * a.experts / (static_cast<double>(n) * a.per) : 0.0);
+            }
+            return;
+        }
         float *to = a.part_share + static_cast<int64_t>(blockIdx.x) * a.experts;
         int32_t *count = a.part_count + static_cast<int64_t>(blockIdx.x) * (a.experts + 1);
         for (int i = threadIdx.x; i < a.experts; i += kBlock) {
@@ -739,8 +766,12 @@ int64_t balance_tokens(int64_t experts) {
     return experts <= 128 ? 128 : (experts <= 192 ? 64 : (experts <= 256 ? 64 : (experts <= 512 ? 32 : 16)));
 }
 
-// Workgroups of a pass with the balance: one a compute unit, and more where a
-// lane would add over 64 rows, one after another in fp32.
+// Workgroups of a pass with the balance: one alone for up to four rows of a lane,
+// which needs no join (2216 tokens of 231 experts XX against XX us a call), else
+// one a compute unit, and more where a lane would add over 64 rows, one after
+// another in fp32.
+constexpr int64_t kAlone = 4;
+
 struct RoutePlan {
     int64_t blocks;
     size_t share, count, loss, bytes;  // offsets into the scratch
@@ -750,8 +781,9 @@ RoutePlan route_plan(int64_t tokens, int64_t experts) {
     RoutePlan p{};
     const int64_t each = balance_tokens(experts);
     const int64_t all = (tokens + each - 1) / each;
-    p.blocks = all < 1 ? 1 : (all < 256 ? all : 256);
+    p.blocks = all <= kAlone ? 1 : (all < 256 ? all : 256);
     if (p.blocks < (all + 63) / 64) p.blocks = (all + 63) / 64;
+    if (p.blocks == 1) return p;
     p.loss = 16;
     p.share = p.loss + 8 * ((experts + kJoinCols - 1) / kJoinCols);
     p.count = p.share + static_cast<size_t>(p.blocks) * experts * 4;
@@ -822,7 +854,11 @@ int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t expert
     a.normalize = normalize != 0;
     a.ids = ids;
     a.weights = weights;
-    if (balance) {
+    if (balance && p.blocks == 1) {
+        a.counts = counts;
+        a.share = share;
+        a.loss = loss;
+    } else if (balance) {
         char *at = static_cast<char *>(scratch);
         a.done = reinterpret_cast<uint32_t *>(at);
         a.part_loss = reinterpret_cast<double *>(at + p.loss);
@@ -853,7 +889,7 @@ int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t expert
             return launch(std::integral_constant<int, N>{}, std::false_type{});
         });
     }));
-    if (!balance) return SSC_OK;
+    if (!balance || p.blocks == 1) return SSC_OK;
     hipLaunchKernelGGL(route_join_kernel, dim3(static_cast<unsigned>((experts + kJoinCols - 1) / kJoinCols)),
                        dim3(kJoinBlock), 0, s, a, static_cast<int>(p.blocks), counts, share, loss);
     return launched();

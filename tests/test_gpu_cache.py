@@ -50,7 +50,8 @@ def check_accumulate(scores, weights, lengths=None, fresh=0, decay=1.0):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("batch,heads,group,queries,length,capacity", [
     (1, 1, 1, 1, 1, 1), (2, 3, 1, 1, 7, 9), (3, 2, 4, 1, 511, 512), (2, 2, 3, 5, 513, 600), (1, 2, 8, 2, 1000, 1000),
-    (2, 1, 4, 16, 1025, 1025), (1, 2, 4, 17, 300, 301), (1, 1, 8, 64, 77, 100), (1, 1, 1, 200, 2049, 4000), (2, 1, 1, 0, 5, 5)])
+    (2, 1, 4, 16, 1025, 1025), (1, 2, 4, 17, 300, 301), (1, 1, 8, 64, 77, 100), (1, 1, 1, 200, 2049, 4000), (2, 1, 1, 0, 5, 5),
+    (2, 1, 8, 57, 1390, 1390), (1, 2, 3, 700, 513, 600), (1, 1, 2, 3000, 33, 40), (1, 1, 1, 65_600, 9, 9)])
 def test_accumulate_sizes(batch, heads, group, queries, length, capacity, dtype):
     g = gen(length + queries)
     w = torch.rand(batch, heads * group, queries, length, device=DEV, generator=g).to(dtype)
@@ -171,6 +172,18 @@ def test_evict_equal_and_special_scores(capacity):
     nan[0, 1, ::2] = -float("inf")
     check_evict(nan, capacity // 2 + 3)
     check_evict(-torch.rand(1, 1, capacity, device=DEV, generator=g), capacity // 4, 2, 5)
+
+
+@pytest.mark.parametrize("capacity", [17_000, 66_000])
+def test_evict_borders_in_every_digit(capacity):
+    """Scores that share their first 11, 22 or 31 bits with the border's, spread over all splits."""
+    g = gen(capacity + 7)
+    one = torch.full((1,), 1.0, device=DEV).view(torch.int32)
+    for spread in (2, 2 ** 9, 2 ** 12, 2 ** 20, 2 ** 22):
+        s = (one + torch.randint(0, spread, (1, 2, capacity), device=DEV, generator=g)).int().view(torch.float32)
+        s = torch.where(torch.rand(s.shape, device=DEV, generator=g) < 0.3, 0.5 * s, s)
+        for keep in (5, capacity // 3, capacity // 2, capacity - 3):
+            check_evict(s, keep, 1, 3)
 
 
 def test_evict_lengths_strides_and_outputs():

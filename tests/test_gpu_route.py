@@ -94,6 +94,14 @@ def test_forward_sizes(n, experts, per, dtype):
     check_forward((x.float() * 2).round().to(dtype), per)
 
 
+@pytest.mark.parametrize("experts", [24, 150, 250, 500, 1000])
+def test_tokens_of_one_workgroup_and_more(experts):
+    alone = 4 * 16_384 // (8 * (1 if experts <= 128 else 2 if experts <= 256 else 4 if experts <= 512 else 8) * 16)
+    for n in (alone, alone + 1):
+        x, g = inputs(n, n, experts, torch.float32)
+        check_forward(x, 5, live=torch.rand(n, device=DEV, generator=g) < 0.8)
+
+
 @pytest.mark.parametrize("n", [16_383, 40_000, 300_001])
 def test_many_tokens(n):
     x, g = inputs(n, n, 24, torch.bfloat16, 2.0)

@@ -21,8 +21,8 @@ def _call(name, defaults, **kw):
 
 def test_scratch_sizes():
     # one count of workgroups done, a loss for each 16 experts, shares and counts of each workgroup
-    assert ssc.route_scratch_bytes(0, 8) == 16 + 8 + 8 * 4 + 9 * 4
-    assert ssc.route_scratch_bytes(100, 128) == 16 + 8 * 8 + (128 + 129) * 4
+    assert ssc.route_scratch_bytes(0, 8) == ssc.route_scratch_bytes(512, 128) == ssc.route_scratch_bytes(64, 1024) == 0
+    assert ssc.route_scratch_bytes(513, 128) == 16 + 8 * 8 + 5 * (128 + 129) * 4
     assert ssc.route_scratch_bytes(65_536, 128) == 16 + 8 * 8 + 256 * (128 + 129) * 4
     # at most 64 rows of a lane: 32 rows of 512 experts to a workgroup at a time
     assert ssc.route_scratch_bytes(2 ** 20, 512) == 16 + 8 * 32 + 512 * (512 + 513) * 4
@@ -33,11 +33,16 @@ def test_scratch_sizes():
     assert ssc.verify_scratch_bytes(3, 65_536) == ssc.verify_scratch_bytes(160, 131_072) == 0
     assert ssc.verify_scratch_bytes(3, 65_537) == 32 + 3 * 65 * 8
     assert ssc.verify_scratch_bytes(160, 131_073) == 160 * 8 + 160 * 129 * 8
-    # two tables of 2048 counts a split, three thresholds a head, one number a split
+    # sums of each part: one for each 128 rows, up to 4096 wavefronts
+    assert ssc.accumulate_scratch_bytes(2, 3, 4, 100, 90, torch.bfloat16) == 4 * 6 * 90 * 4
+    assert ssc.accumulate_scratch_bytes(1, 1, 4, 10_000, 90, torch.float32) == 313 * 90 * 4
+    assert ssc.accumulate_scratch_bytes(8, 8, 4, 10_000, 1025, torch.bfloat16) == 3 * 64 * 1025 * 4
+    assert ssc.accumulate_scratch_bytes(8, 8, 4, 32, 90, torch.bfloat16) == ssc.accumulate_scratch_bytes(32, 8, 8, 100, 90, torch.float16) == 0
+    # two tables of 2048 counts a split, a threshold a head, two numbers a split, a list of its positions
     assert ssc.evict_scratch_bytes(1, 8, 16_384) == ssc.evict_scratch_bytes(40, 8, 32_768) == 0
-    assert ssc.evict_scratch_bytes(1, 8, 131_072) == 8 * 16 * 16_384 + 8 * 48 + 8 * 16 * 4
-    assert ssc.evict_scratch_bytes(40, 8, 131_072) == 320 * (4 * 16_384 + 48 + 4 * 4)
-    assert ssc.evict_scratch_bytes(1, 1, 2 ** 24) == 64 * 16_384 + 48 + 64 * 4
+    assert ssc.evict_scratch_bytes(1, 8, 131_072) == 8 * 16 * (16_384 + 8 + 4 * 8192) + 8 * 16
+    assert ssc.evict_scratch_bytes(40, 8, 131_072) == 320 * (4 * (16_384 + 8 + 4 * 32_768) + 16)
+    assert ssc.evict_scratch_bytes(1, 1, 2 ** 24) == 64 * (16_384 + 8 + 4 * 2 ** 18) + 16
     assert ssc.evict_scratch_bytes(1, 0, 100) == ssc.evict_scratch_bytes(-1, 1, 100) == ssc.evict_scratch_bytes(0, 1, 2 ** 20) == 0
 
 
@@ -60,15 +65,16 @@ def test_route_refusals():
         assert _call(name, d, **{key: None}) == ARG
     for key in ("logits", "ids", "weights", "counts", "share", "loss"):
         assert _call(name, d, **{key: d[key] + 2}) == ARG
-    assert _call(name, d, scratch=None) == SCRATCH
-    assert _call(name, d, scratch=S + 8) == SCRATCH
-    assert _call(name, d, sbytes=ssc.route_scratch_bytes(100, 16) - 1) == SCRATCH
+    many = dict(d, tokens=1000, ids=B, weights=C)
+    assert _call(name, many, scratch=None) == SCRATCH
+    assert _call(name, many, scratch=S + 8) == SCRATCH
+    assert _call(name, many, sbytes=ssc.route_scratch_bytes(1000, 16) - 1) == SCRATCH
+    assert _call(name, many, scratch=A) == ALIAS
     assert _call(name, d, ids=A + 6396) == ALIAS
     assert _call(name, d, weights=B + 1596) == ALIAS
     assert _call(name, d, live=C, ) == ALIAS
     assert _call(name, d, share=D + 64) == ALIAS
     assert _call(name, d, loss=E) == ALIAS
-    assert _call(name, d, scratch=A) == ALIAS
 
 
 def test_route_grad_refusals():
@@ -125,7 +131,8 @@ def test_verify_refusals(name):
 
 def test_accumulate_refusals():
     d = dict(scores=A, batch=2, heads=3, capacity=100, sb=300, sh=100, weights=B, dtype=1, group=4, queries=2,
-             length=90, wb=12 * 180, wh=180, wq=90, lengths=C, fresh=1, decay=1.0, stream=None)
+             length=90, wb=12 * 180, wh=180, wq=90, lengths=C, fresh=1, decay=1.0,
+             scratch=S, sbytes=1 << 24, stream=None)
     name = "ssc_accumulate_weights"
     assert _call(name, d, batch=-1) == ARG
     assert _call(name, d, heads=0) == ARG
@@ -147,6 +154,12 @@ def test_accumulate_refusals():
     assert _call(name, d, weights=B + 1) == ARG
     assert _call(name, d, weights=A + 2396) == ALIAS
     assert _call(name, d, lengths=A) == ALIAS
+    many = dict(d, queries=100, wh=9000, wb=12 * 9000)
+    assert _call(name, many, scratch=None) == SCRATCH
+    assert _call(name, many, scratch=S + 8) == SCRATCH
+    assert _call(name, many, sbytes=ssc.accumulate_scratch_bytes(2, 3, 4, 100, 90, torch.bfloat16) - 1) == SCRATCH
+    assert _call(name, many, scratch=A + 16) == ALIAS
+    assert _call(name, many, scratch=B) == ALIAS
 
 
 def test_evict_refusals():
@@ -177,7 +190,7 @@ def test_evict_refusals():
 
 def test_move_refusals():
     d = dict(cache=A, es=2, batch=2, heads=3, capacity=100, width=16, cb=4800, ch=1600, cr=16, kept=B, keep=50, out=C,
-             ob=2400, oh=800, orow=16, stream=None)
+             ob=2400, oh=800, orow=16, scratch=None, sbytes=0, stream=None)
     name = "ssc_move_rows"
     for es in (0, 3, 16):
         assert _call(name, d, es=es) == ARG
@@ -198,6 +211,17 @@ def test_move_refusals():
     # in place the whole cache is written to
     place = dict(d, out=A, ob=4800, oh=1600)
     assert _call(name, place, kept=A + 2 * 9600 - 4) == ALIAS
+    # few long heads go by way of scratch
+    assert ssc.move_scratch_bytes(2, 1, 2, 20_000, 64) == 2 * 20_000 * 128 and ssc.move_scratch_bytes(2, 2, 3, 50, 16) == 0
+    long = dict(place, capacity=40_000, width=64, keep=20_000, ch=40_000 * 64, oh=40_000 * 64, cb=120_000 * 64,
+                ob=120_000 * 64, cr=64, orow=64)
+    need = ssc.move_scratch_bytes(2, 2, 3, 20_000, 64)
+    assert need == 6 * 20_000 * 128
+    assert _call(name, long) == SCRATCH
+    assert _call(name, long, scratch=S + 8, sbytes=need) == SCRATCH
+    assert _call(name, long, scratch=S, sbytes=need - 1) == SCRATCH
+    assert _call(name, long, scratch=A + 64, sbytes=need) == ALIAS
+    assert _call(name, long, scratch=B, sbytes=need) == ALIAS
     # positions before heads, keys beside values: strides that interleave are no overlap of the cache with itself
     assert _call(name, d, cache=A, cb=100 * 96, ch=32, cr=96, out=A + 32, ob=100 * 96, oh=32, orow=96) == ALIAS
 
