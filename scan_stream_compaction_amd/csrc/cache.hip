@@ -65,9 +65,10 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     Score before[kN / 4];
     const bool vector = first + kN <= len && first + kN <= old && w == 0 && a.splits == 1;
 #pragma unroll
-    for (int i = 0; i < kN / 4; ++i) {
-        before[i] = Score{0.0f, 0.0f, 0.0f, 0.0f};
-        if (vector) before[i] = *reinterpret_cast<const ScoreAny *>(to + 4 * i);
+    for (int i = 0; i < kN / 4; ++i) before[i] = Score{0.0f, 0.0f, 0.0f, 0.0f};
+    if (vector) {
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) before[i] = *reinterpret_cast<const ScoreAny *>(to + 4 * i);
     }
     float sum[kN];
 #pragma unroll
@@ -95,6 +96,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 raw[j] = __builtin_nontemporal_load(reinterpret_cast<const RawAny *>(row(r + j * WAVES)));
+            __builtin_amdgcn_sched_barrier(0);  // all of them first: left alone, one waits for another
 #pragma unroll
             for (int j = 0; j < C; ++j) add(__builtin_bit_cast(V, raw[j]));
             r += C * WAVES;
@@ -631,23 +633,30 @@ __global__ __launch_bounds__(kMoveBlock) void move_kernel(MoveArgs a) {
     const int32_t *kept = a.kept + bh * a.keep;
     const int rows = kMoveBlock >> a.lg;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * rows * kMoveFlight + (threadIdx.x >> a.lg);
-    int64_t pos[kMoveFlight];
+    // no load waits behind a branch: a slot without a row reads row 0
+    int32_t k[kMoveFlight];
 #pragma unroll
     for (int j = 0; j < kMoveFlight; ++j) {
         const int64_t s = first + j * rows;
-        const int32_t k = s < a.keep ? kept[s] : -1;
-        const bool moves = k >= 0 && k < a.capacity && (a.moved == 0 || k > s);
-        pos[j] = moves ? (a.moved == 2 ? s : k) : -1;
+        k[j] = kept[s < a.keep ? s : a.keep - 1];
+    }
+    bool moves[kMoveFlight];
+    const char *src[kMoveFlight];
+#pragma unroll
+    for (int j = 0; j < kMoveFlight; ++j) {
+        const int64_t s = first + j * rows;
+        moves[j] = s < a.keep && k[j] >= 0 && k[j] < a.capacity && (a.moved == 0 || k[j] > s);
+        src[j] = from + (moves[j] ? (a.moved == 2 ? s : k[j]) : 0) * a.from_row;
     }
     for (int c = static_cast<int>(threadIdx.x) & ((1 << a.lg) - 1); c < a.chunks; c += 1 << a.lg) {
         const int at = piece_at<BYTES>(a, c);
         typename P::V v[kMoveFlight];
 #pragma unroll
-        for (int j = 0; j < kMoveFlight; ++j)
-            if (pos[j] >= 0) v[j] = P::load_stream(from + pos[j] * a.from_row + at);
+        for (int j = 0; j < kMoveFlight; ++j) v[j] = P::load_stream(src[j] + at);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < kMoveFlight; ++j)
-            if (pos[j] >= 0) P::store_stream(to + (first + j * rows) * a.to_row + at, v[j]);
+            if (moves[j]) P::store_stream(to + (first + j * rows) * a.to_row + at, v[j]);
     }
 }
 
@@ -669,20 +678,26 @@ __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) 
     // that lies before its slot is none of evict_rows
     int32_t pos[kPlaceFlight], next[kPlaceFlight];
     const auto positions = [&](int64_t set, int32_t(&p)[kPlaceFlight]) {
+        int32_t k[kPlaceFlight];
 #pragma unroll
         for (int j = 0; j < kPlaceFlight; ++j) {
             const int64_t s = set + (threadIdx.x >> a.lg) + j * rows;
-            const int32_t k = kept[s < a.keep ? s : a.keep - 1];
-            p[j] = s < a.keep && k < a.capacity && k > s ? k : -1;
+            k[j] = kept[s < a.keep ? s : a.keep - 1];
+        }
+#pragma unroll
+        for (int j = 0; j < kPlaceFlight; ++j) {
+            const int64_t s = set + (threadIdx.x >> a.lg) + j * rows;
+            p[j] = s < a.keep && k[j] < a.capacity && k[j] > s ? k[j] : -1;
         }
     };
+    // no load waits behind a branch: a slot without a row reads row 0
     typename P::V v[kPlaceFlight];
     const auto load = [&](int base, const int32_t(&p)[kPlaceFlight]) {
         const int c = base + lane_col;
         const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
 #pragma unroll
         for (int j = 0; j < kPlaceFlight; ++j)
-            if (p[j] >= 0 && c < c1) v[j] = P::load_stream(rows_at + static_cast<int64_t>(p[j]) * a.to_row + at);
+            v[j] = P::load_stream(rows_at + static_cast<int64_t>(p[j] >= 0 ? p[j] : 0) * a.to_row + at);
     };
     positions(0, pos);
     load(c0, pos);
