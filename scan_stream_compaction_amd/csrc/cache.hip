@@ -20,6 +20,13 @@ namespace {
 // A lane holds 16 bytes of columns of the weights and adds up its rows (the
 // queries of the heads that share a cache head), sixteen in flight; the
 // wavefronts of a workgroup take every WAVES-th row and are joined in LDS.
+//
+// Rows that start anywhere are read by aligned loads and shifted into place in
+// registers: a lane's piece ends in the next lane's load, so the last lane only
+// reads. The loads stay inside the 16 bytes that hold a row's first and last
+// element. 4 x 8 heads, 128 rows of 10,007 fp16: 18.8 us so, 23.7 by 16-byte loads
+// from any address; of 10,240, where every row starts at such bytes: 16.5 without
+// the shift, 19.5 with it.
 struct AccumulateArgs {
     float *scores;
     int64_t score_batch, score_head;
@@ -35,14 +42,18 @@ struct AccumulateArgs {
     float *part;  // [splits][batch][heads][length]
 };
 
+// Lanes of a wavefront that hold columns; SHIFT: rows that do not all start at a
+// multiple of 16 bytes.
+template <bool SHIFT>
+constexpr int kColumnLanes = SHIFT ? kWave - 1 : kWave;
+
 // EVEN: the rows of a cache head lie evenly apart (queries of one head)
-template <class T, int WAVES, bool EVEN>
+template <class T, int WAVES, bool EVEN, bool SHIFT>
 __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs a) {
     constexpr int kN = 16 / static_cast<int>(sizeof(T));
     constexpr int kFlight = 16;
     typedef T V __attribute__((ext_vector_type(kN)));
     typedef uint32_t Raw __attribute__((ext_vector_type(4)));
-    typedef uint32_t RawAny __attribute__((ext_vector_type(4), aligned(2), may_alias));
     typedef float Score __attribute__((ext_vector_type(4)));
     typedef float ScoreAny __attribute__((ext_vector_type(4), aligned(4), may_alias));
     __shared__ float s_sum[WAVES > 1 ? WAVES - 1 : 1][WAVES > 1 ? kWave * kN : 1];
@@ -50,20 +61,20 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     const int w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int lane = lane_id();
     const uint32_t split = blockIdx.x / a.col_blocks;
-    const int64_t first = static_cast<int64_t>(blockIdx.x - split * a.col_blocks) * kWave * kN + lane * kN;
-    const T *from = static_cast<const T *>(a.weights) + b * a.weight_batch + h * a.weight_group + first;
+    const int64_t block_first = static_cast<int64_t>(blockIdx.x - split * a.col_blocks) * (kColumnLanes<SHIFT> * kN);
+    const int64_t first = block_first + lane * kN;
     float *to = a.scores + b * a.score_batch + h * a.score_head + first;
     int64_t len = a.length;
     if (a.lengths != nullptr) {
         const int64_t l = a.lengths[b];
         len = l < len ? l : len;
     }
-    if (first - lane * kN >= len) return;
-    const bool whole = first + kN <= a.length;
+    if (block_first >= len) return;
     // the earlier scores are on their way while the weights are read
     const int64_t old = len - a.fresh;  // positions with an earlier score
     Score before[kN / 4];
-    const bool vector = first + kN <= len && first + kN <= old && w == 0 && a.splits == 1;
+    const bool mine = w == 0 && lane < kColumnLanes<SHIFT>;
+    const bool vector = first + kN <= len && first + kN <= old && mine && a.splits == 1;
 #pragma unroll
     for (int i = 0; i < kN / 4; ++i) before[i] = Score{0.0f, 0.0f, 0.0f, 0.0f};
     if (vector) {
@@ -76,44 +87,60 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     const uint32_t all = a.group * a.queries, share = (all + a.splits - 1) / a.splits;
     const uint32_t begin = split * share < all ? split * share : all;  // the last parts may be empty
     const uint32_t rows = all - begin < share ? all : begin + share;
-    // a weight that is no number (of a query whose mask left nothing) adds nothing
-    const auto add = [&](const V &v) {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const float x = static_cast<float>(v[e]);
-            sum[e] += x == x ? x : 0.0f;
-        }
-    };
+    // the row at the workgroup's first column, the same in all lanes
+    const T *from = static_cast<const T *>(a.weights) + b * a.weight_batch + h * a.weight_group + block_first;
     const auto row = [&](uint32_t r) {
         if constexpr (EVEN) return from + r * a.weight_query;
         return from + (r / a.queries) * a.weight_head + (r % a.queries) * a.weight_query;
     };
-    if (whole) {
-        uint32_t r = begin + w;
-        const auto some = [&](auto count) {
-            constexpr int C = decltype(count)::value;
-            Raw raw[C];
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-                raw[j] = __builtin_nontemporal_load(reinterpret_cast<const RawAny *>(row(r + j * WAVES)));
-            __builtin_amdgcn_sched_barrier(0);  // all of them first: left alone, one waits for another
-#pragma unroll
-            for (int j = 0; j < C; ++j) add(__builtin_bit_cast(V, raw[j]));
-            r += C * WAVES;
-        };
-        while (r + (kFlight - 1) * WAVES < rows) some(std::integral_constant<int, kFlight>{});
-        if (r + 7 * WAVES < rows) some(std::integral_constant<int, 8>{});
-        if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
-        while (r < rows) some(std::integral_constant<int, 1>{});
-    } else if (first < a.length) {
-        for (uint32_t r = begin + w; r < rows; r += WAVES) {
-            const T *p = row(r);
-            V v;
-#pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = first + e < a.length ? p[e] : static_cast<T>(0.0f);
-            add(v);
+    // bytes of a row's first load before that column
+    const auto skip_of = [](const T *p) {
+        return SHIFT ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u : 0u;
+    };
+    const uint64_t left = static_cast<uint64_t>(a.length - block_first) * sizeof(T) - 1;  // to the row's last byte
+    const uint32_t last = left < 65536 ? static_cast<uint32_t>(left) : 65536u;
+    const auto load = [&](const T *p) {
+        const uint32_t skip = skip_of(p), most = (last + skip) & ~15u, at = 16u * lane;
+        return __builtin_nontemporal_load(
+            reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(p) - skip + (at < most ? at : most)));
+    };
+    // a weight that is no number (of a query whose mask left nothing) adds nothing
+    const auto add = [&](Raw raw, uint32_t skip) {
+        if (skip != 0) {  // the same in all lanes
+            const uint32_t two = skip & 8u ? ~0u : 0u, one = skip & 4u ? ~0u : 0u;
+            const auto pick = [](uint32_t mask, uint32_t x, uint32_t y) { return (x & ~mask) | (y & mask); };
+            const uint32_t x0 = raw[0], x1 = raw[1], x2 = raw[2], x3 = raw[3];
+            const uint32_t x4 = dpp_move<0x130, 0xf>(x0), x5 = dpp_move<0x130, 0xf>(x1);  // of the next lane
+            const uint32_t x6 = dpp_move<0x130, 0xf>(x2), x7 = dpp_move<0x130, 0xf>(x3);
+            const uint32_t y0 = pick(two, x0, x2), y1 = pick(two, x1, x3), y2 = pick(two, x2, x4);
+            const uint32_t y3 = pick(two, x3, x5), y4 = pick(two, x4, x6), y5 = pick(two, x5, x7);
+            const uint32_t z0 = pick(one, y0, y1), z1 = pick(one, y1, y2), z2 = pick(one, y2, y3);
+            const uint32_t z3 = pick(one, y3, y4), z4 = pick(one, y4, y5);
+            raw = Raw{__builtin_amdgcn_alignbyte(z1, z0, skip & 3u), __builtin_amdgcn_alignbyte(z2, z1, skip & 3u),
+                      __builtin_amdgcn_alignbyte(z3, z2, skip & 3u), __builtin_amdgcn_alignbyte(z4, z3, skip & 3u)};
         }
-    }
+        const V v = __builtin_bit_cast(V, raw);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const float y = static_cast<float>(v[e]);
+            sum[e] += y == y ? y : 0.0f;
+        }
+    };
+    uint32_t r = begin + w;
+    const auto some = [&](auto count) {
+        constexpr int C = decltype(count)::value;
+        Raw raw[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) raw[j] = load(row(r + j * WAVES));
+        __builtin_amdgcn_sched_barrier(0);  // all of them first: left alone, one waits for another
+#pragma unroll
+        for (int j = 0; j < C; ++j) add(raw[j], skip_of(row(r + j * WAVES)));
+        r += C * WAVES;
+    };
+    while (r + (kFlight - 1) * WAVES < rows) some(std::integral_constant<int, kFlight>{});
+    if (r + 7 * WAVES < rows) some(std::integral_constant<int, 8>{});
+    if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
+    while (r < rows) some(std::integral_constant<int, 1>{});
     if constexpr (WAVES > 1) {
         if (w > 0) {
 #pragma unroll
@@ -130,7 +157,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
         float *part = a.part + ((static_cast<int64_t>(split) * gridDim.z + b) * gridDim.y + h) * a.length + first;
 #pragma unroll
         for (int e = 0; e < kN; ++e)
-            if (first + e < len) part[e] = sum[e];
+            if (mine && first + e < len) part[e] = sum[e];
     } else if (vector) {
 #pragma unroll
         for (int i = 0; i < kN / 4; ++i) {
@@ -143,7 +170,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
             const int64_t i = first + e;
-            if (i < len) to[e] = i < old ? __builtin_fmaf(to[e], a.decay, sum[e]) : sum[e];
+            if (mine && i < len) to[e] = i < old ? __builtin_fmaf(to[e], a.decay, sum[e]) : sum[e];
         }
     }
 }
@@ -730,20 +757,20 @@ int check_cache(int64_t batch, int64_t heads, int64_t capacity) {
     return SSC_OK;
 }
 
-// Workgroups of 64 lanes' columns; and where the wavefronts of these are few
+// Where the wavefronts are few
 // (under 2048) and have over 16 rows each, the rows in parts, up to 4096 wavefronts
-// in all. Two heads of 4 sequences, 456 rows of 1390 fp16: 36 us in one part.
+// in all. Two heads of 4 sequences, 456 rows of 1390 fp16: 39 us a call in one part,
+// 12 in four.
 struct AccumulatePlan {
-    uint32_t splits, col_blocks;
+    uint32_t splits;
     size_t bytes;
 };
 
 AccumulatePlan accumulate_plan(int64_t heads, int64_t rows, int64_t length, int dtype) {
     AccumulatePlan p{};
-    const int64_t cols = kWave * 16 / static_cast<int64_t>(elem_bytes(dtype));
-    p.col_blocks = static_cast<uint32_t>((length + cols - 1) / cols);
+    const int64_t cols = kColumnLanes<true> * 16 / static_cast<int64_t>(elem_bytes(dtype));
     p.splits = 1;
-    const int64_t waves = heads * p.col_blocks * 8;
+    const int64_t waves = heads * ((length + cols - 1) / cols) * 8;
     if (waves > 0 && waves < 2048 && rows > 128) {
         const int64_t wanted = (4096 + waves - 1) / waves, most = (rows + 127) / 128;
         p.splits = static_cast<uint32_t>(wanted < most ? wanted : most);
@@ -885,24 +912,31 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
     const bool even = group == 1 || queries <= 1 || weight_head == queries * weight_query;
     const int64_t rows = group * queries;
     a.splits = p.splits;
-    a.col_blocks = p.col_blocks;
     a.part = static_cast<float *>(scratch);
+    const int64_t es = static_cast<int64_t>(elem_bytes(dtype));
+    const bool shift = !aligned(weights, 16) || (batch > 1 && weight_batch * es % 16 != 0) ||
+                       (heads * group > 1 && weight_head * es % 16 != 0) || (queries > 1 && weight_query * es % 16 != 0);
+    const int64_t cols = (shift ? kColumnLanes<true> : kColumnLanes<false>)*16 / es;
+    a.col_blocks = static_cast<uint32_t>((length + cols - 1) / cols);
     SSC_TRY(with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        const dim3 grid(p.splits * p.col_blocks, static_cast<unsigned>(heads), static_cast<unsigned>(batch));
-        const auto launch = [&](auto waves) {
+        const dim3 grid(p.splits * a.col_blocks, static_cast<unsigned>(heads), static_cast<unsigned>(batch));
+        const auto launch = [&](auto waves, auto e, auto sh) {
             constexpr int W = decltype(waves)::value;
-            if (even)
-                hipLaunchKernelGGL((accumulate_kernel<T, W, true>), grid, dim3(W * kWave), 0,
-                                   static_cast<hipStream_t>(stream), a);
-            else
-                hipLaunchKernelGGL((accumulate_kernel<T, W, false>), grid, dim3(W * kWave), 0,
-                                   static_cast<hipStream_t>(stream), a);
+            hipLaunchKernelGGL((accumulate_kernel<T, W, decltype(e)::value, decltype(sh)::value>), grid,
+                               dim3(W * kWave), 0, static_cast<hipStream_t>(stream), a);
             return launched();
         };
-        if (rows <= 16) return launch(std::integral_constant<int, 1>{});
-        if (rows <= 64) return launch(std::integral_constant<int, 4>{});
-        return launch(std::integral_constant<int, 8>{});
+        const auto shaped = [&](auto waves) {
+            if (even)
+                return shift ? launch(waves, std::true_type{}, std::true_type{})
+                             : launch(waves, std::true_type{}, std::false_type{});
+            return shift ? launch(waves, std::false_type{}, std::true_type{})
+                         : launch(waves, std::false_type{}, std::false_type{});
+        };
+        if (rows <= 16) return shaped(std::integral_constant<int, 1>{});
+        if (rows <= 64) return shaped(std::integral_constant<int, 4>{});
+        return shaped(std::integral_constant<int, 8>{});
     }));
     if (p.splits == 1) return SSC_OK;
     hipLaunchKernelGGL(accumulate_join_kernel,

@@ -87,6 +87,23 @@ def test_accumulate_masked_places_and_fresh_scores(dtype):
     check_accumulate(got2[:1], w[:1], lengths[:1], fresh=0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_accumulate_rows_that_start_anywhere(dtype):
+    """Each start within 16 bytes and lengths around a wavefront's columns; guard
+    values that no sum may take lie on both sides of every row."""
+    g = gen(5)
+    per = 16 // torch.empty(0, dtype=dtype).element_size()
+    for start in range(per + 1):
+        for length in (1, per - 1, per, per + 1, 63 * per - 1, 63 * per, 63 * per + 1, 64 * per, 2 * 63 * per + 3):
+            for apart in (0, 1):
+                full = torch.full((1, 6, 3, length + start + 5 + apart), 1e4, device=DEV).to(dtype)
+                w = full[:, :, :, start:start + length]
+                w.copy_(torch.rand(w.shape, device=DEV, generator=g))
+                s = torch.rand(1, 2, length, device=DEV, generator=g)
+                check_accumulate(s.clone(), w)
+                check_accumulate(s.clone(), w.transpose(1, 2).contiguous().transpose(1, 2))
+
+
 def test_accumulate_strides():
     """Weights of (batch, queries, heads, length), scores as every second head of a buffer."""
     g = gen(2)
