@@ -588,8 +588,8 @@ int ssc_verify_rows_i64(const void *probs, int dtype, int64_t rows, int64_t draf
  * lengths[b] (nullable: all) is the number of positions in use, held to what there
  * is. */
 
-/* Scratch bytes of ssc_accumulate_weights: sums of the parts that many rows of a
- * few short heads are added up in, 0 otherwise. */
+/* Scratch bytes of ssc_accumulate_weights: sums of the parts that the rows (group *
+ * queries) of a few short heads are added up in; 0 otherwise, and for up to 128 rows. */
 size_t ssc_accumulate_scratch_bytes(int64_t batch, int64_t heads, int64_t group, int64_t queries,
                                     int64_t length, int dtype);
 
