@@ -731,7 +731,10 @@ __global__ __launch_bounds__(kPlaceBlock) void move_in_place_kernel(MoveArgs a) 
     for (int64_t set = 0; set < a.keep; set += step) {
         if (set + step < a.keep) positions(set + step, next);
         for (int base = c0; base < c1; base += 1 << a.lg) {
-            __syncthreads();  // all of this set's pieces have been read
+            // All of this set's pieces have been read: the barrier alone does not wait for
+            // loads under way, and other wavefronts store where they read.
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
             const int c = base + lane_col;
             const int at = piece_at<BYTES>(a, c < c1 ? c : c0);
             const int64_t first = set + (threadIdx.x >> a.lg);

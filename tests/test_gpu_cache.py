@@ -285,6 +285,21 @@ def test_move_in_place_of_each_shape(batch, heads, capacity, keep, width):
         assert torch.equal(ssc.move_rows(cache, k, out=out).cpu(), want)
 
 
+@pytest.mark.parametrize("batch,heads,keep,width", [(1, 3, 40, 64), (2, 4, 700, 128), (64, 8, 8, 9008), (64, 8, 8, 2051)])
+def test_move_each_row_one_place(batch, heads, keep, width):
+    """Each slot is stored where the slot before it is read from, rows of several
+    column passes of a workgroup among them: no store may pass a load."""
+    g = gen(width)
+    cache = torch.randint(-2 ** 15, 2 ** 15, (batch, heads, keep + 1, width), device=DEV, generator=g).short()
+    kept = torch.arange(1, keep + 1, dtype=torch.int32, device=DEV).expand(batch, heads, keep).contiguous()
+    want = cache.clone()
+    want[:, :, :keep] = cache[:, :, 1:]
+    for _ in range(3):
+        c = cache.clone()
+        ssc.move_rows(c, kept)
+        assert torch.equal(c, want)
+
+
 def test_move_strides():
     """Caches of (batch, capacity, heads, width), keys and values in one buffer; the front of the same cache."""
     g = gen(3)
