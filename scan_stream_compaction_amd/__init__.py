@@ -1163,11 +1163,9 @@ def accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, *, lengths: 
     if lengths is not None:
         _exactly(lengths, "lengths", scores, scores.get_device(), torch.int32, batch, "sequence")
     group = count // heads
-    if group * queries > 128:  # fewer rows take no scratch
+    if scratch is not None or group * queries > 128:  # fewer rows take no scratch
         scratch = _work_bytes(scratch, scores,
                               accumulate_scratch_bytes(batch, heads, group, queries, length, weights.dtype))
-    else:
-        scratch = None
     _row_call("ssc_accumulate_weights", scores, scores, batch, heads, capacity, scores.stride(0), scores.stride(1),
               weights, DTYPE[weights.dtype], group, queries, length, weights.stride(0), weights.stride(1),
               weights.stride(2), lengths, min(fresh, capacity), float(decay), scratch, _numel(scratch))

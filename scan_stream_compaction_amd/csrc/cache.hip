@@ -24,9 +24,12 @@ namespace {
 // Rows that start anywhere are read by aligned loads and shifted into place in
 // registers: a lane's piece ends in the next lane's load, so the last lane only
 // reads. The loads stay inside the 16 bytes that hold a row's first and last
-// element. 4 x 8 heads, 128 rows of 10,007 fp16: 18.8 us so, 23.7 by 16-byte loads
+// element. 4 x 8 heads, 128 rows of 10,007 fp16: 18.9 us so, 23.7 by 16-byte loads
 // from any address; of 10,240, where every row starts at such bytes: 16.5 without
 // the shift, 19.5 with it.
+//
+// Bound by HBM: those 10,240 at 5.2 TB/s, 10,007 at 4.5; 32 x 8 heads of 8192, 4
+// rows of bf16, 6.5 us (34 MB, 5.2 TB/s).
 struct AccumulateArgs {
     float *scores;
     int64_t score_batch, score_head;
@@ -207,6 +210,11 @@ __global__ __launch_bounds__(256) void accumulate_join_kernel(AccumulateArgs a) 
 // several workgroups (splits) and three launches: counts by the first digit;
 // these joined, counts by the second and a list of the scores that share the
 // first; those joined, the third digit from the lists, and the output.
+//
+// Bound by latency, of the steps of a workgroup or of three launches: 256 heads of
+// 8192 cut to 4096 9.6 us (10 MB moved, 2 us at a copy's rate), 8 of 131,072 cut to
+// 16,384 4.5 + 7.9 + 9.1 us traced and 16 to 18 a call; by one workgroup a head
+// 168.
 constexpr int kEvictBlock = 1024;
 constexpr int kEvictWaves = kEvictBlock / kWave;
 constexpr int kEvictBins = 2048;
@@ -787,7 +795,7 @@ AccumulatePlan accumulate_plan(int64_t heads, int64_t rows, int64_t length, int 
 // by way of scratch. A workgroup's set of rows takes 4.5 us one after another; the
 // scratch doubles the traffic but has no such order. Rows moved, direct against
 // scratch, us:
-//   2 heads x 20,000 of 128 bytes   84   11      4 heads x 2500 of 1024 bytes   19   13
+//   2 heads x 20,000 of 128 bytes   84  9.5      4 heads x 2500 of 1024 bytes   19   13
 //   8 x 20,000 of 256               88   35      8 x 1024 of 256               5.6  9.8
 //   22 x 4382 of 192                25   18      48 x 4695 of 256               34   46
 //   32 x 2048 of 130                32   14      256 x 4096 of 256             102  188

@@ -11,6 +11,11 @@
 // A row is held by G lanes of a wavefront (8 to 64), N logits each, so that
 // one instruction serves 64 / G tokens and a sum over the row is three to six
 // steps across lanes. The row is read once and stays in registers.
+//
+// Few tokens are bound by the launch: 16 of 8 of 128 bf16 2.6 us. Many by
+// instructions and by HBM: 65,536 tokens, 8 of 128 fp32 with the balance, 17.7 us
+// and 4.3 for the join (34 MB read, 4 written: 7 us at a copy's 5.15 TB/s; 5.9 M
+// vector instructions, 1440 a wavefront for its 16 rows: 9.6 us at 2.4 GHz).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -530,7 +535,8 @@ __global__ __launch_bounds__((kThreads<N, BALANCE>)) void route_kernel(RouteArgs
 }
 
 // The workgroups' sums joined, in fp64: 16 experts to a workgroup, 64 threads
-// to an expert. The workgroup that is done last adds the loss.
+// to an expert. The workgroup that is done last adds the loss. 256 workgroups of
+// 128 experts: 4.3 us, all of it latency (1 MB read).
 constexpr int kJoinBlock = 1024;
 constexpr int kJoinCols = 16;
 constexpr int kJoinRows = kJoinBlock / kJoinCols;
@@ -605,7 +611,9 @@ static_assert(kExpertsMax / kJoinCols <= kWave, "a lane a workgroup");
 
 // The gradient. What a chosen expert adds is computed by the lane that holds
 // its place among the chosen and handed to the lane that holds its logit
-// through LDS; an id that a row names twice counts twice.
+// through LDS; an id that a row names twice counts twice. 65,536 tokens, 6 of 160
+// bf16: 14.9 us, 25 MB read and 21 written (8.8 us at a copy's rate); with the
+// prologue's loads behind one another and no row on its way ahead 26.9.
 struct RouteGradArgs {
     const void *logits;
     int64_t stride, tokens;

@@ -13,8 +13,11 @@
 // and the token in it by reading it again: in one launch, or in two where few
 // long rows would leave the chip empty. Sums are fp64, in an order that the sizes
 // fix: a border of u that fp32 sums would miss once in some hundred rows (131,072
-// borders, 1e-8 of the sum each) is met. Bound by HBM for many rows (192 of
-// 131,072 bf16, p and q: 20 us a call, 5.0 TB/s), by latency for few.
+// borders, 1e-8 of the sum each) is met. For few rows bound
+// by latency (one of 131,072 fp32, in two launches: 3.5 + 3.6 us). 192 of 131,072
+// bf16 with 4 drafts: 21.4 us for 75 MB, 3.5 TB/s where a copy reaches 5.15: a row
+// whose drafts all stand reads p alone, another p and q, and one workgroup has
+// either; in two launches, with the segments spread evenly, 17.9 + 4.2.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

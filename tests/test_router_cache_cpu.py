@@ -38,6 +38,9 @@ def test_scratch_sizes():
     assert ssc.accumulate_scratch_bytes(1, 1, 4, 10_000, 90, torch.float32) == 313 * 90 * 4
     assert ssc.accumulate_scratch_bytes(8, 8, 4, 10_000, 1025, torch.bfloat16) == 3 * 64 * 1025 * 4
     assert ssc.accumulate_scratch_bytes(8, 8, 4, 32, 90, torch.bfloat16) == ssc.accumulate_scratch_bytes(32, 8, 8, 100, 90, torch.float16) == 0
+    # up to 128 rows take none, however few the heads
+    assert ssc.accumulate_scratch_bytes(1, 1, 4, 32, 90, torch.float32) == 0
+    assert ssc.accumulate_scratch_bytes(1, 1, 1, 129, 90, torch.float32) == 2 * 90 * 4
     # two tables of 2048 counts a split, a threshold a head, two numbers a split, a list of its positions
     assert ssc.evict_scratch_bytes(1, 8, 16_384) == ssc.evict_scratch_bytes(40, 8, 32_768) == 0
     assert ssc.evict_scratch_bytes(1, 8, 131_072) == 8 * 16 * (16_384 + 8 + 4 * 8192) + 8 * 16
