@@ -1222,16 +1222,16 @@ def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | No
         raise ValueError("kept is (batch, heads, keep)")
     keep = kept.size(2)
     to = cache
-    if out is None or out.data_ptr() == cache.data_ptr():
-        scratch = _work_bytes(scratch, cache, move_scratch_bytes(cache.element_size(), batch, heads, keep, width))
-    else:
-        scratch = None
     if out is not None:
         to = _view(out, "out", 4, (cache.dtype,), cache)
         if out.size(0) != batch or out.size(1) != heads or out.size(3) != width or out.size(2) < keep:
             raise ValueError("out is (batch, heads, at least keep, width)")
         if out.size(2) != keep:
             out = out[:, :, :keep]
+    place = to.data_ptr() == cache.data_ptr()
+    if place or scratch is not None:  # a move to another cache takes none
+        scratch = _work_bytes(scratch, cache, move_scratch_bytes(cache.element_size(), batch, heads, keep, width)
+                              if place else 0)
     _row_call("ssc_move_rows", cache, cache, cache.element_size(), batch, heads, capacity, width, cache.stride(0),
               cache.stride(1), cache.stride(2), kept, keep, to, to.stride(0), to.stride(1), to.stride(2),
               scratch, _numel(scratch))

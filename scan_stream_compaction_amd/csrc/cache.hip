@@ -213,8 +213,8 @@ __global__ __launch_bounds__(256) void accumulate_join_kernel(AccumulateArgs a) 
 //
 // Bound by latency, of the steps of a workgroup or of three launches: 256 heads of
 // 8192 cut to 4096 9.6 us (10 MB moved, 2 us at a copy's rate), 8 of 131,072 cut to
-// 16,384 4.5 + 7.9 + 9.1 us traced and 16 to 18 a call; by one workgroup a head
-// 168.
+// 16,384 4.5 + 7.9 + 9.1 us traced and 16 to 20 a call, as their lengths fall; by one
+// workgroup a head 168.
 constexpr int kEvictBlock = 1024;
 constexpr int kEvictWaves = kEvictBlock / kWave;
 constexpr int kEvictBins = 2048;

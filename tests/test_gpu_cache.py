@@ -419,3 +419,84 @@ def test_graph_replays_and_streams():
         now = [x.clone() for x in got]
         want = step(other)
         assert torch.equal(s, other) and all(torch.equal(a, b) for a, b in zip(now, want))
+
+
+def test_refusals_of_arguments():
+    cache, kept = torch.zeros(1, 2, 8, 4, device=DEV), torch.zeros(1, 2, 3, dtype=torch.int32, device=DEV)
+    for out in ([1.0], 3):
+        with pytest.raises(TypeError, match="out must be a torch tensor"):
+            ssc.move_rows(cache, kept, out=out)
+    with pytest.raises(ValueError, match="at least keep"):
+        ssc.move_rows(cache, kept, out=torch.zeros(1, 2, 2, 4, device=DEV))
+    with pytest.raises(ssc.SSCError):  # another layout of the same memory
+        ssc.move_rows(cache, kept, out=cache.as_strided((1, 2, 8, 4), (64, 4, 8, 1)))
+    # a scratch is checked also where none is needed
+    scores, weights = torch.zeros(1, 2, 8, device=DEV), torch.zeros(1, 2, 1, 8, device=DEV)
+    wrong = torch.zeros(64, device=DEV)
+    for call in (lambda: ssc.accumulate_weights(scores, weights, scratch=wrong),
+                 lambda: ssc.move_rows(cache, kept, scratch=wrong),
+                 lambda: ssc.move_rows(cache, kept, out=cache.clone(), scratch=wrong),
+                 lambda: ssc.evict_rows(scores, 2, scratch=wrong)):
+        with pytest.raises(TypeError, match="scratch"):
+            call()
+    none = torch.zeros(0, dtype=torch.uint8, device=DEV)
+    ssc.move_rows(cache, kept, out=cache.clone(), scratch=none)
+    ssc.accumulate_weights(scores, weights, scratch=none)
+
+
+def _long_step(s, w, cache):
+    """The forms that go by way of scratch: rows in parts, heads in splits, moves in place."""
+    ssc.accumulate_weights(s, w, fresh=3)
+    kept, counts = ssc.evict_rows(s, 9000, first=4, recent=100)
+    ssc.move_rows(cache, kept)
+    return kept, counts
+
+
+def _long_inputs(g):
+    return (torch.rand(1, 2, 20_000, device=DEV, generator=g), torch.rand(1, 4, 100, 20_000, device=DEV, generator=g).half(),
+            torch.randn(1, 2, 20_000, 64, device=DEV, generator=g).to(torch.bfloat16))
+
+
+def test_the_forms_with_scratch_in_a_graph():
+    g = gen(31)
+    s, w, cache = _long_inputs(g)
+    assert ssc.accumulate_scratch_bytes(1, 2, 2, 100, 20_000, torch.float16) > 0
+    assert ssc.evict_scratch_bytes(1, 2, 20_000) > 0 and ssc.move_scratch_bytes(2, 1, 2, 9000, 64) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _long_step(s.clone(), w, cache.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _long_step(s, w, cache)
+    for _ in range(4):
+        w.copy_(torch.rand(w.shape, device=DEV, generator=g))
+        cache.copy_(torch.randn(cache.shape, device=DEV, generator=g))
+        other, moved = s.clone(), cache.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        now = [x.clone() for x in got]
+        want = _long_step(other, w, moved)
+        assert torch.equal(s, other) and torch.equal(cache, moved)
+        assert all(torch.equal(a, b) for a, b in zip(now, want))
+
+
+def test_two_calls_at_once():
+    g = gen(32)
+    sets = [_long_inputs(g) for _ in range(2)]
+    want = []
+    for s, w, cache in sets:
+        s, cache = s.clone(), cache.clone()
+        want.append((*_long_step(s, w, cache), s, cache))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        copies = [(s.clone(), w, cache.clone()) for s, w, cache in sets]
+        torch.cuda.synchronize()
+        for stream, (s, w, cache) in zip(streams, copies):
+            with torch.cuda.stream(stream):
+                got.append((*_long_step(s, w, cache), s, cache))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
