@@ -599,7 +599,9 @@ size_t ssc_accumulate_scratch_bytes(int64_t batch, int64_t heads, int64_t group,
  * over the heads g in [h * group, (h + 1) * group) and all queries. Of the last
  * `fresh` of these positions (new ones) the score is not read but taken as 0.
  * Positions past them are left as they were. A weight of NaN adds nothing. weights
- * is batch x (heads * group) x queries x length, length <= capacity. */
+ * is batch x (heads * group) x queries x length, length <= capacity. Each score is
+ * within 26 half steps of fp32 (2^-24 of the sum of the magnitudes that it is made
+ * of), for any number of rows (group * queries, up to 2^30). */
 int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t capacity,
                            int64_t score_stride_batch, int64_t score_stride_head, const void *weights,
                            int dtype, int64_t group, int64_t queries, int64_t length,

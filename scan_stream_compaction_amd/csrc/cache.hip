@@ -21,6 +21,12 @@ namespace {
 // queries of the heads that share a cache head), sixteen in flight; the
 // wavefronts of a workgroup take every WAVES-th row and are joined in LDS.
 //
+// Only the sixteen (or the last fifteen) are added up in fp32; what a wavefront of
+// more has is held in fp64 and rounded once, so that a sum is off by 25 half steps
+// of the magnitudes' at most (15, one rounding, 7 over the wavefronts, one over the
+// parts, one for the earlier score), for any number of rows: 262,144 rows of one
+// weight, in one chain a wavefront, were off by up to 3000.
+//
 // Rows that start anywhere are read by aligned loads and shifted into place in
 // registers: a lane's piece ends in the next lane's load, so the last lane only
 // reads. The loads stay inside the 16 bytes that hold a row's first and last
@@ -49,6 +55,9 @@ struct AccumulateArgs {
 // multiple of 16 bytes.
 template <bool SHIFT>
 constexpr int kColumnLanes = SHIFT ? kWave - 1 : kWave;
+
+// Workgroups of up to this many wavefronts have up to sixteen rows for each.
+constexpr int kFewWaves = 4;
 
 // EVEN: the rows of a cache head lie evenly apart (queries of one head)
 template <class T, int WAVES, bool EVEN, bool SHIFT>
@@ -129,6 +138,9 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
             sum[e] += y == y ? y : 0.0f;
         }
     };
+    double total[WAVES > kFewWaves ? kN : 1];  // of the wavefront's rows before those in `sum`
+#pragma unroll
+    for (double &t : total) t = 0.0;
     uint32_t r = begin + w;
     const auto some = [&](auto count) {
         constexpr int C = decltype(count)::value;
@@ -140,10 +152,23 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
         for (int j = 0; j < C; ++j) add(raw[j], skip_of(row(r + j * WAVES)));
         r += C * WAVES;
     };
-    while (r + (kFlight - 1) * WAVES < rows) some(std::integral_constant<int, kFlight>{});
+    while (r + (kFlight - 1) * WAVES < rows) {
+        some(std::integral_constant<int, kFlight>{});
+        if constexpr (WAVES > kFewWaves) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                total[e] += static_cast<double>(sum[e]);
+                sum[e] = 0.0f;
+            }
+        }
+    }
     if (r + 7 * WAVES < rows) some(std::integral_constant<int, 8>{});
     if (r + 3 * WAVES < rows) some(std::integral_constant<int, 4>{});
     while (r < rows) some(std::integral_constant<int, 1>{});
+    if constexpr (WAVES > kFewWaves) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) sum[e] = static_cast<float>(total[e] + static_cast<double>(sum[e]));
+    }
     if constexpr (WAVES > 1) {
         if (w > 0) {
 #pragma unroll
@@ -178,7 +203,7 @@ __global__ __launch_bounds__(WAVES *kWave) void accumulate_kernel(AccumulateArgs
     }
 }
 
-// The parts' sums joined, in their order.
+// The parts' sums joined, in their order, in fp64.
 __global__ __launch_bounds__(256) void accumulate_join_kernel(AccumulateArgs a) {
     const int64_t h = blockIdx.y, b = blockIdx.z;
     int64_t len = a.length;
@@ -192,9 +217,10 @@ __global__ __launch_bounds__(256) void accumulate_join_kernel(AccumulateArgs a) 
     const float old = i < len - a.fresh ? *to : 0.0f;
     const int64_t step = static_cast<int64_t>(gridDim.z) * gridDim.y * a.length;
     const float *part = a.part + (b * gridDim.y + h) * a.length + i;
-    float sum = 0.0f;
+    double all = 0.0;
 #pragma unroll 8
-    for (uint32_t s = 0; s < a.splits; ++s) sum += part[s * step];
+    for (uint32_t s = 0; s < a.splits; ++s) all += static_cast<double>(part[s * step]);
+    const float sum = static_cast<float>(all);
     *to = i < len - a.fresh ? __builtin_fmaf(old, a.decay, sum) : sum;
 }
 
@@ -950,7 +976,7 @@ int ssc_accumulate_weights(float *scores, int64_t batch, int64_t heads, int64_t 
                          : launch(waves, std::false_type{}, std::false_type{});
         };
         if (rows <= 16) return shaped(std::integral_constant<int, 1>{});
-        if (rows <= 64) return shaped(std::integral_constant<int, 4>{});
+        if (rows <= 16 * kFewWaves) return shaped(std::integral_constant<int, kFewWaves>{});
         return shaped(std::integral_constant<int, 8>{});
     }));
     if (p.splits == 1) return SSC_OK;

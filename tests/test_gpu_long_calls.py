@@ -1,0 +1,92 @@
+"""Calls large enough that a lane takes further batches of rows."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import scan_stream_compaction_amd as ssc
+from tests import test_gpu_cache as cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+STEP = 2.0 ** -24  # half a step of fp32
+
+
+# ---- accumulate_weights: sums over many rows ----
+#
+# Sixteen rows at most are added up in fp32, 15 roundings; such sums are added in
+# fp64 and rounded once a wavefront; eight wavefronts are joined by 7 additions, parts
+# in fp64 and one rounding, and the earlier score by one: 25 half steps of the sum of
+# the magnitudes at most, and under one for the additions in fp64, for any number of rows.
+ACCUMULATE_STEPS = 26
+
+
+def check_sums(scores, weights, added, size, decay=1.0):
+    """scores' new values against old * decay + added, both given in 64 bits."""
+    want = scores.double().cpu() * float(np.float32(decay)) + added
+    bound = ACCUMULATE_STEPS * STEP * (scores.double().abs().cpu() * abs(decay) + size)
+    got = ssc.accumulate_weights(scores.clone(), weights, decay=decay).double().cpu()
+    err = (got - want).abs()
+    assert bool((err <= bound).all()), float((err / bound.clamp(min=1e-300)).max())
+
+
+@pytest.mark.parametrize("value", [0.1, 1.0 / 3.0, 0.7])
+def test_accumulate_one_weight_added_often(value):
+    """Roundings of equal additions all go one way: 262,144 of one weight, so many heads that their rows are in one part."""
+    heads, group, queries = 256, 8, 32_768
+    assert ssc.accumulate_scratch_bytes(1, heads, group, queries, 3, torch.float32) == 0
+    weights = torch.full((1, 1, 1, 3), value, device=DEV).expand(1, heads * group, queries, 3)
+    scores = torch.rand(1, heads, 3, device=DEV, generator=cache.gen(1))
+    total = float(np.float32(value)) * group * queries
+    check_sums(scores, weights, total, total)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,heads,group,queries,length", [
+    (64, 4, 1, 129, 5), (32, 8, 3, 700, 3), (16, 16, 1, 2063, 9), (1, 1, 1, 65_600, 9), (2, 1, 8, 57, 1390), (1, 2, 2, 3000, 33)])
+def test_accumulate_many_rows(batch, heads, group, queries, length, dtype):
+    g = cache.gen(queries)
+    weights = torch.rand(batch, heads * group, queries, length, device=DEV, generator=g).to(dtype)
+    scores = torch.rand(batch, heads, length, device=DEV, generator=g)
+    added = weights.double().view(batch, heads, group * queries, length).sum(2).cpu()
+    check_sums(scores, weights, added, added)
+    check_sums(scores, weights, added, added, decay=0.9)
+    weights = weights - 0.5  # of both signs
+    grouped = weights.double().view(batch, heads, group * queries, length)
+    check_sums(scores, weights, grouped.sum(2).cpu(), grouped.abs().sum(2).cpu())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,heads,group,queries,length", [
+    (1, 1, 1, 1, 5), (2, 3, 4, 16, 1025), (1, 2, 4, 17, 300), (3, 2, 1, 128, 511), (1, 1, 1, 129, 90), (2, 1, 8, 57, 1390),
+    (1, 2, 3, 700, 513), (1, 1, 2, 3000, 33), (1, 1, 1, 65_600, 9), (1, 1, 1, 65_599, 8), (64, 4, 8, 37, 5), (16, 16, 1, 2063, 9)])
+def test_accumulate_each_row_once(batch, heads, group, queries, length, dtype):
+    """Whole weights of 1 to 7, whose sums below 2^24 are exact: a row that is lost or added twice changes every column."""
+    g = cache.gen(queries + length)
+    weights = torch.randint(1, 8, (batch, heads * group, queries, length), device=DEV, generator=g).to(dtype)
+    scores = torch.randint(0, 100, (batch, heads, length), device=DEV, generator=g).float()
+    added = weights.double().view(batch, heads, group * queries, length).sum(2)
+    assert float(added.max()) + 100 < 2 ** 24
+    want = scores.double() + added
+    assert torch.equal(ssc.accumulate_weights(scores, weights).double(), want)
+    # the queries before the heads: rows that lie unevenly apart
+    apart = weights.transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(ssc.accumulate_weights(scores, apart, decay=0.5).double(), 0.5 * want + added)
+
+
+@pytest.mark.parametrize("queries", [40, 300, 5000])
+def test_accumulate_infinities_among_many_rows(queries):
+    """As a sum of plain additions: infinities of one sign give it, of both no number; NaN adds nothing."""
+    inf, nan = float("inf"), float("nan")
+    for heads in (1, 256):
+        weights = torch.rand(1, heads, queries, 4, device=DEV, generator=cache.gen(queries))
+        weights[:, :, queries // 2, 0] = inf
+        weights[:, :, 1, 1] = -inf
+        weights[:, :, [0, queries - 1], 2] = torch.tensor([inf, -inf], device=DEV)
+        weights[:, :, ::3, 3] = nan
+        got = ssc.accumulate_weights(torch.zeros(1, heads, 4, device=DEV), weights)
+        assert bool((got[..., 0] == inf).all()) and bool((got[..., 1] == -inf).all()) and bool(torch.isnan(got[..., 2]).all())
+        want = torch.nan_to_num(weights[..., 3].double(), nan=0.0).sum(2)
+        assert bool(((got[..., 3] - want).abs() <= ACCUMULATE_STEPS * STEP * want).all())
