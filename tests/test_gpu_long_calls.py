@@ -1,4 +1,7 @@
-"""Calls large enough that a lane takes further batches of rows."""
+"""Calls large enough that a workgroup takes further rows, a lane further batches
+of rows, a wavefront further segments, or a head several tiles or parts; and the
+form of a head in one workgroup that only many long heads take. The references are
+those of the operators' own tests, with their tolerances unless stated."""
 from __future__ import annotations
 
 import numpy as np
@@ -7,6 +10,7 @@ import torch
 
 import scan_stream_compaction_amd as ssc
 from tests import test_gpu_cache as cache
+from tests import test_gpu_route as route
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -90,3 +94,27 @@ def test_accumulate_infinities_among_many_rows(queries):
         assert bool((got[..., 0] == inf).all()) and bool((got[..., 1] == -inf).all()) and bool(torch.isnan(got[..., 2]).all())
         want = torch.nan_to_num(weights[..., 3].double(), nan=0.0).sum(2)
         assert bool(((got[..., 3] - want).abs() <= ACCUMULATE_STEPS * STEP * want).all())
+
+
+# ---- route_rows_grad: further rows of a workgroup ----
+
+
+@pytest.mark.parametrize("n,experts,per,dtype", [
+    (40_001, 11, 2, torch.float32), (70_000, 24, 9, torch.bfloat16), (33_000, 160, 6, torch.bfloat16), (33_000, 128, 8, torch.float32),
+    (40_001, 60, 20, torch.float16), (17_000, 250, 5, torch.float32), (8300, 300, 8, torch.float16), (4200, 600, 4, torch.bfloat16),
+    (13_000, 1000, 3, torch.float32)])
+def test_gradient_of_many_tokens(n, experts, per, dtype):
+    """A workgroup takes two rows or more; what a row added in LDS must be gone when the next one begins."""
+    x, g = route.inputs(n + experts, n, experts, dtype)
+    live = torch.rand(n, device=DEV, generator=g) < 0.8
+    dw = torch.randn(n, per, device=DEV, generator=g)
+    dloss = torch.full((1,), 0.5 * n, device=DEV)
+    for normalize in (True, False):
+        ids, _, counts, _, _ = ssc.route_rows(x, per, normalize=normalize, live=live, balance=True)
+        route.check_gradient(x, ids, dw, normalize, live, counts, dloss)
+    any_ids = torch.randint(-1, experts + 1, (n, per), device=DEV, generator=g).int()
+    any_ids[::7, -1] = any_ids[::7, 0]
+    # few rows name an expert: what the row before left would show in the others
+    any_ids[:, 1:] = torch.where(torch.rand(n, 1, device=DEV, generator=g) < 0.5, -1, any_ids[:, 1:])
+    # of one sign, so that what one expert is named for twice does not cancel
+    route.check_gradient(x, any_ids, dw.abs(), False, live)
