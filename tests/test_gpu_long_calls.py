@@ -118,3 +118,40 @@ def test_gradient_of_many_tokens(n, experts, per, dtype):
     any_ids[:, 1:] = torch.where(torch.rand(n, 1, device=DEV, generator=g) < 0.5, -1, any_ids[:, 1:])
     # of one sign, so that what one expert is named for twice does not cancel
     route.check_gradient(x, any_ids, dw.abs(), False, live)
+
+
+# ---- route_rows: more workgroups than one a compute unit, so that no lane adds over 64 rows ----
+
+
+def test_balance_of_two_million_tokens():
+    n = 64 * 256 * 128 + 1
+    assert ssc.route_scratch_bytes(n, 8) == 16 + 8 + 257 * (8 + 9) * 4
+    x, g = route.inputs(2, n, 8, torch.bfloat16)
+    route.check_forward(x, 2, live=torch.rand(n, device=DEV, generator=g) < 0.9)
+
+
+def test_balance_of_many_tokens_and_experts():
+    """262,200 of 520 experts, the definition in 64 bits by parts on the GPU."""
+    n, experts, per = 262_200, 520, 10
+    assert ssc.route_scratch_bytes(n, experts) > ssc.route_scratch_bytes(262_144, experts)
+    x, _ = route.inputs(3, n, experts, torch.bfloat16)
+    ids, weights, counts, share, loss = ssc.route_rows(x, per, balance=True)
+    tol = (60 + 2 * 30) * STEP  # logits of a normal distribution lie within 30 of the row's largest
+    total = torch.zeros(experts, dtype=torch.float64, device=DEV)
+    many = torch.zeros(experts, dtype=torch.int64, device=DEV)
+    for part, i, w in zip(x.split(20_000), ids.split(20_000), weights.split(20_000)):
+        p = torch.softmax(part.double(), 1)
+        assert float((part.amax(1) - part.amin(1)).max()) < 30
+        at = torch.sort(part, dim=1, descending=True, stable=True)[1][:, :per]
+        assert torch.equal(i.long(), at)
+        want = p.gather(1, at)
+        want = want / want.sum(1, keepdim=True)
+        assert bool(((w - want).abs() <= want * tol).all())
+        total += p.sum(0)
+        many += torch.bincount(at.reshape(-1), minlength=experts)
+    assert torch.equal(counts.long(), torch.cat([many, torch.tensor([n], device=DEV)]))
+    want = total / n
+    tol += 75 * STEP
+    assert bool(((share - want).abs() <= want * tol).all())
+    want = experts * float((many / (per * n) * want).sum())
+    assert abs(float(loss) - want) <= want * tol
