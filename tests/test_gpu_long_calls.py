@@ -11,6 +11,7 @@ import torch
 import scan_stream_compaction_amd as ssc
 from tests import test_gpu_cache as cache
 from tests import test_gpu_route as route
+from tests import test_gpu_verify as verify
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -155,3 +156,23 @@ def test_balance_of_many_tokens_and_experts():
     assert bool(((share - want).abs() <= want * tol).all())
     want = experts * float((many / (per * n) * want).sum())
     assert abs(float(loss) - want) <= want * tol
+
+
+# ---- verify_rows: several segments to a wavefront, in two launches ----
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [
+    (159, 131_072, torch.bfloat16), (160, 131_073, torch.float16), (200, 140_000, torch.bfloat16), (100, 200_704, torch.float32),
+    (16, 2 ** 22 - 5, torch.bfloat16), (12, 2 ** 22, torch.float16)])
+def test_drafts_of_long_vocabularies(rows, vocab, dtype):
+    assert rows * -(-vocab // 1024) >= 2 * 6144 and ssc.verify_scratch_bytes(rows, vocab) > 0
+    p, x, u, q, g = verify.inputs(rows, rows, 1, vocab, dtype)
+    verify.check(p, x, u, q)
+    lengths = torch.randint(0, 2, (rows,), device=DEV, generator=g).int()
+    verify.check(p, x, u, None, lengths)
+    # q covers p: p draws
+    p[::3] = 0.5 * p[::3]
+    x[::3] = 0
+    u[::3, 0] = 0.9999999
+    q[::3] = 1.0
+    verify.check(p, x, u, q)
