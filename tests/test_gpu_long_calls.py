@@ -176,3 +176,56 @@ def test_drafts_of_long_vocabularies(rows, vocab, dtype):
     u[::3, 0] = 0.9999999
     q[::3] = 1.0
     verify.check(p, x, u, q)
+
+
+# ---- evict_rows: heads of up to 32,768 by one workgroup where there are many, and splits of several tiles ----
+
+
+def check_cut(scores, keep, first=0, recent=0, lengths=None):
+    """Against a stable sort on the GPU in 64 bits, NaN below -infinity."""
+    kept, counts = ssc.evict_rows(scores, keep, first=first, recent=recent, lengths=lengths)
+    batch, heads, capacity = scores.shape
+    for b in range(batch):
+        n = capacity if lengths is None else int(lengths[b])
+        want = torch.arange(min(n, keep), device=DEV).expand(heads, -1)
+        if n > keep:
+            x = scores[b, :, first:n - recent].double() + 0.0  # -0 as 0
+            x = torch.where(x == -float("inf"), -1e300, x)
+            x = torch.where(torch.isnan(x), -float("inf"), x)
+            best = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :keep - first - recent].sort(1)[0]
+            want = torch.cat([want[:, :first], first + best, torch.arange(n - recent, n, device=DEV).expand(heads, -1)], 1)
+        assert bool((counts[b] == want.shape[1]).all())
+        assert torch.equal(kept[b, :, :want.shape[1]].long(), want) and bool((kept[b, :, want.shape[1]:] == -1).all())
+
+
+@pytest.mark.parametrize("batch,heads,capacity,splits,tiles", [
+    (26, 8, 16_385, 1, 0), (26, 8, 20_001, 1, 0), (130, 1, 32_768, 1, 0), (130, 1, 32_769, 2, 4), (13, 10, 40_000, 2, 4),
+    (27, 3, 66_000, 3, 4), (1, 1, 524_289, 33, 2), (1, 1, 2 ** 20, 64, 2), (2, 2, 1_100_000, 34, 4)])
+def test_evict_many_and_longest_heads(batch, heads, capacity, splits, tiles):
+    """Tiles of 8192 positions: over 512 in all, or over 64 a head."""
+    rows = batch * heads
+    table = rows * splits * (16_384 + 8 + 4 * 8192 * tiles) + 16 * rows
+    assert ssc.evict_scratch_bytes(batch, heads, capacity) == (table if splits > 1 else 0)
+    g = cache.gen(capacity)
+    s = torch.exp(2.5 * torch.randn(batch, heads, capacity, device=DEV, generator=g))
+    s = torch.where(torch.rand(s.shape, device=DEV, generator=g) < 0.1, 0.0, s)
+    lengths = torch.randint(0, capacity + 1, (batch,), device=DEV, generator=g).int()
+    lengths[0] = capacity
+    check_cut(s, capacity // 2, 4, 256)
+    check_cut(s, capacity // 8, 4, capacity // 100, lengths)
+    check_cut(s, capacity - 1, 0, 1, lengths)
+    check_cut(s, 1)
+    # few values: the border falls among equal scores of every tile
+    few = torch.randint(0, 4, s.shape, device=DEV, generator=g).float()
+    few[0, :, ::3] = float("nan")
+    few[-1, :, 1::5] = -float("inf")
+    check_cut(few, capacity // 3, 3, 1000, lengths)
+    check_cut(few, capacity - 7)
+    # neighbours that share their first 11 or 22 bits
+    one = torch.full((1,), 1.0, device=DEV).view(torch.int32)
+    for spread in (2 ** 9, 2 ** 20):
+        near = (one + torch.randint(0, spread, s.shape, device=DEV, generator=g)).int().view(torch.float32)
+        check_cut(near, capacity // 3, 1, 3, lengths)
+    nan = torch.full(s.shape, float("nan"), device=DEV)
+    nan[..., ::2] = -float("inf")
+    check_cut(nan, capacity // 2 + 3)
