@@ -229,3 +229,102 @@ def test_evict_many_and_longest_heads(batch, heads, capacity, splits, tiles):
     nan = torch.full(s.shape, float("nan"), device=DEV)
     nan[..., ::2] = -float("inf")
     check_cut(nan, capacity // 2 + 3)
+
+
+# ---- views whose offsets pass 2^32 elements ----
+
+
+def far(shape, strides, dtype, values):
+    """A view of `shape` with its first dimensions far apart, holding `values`."""
+    span = sum((n - 1) * s for n, s in zip(shape, strides)) + 1
+    view = torch.empty(span, dtype=dtype, device=DEV).as_strided(shape, strides)
+    view.copy_(values)
+    return view
+
+
+def test_rows_far_apart():
+    """Results equal those of the same values side by side."""
+    g = cache.gen(9)
+    x = torch.randn(9, 40, device=DEV, generator=g).to(torch.bfloat16)
+    away = far(x.shape, (2 ** 30, 1), x.dtype, x)
+    want = ssc.route_rows(x, 4, balance=True)
+    assert all(torch.equal(a, b) for a, b in zip(ssc.route_rows(away, 4, balance=True), want))
+    dw = torch.randn(9, 4, device=DEV, generator=g)
+    assert torch.equal(ssc.route_rows_grad(away, want[0], dw), ssc.route_rows_grad(x, want[0], dw))
+    del away
+    for vocab in (3000, 70_000):
+        p, ids, u, q, _ = verify.inputs(9, 3, 2, vocab, torch.bfloat16)
+        want = ssc.verify_rows(p, ids, u, q)
+        # the places of a sequence side by side, and the sequences of a place
+        got = ssc.verify_rows(far(p.shape, (2 ** 32, 2 ** 30, 1), p.dtype, p), ids, u, far(q.shape, (2 ** 30, 2 ** 32, 1), q.dtype, q))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_heads_far_apart():
+    g = cache.gen(10)
+    for queries in (1, 200):
+        w = torch.rand(2, 4, queries, 300, device=DEV, generator=g).to(torch.bfloat16)
+        s = torch.rand(2, 2, 300, device=DEV, generator=g)
+        away = far(w.shape, (2 ** 32, 2 ** 30, 2 ** 20, 1), w.dtype, w)
+        to = far(s.shape, (2 ** 32 + 2 ** 20, 2 ** 31, 1), s.dtype, s)
+        ssc.accumulate_weights(to, away)
+        assert torch.equal(to, ssc.accumulate_weights(s, w))
+        del away, to
+    for capacity in (900, 20_000):
+        s = torch.rand(2, 2, capacity, device=DEV, generator=g)
+        away = far(s.shape, (2 ** 32 + 2 ** 20, 2 ** 31, 1), s.dtype, s)
+        want = ssc.evict_rows(s, capacity // 2, first=2, recent=100)
+        assert all(torch.equal(a, b) for a, b in zip(ssc.evict_rows(away, capacity // 2, first=2, recent=100), want))
+        del away
+    rows = torch.randn(2, 2, 50, 24, device=DEV, generator=g).to(torch.bfloat16)
+    kept = cache.positions(g, 2, 2, 50, 20)
+    away = far(rows.shape, (2 ** 33, 2 ** 32, 2 ** 25, 1), rows.dtype, rows)
+    ssc.move_rows(away, kept)
+    assert torch.equal(away, ssc.move_rows(rows, kept))
+
+
+# ---- one scratch buffer of two captured graphs ----
+
+
+def test_graphs_that_share_scratch():
+    """Replayed in turn, over changed inputs: each graph writes what it reads of the scratch."""
+    g = cache.gen(11)
+    scratch = torch.full((2 ** 22,), 255, dtype=torch.uint8, device=DEV)
+
+    def inputs_of(n):
+        return dict(logits=torch.randn(900 * n, 60, device=DEV, generator=g), scores=torch.rand(1, n, 17_000 * n, device=DEV, generator=g),
+                    weights=torch.rand(1, n, 300, 900, device=DEV, generator=g), sums=torch.rand(1, n, 900, device=DEV, generator=g),
+                    rows=torch.randn(1, n, 9000, 16, device=DEV, generator=g), kept=cache.positions(g, 1, n, 9000, 8000),
+                    drafts=verify.inputs(n, 3 * n, 2, 70_000, torch.float32)[:4])
+
+    def step(s, scratch):
+        routed = ssc.route_rows(s["logits"], 4, balance=True, scratch=scratch)
+        ssc.accumulate_weights(s["sums"], s["weights"], scratch=scratch)
+        ssc.move_rows(s["rows"], s["kept"], scratch=scratch)
+        return (*routed, *ssc.evict_rows(s["scores"], 5000, first=3, recent=50, scratch=scratch),
+                *ssc.verify_rows(*s["drafts"], scratch=scratch), s["sums"], s["rows"])
+
+    def copy_of(s):
+        return {k: v.clone() if isinstance(v, torch.Tensor) else tuple(x.clone() for x in v) for k, v in s.items()}
+
+    sets = [inputs_of(1), inputs_of(2)]
+    assert ssc.accumulate_scratch_bytes(1, 1, 1, 300, 900, torch.float32) > 0 and ssc.move_scratch_bytes(4, 1, 1, 8000, 16) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for s in sets:
+            step(copy_of(s), scratch)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, got = [], []
+    for s in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(step(s, scratch))
+    for i in range(6):
+        s = sets[i % 2]
+        s["logits"].copy_(torch.randn(s["logits"].shape, device=DEV, generator=g))
+        s["scores"].copy_(torch.rand(s["scores"].shape, device=DEV, generator=g))
+        want = step(copy_of(s), None)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[i % 2], want))
