@@ -328,3 +328,40 @@ def test_graphs_that_share_scratch():
         graphs[i % 2].replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got[i % 2], want))
+
+
+# ---- move_rows in place: positions in any order ----
+
+
+@pytest.mark.parametrize("batch,heads,capacity,keep,width", [(1, 2, 6000, 5000, 64), (1, 3, 90, 80, 33), (40, 8, 300, 200, 40), (2, 2, 700, 650, 5000)])
+def test_moves_of_positions_in_any_order(batch, heads, capacity, keep, width):
+    """At or past their slots, in no order, one for several slots; those before their slots stay where they are."""
+    g = cache.gen(keep)
+    rows = torch.randint(-2 ** 15, 2 ** 15, (batch, heads, capacity, width), device=DEV, generator=g).short()
+    slots = torch.arange(keep, device=DEV)
+    kept = slots + (torch.rand(batch, heads, keep, device=DEV, generator=g) * (capacity - slots)).long()
+    kept = torch.where(torch.rand(kept.shape, device=DEV, generator=g) < 0.2, capacity - 1, kept)
+    before = torch.rand(kept.shape, device=DEV, generator=g) < 0.1
+    at = kept.clone()
+    kept = torch.where(before, (torch.rand(kept.shape, device=DEV, generator=g) * slots).long(), kept)
+    want = rows.clone()
+    at = torch.where(before, slots, at)
+    want[:, :, :keep] = rows.gather(2, at[..., None].expand(-1, -1, -1, width))
+    for _ in range(3):
+        assert torch.equal(ssc.move_rows(rows.clone(), kept.int()), want)
+
+
+# ---- calls with nothing to do ----
+
+
+def test_calls_of_no_sequences_and_no_positions():
+    w, s = torch.rand(2, 4, 3, 0, device=DEV), torch.rand(2, 2, 9, device=DEV)
+    keep = s.clone()
+    assert torch.equal(ssc.accumulate_weights(s, w, fresh=2, decay=0.0), keep)
+    assert torch.equal(ssc.accumulate_weights(s, torch.rand(2, 2, 200, 9, device=DEV), lengths=torch.zeros(2, dtype=torch.int32, device=DEV)), keep)
+    assert ssc.accumulate_weights(s[:0], torch.rand(0, 4, 300, 9, device=DEV)).shape == (0, 2, 9)
+    kept = torch.zeros(0, 2, 5, dtype=torch.int32, device=DEV)
+    rows = torch.rand(0, 2, 9, 4, device=DEV)
+    assert ssc.move_rows(rows, kept) is rows and ssc.move_rows(rows, kept, out=torch.rand(0, 2, 7, 4, device=DEV)).shape == (0, 2, 5, 4)
+    kept, counts = ssc.evict_rows(s, 4, lengths=torch.zeros(2, dtype=torch.int32, device=DEV), recent=2)
+    assert bool((kept == -1).all()) and bool((counts == 0).all())
