@@ -522,7 +522,9 @@ size_t ssc_route_scratch_bytes(int64_t tokens, int64_t experts);
  *   share[e]   = mean of p[t, e] over them (0 for n = 0)
  *   loss       = experts * sum over e of counts[e] / (per * n) * share[e]: 1 where
  *                tokens fall evenly (0 for n = 0)
- * Sums over tokens are fp32 up to 64 rows of a lane and fp64 beyond. */
+ * What a workgroup adds up is fp32: up to 64 rows of a lane, then its lanes and
+ * wavefronts, up to 8192 tokens of up to 128 experts; sums of workgroups are fp64.
+ * What lies between rows that are apart counts as theirs: no output may lie there. */
 int ssc_route_rows(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
                    const uint8_t *live, int64_t per, int normalize, int32_t *ids, float *weights,
                    int32_t *counts, float *share, float *loss, void *scratch, size_t scratch_bytes,
@@ -584,7 +586,9 @@ int ssc_verify_rows_i64(const void *probs, int dtype, int64_t rows, int64_t draf
  * A cache cut to the rows that were attended to most. Caches are batch x heads x
  * capacity (x width) with strides in elements for all but the last dimension,
  * which is contiguous; strides are not negative, and what a call writes does not
- * overlap itself. At most 65,535 batch * heads and 2^31 - 4097 positions.
+ * overlap itself. A view counts from its first element to its last where overlaps
+ * are checked, the gaps between its rows with it. At most 65,535 batch * heads and
+ * 2^31 - 4097 positions.
  * lengths[b] (nullable: all) is the number of positions in use, held to what there
  * is. */
 
@@ -626,15 +630,17 @@ int ssc_evict_rows(const float *scores, int64_t batch, int64_t heads, int64_t ca
                    int64_t keep, int64_t first, int64_t recent, int32_t *kept, int32_t *counts,
                    void *scratch, size_t scratch_bytes, void *stream);
 
-/* Scratch bytes of ssc_move_rows in place: the rows it moves, where a few long
- * heads go by way of it; 0 otherwise, and for a move to another cache. */
+/* Scratch bytes of ssc_move_rows in place: those of all keep rows of every head,
+ * where a few long heads go by way of it (as many bytes as the cache keeps); 0
+ * otherwise, and for a move to another cache. */
 size_t ssc_move_scratch_bytes(int elem_bytes, int64_t batch, int64_t heads, int64_t keep, int64_t width);
 
 /* Rows of a cache moved together: out[b, h, s, :] = cache[b, h, kept[b, h, s], :]
- * for s < keep, bit for bit, for elements of 1, 2, 4 or 8 bytes. Slots whose position
- * lies outside [0, capacity) are not written. out may be the cache itself (the same
- * address and strides): then positions that lie before their slot, which
- * ssc_evict_rows gives none of, are not moved. Any other overlap is an error. */
+ * for s < keep (1 to capacity), bit for bit, for elements of 1, 2, 4 or 8 bytes.
+ * Slots whose position lies outside [0, capacity) are not written. out may be the
+ * cache itself (the same address and strides): then positions that lie before their
+ * slot, which ssc_evict_rows gives none of, are not moved. Any other overlap is an
+ * error. */
 int ssc_move_rows(const void *cache, int elem_bytes, int64_t batch, int64_t heads, int64_t capacity,
                   int64_t width, int64_t cache_stride_batch, int64_t cache_stride_head,
                   int64_t cache_stride_row, const int32_t *kept, int64_t keep, void *out,

@@ -1214,7 +1214,9 @@ def move_rows(cache: torch.Tensor, kept: torch.Tensor, *, out: torch.Tensor | No
     together. Without out in place, and the cache is returned; otherwise the part
     of out (batch, heads, at least keep, width) that holds them. Slots whose
     position lies outside the cache are not written. All but the last dimension may
-    lie apart; scores move as scores.unsqueeze(3)."""
+    lie apart; scores move as scores.unsqueeze(3). In place a few long heads go by way
+    of scratch that holds all rows kept (move_scratch_bytes says how much; a new
+    tensor unless one is given, which can serve caches one after another)."""
     _view(cache, "cache", 4, None)
     batch, heads, capacity, width = cache.shape
     _given(kept, "kept", cache, cache.get_device(), torch.int32, 0)
