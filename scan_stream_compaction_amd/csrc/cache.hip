@@ -798,10 +798,9 @@ int check_cache(int64_t batch, int64_t heads, int64_t capacity) {
     return SSC_OK;
 }
 
-// Where the wavefronts are few
-// (under 2048) and have over 16 rows each, the rows in parts, up to 4096 wavefronts
-// in all. Two heads of 4 sequences, 456 rows of 1390 fp16: 39 us a call in one part,
-// 12 in four.
+// Where the wavefronts are few (under 2048) and have over 16 rows each, the rows in
+// parts, up to 4096 wavefronts in all. Two heads of 4 sequences, 456 rows of 1390
+// fp16: 39 us a call in one part, 11.5 in four (traced 8.7 and 3.6 for the join).
 struct AccumulatePlan {
     uint32_t splits;
     size_t bytes;
@@ -824,11 +823,12 @@ AccumulatePlan accumulate_plan(int64_t heads, int64_t rows, int64_t length, int 
 // workgroups (no two of these share bytes of a row, nor less than 64 bytes), or
 // by way of scratch. A workgroup's set of rows takes 4.5 us one after another; the
 // scratch doubles the traffic but has no such order. Rows moved, direct against
-// scratch, us:
-//   2 heads x 20,000 of 128 bytes   84  9.5      4 heads x 2500 of 1024 bytes   19   13
-//   8 x 20,000 of 256               88   35      8 x 1024 of 256               5.6  9.8
-//   22 x 4382 of 192                25   18      48 x 4695 of 256               34   46
-//   32 x 2048 of 130                32   14      256 x 4096 of 256             102  188
+// scratch, us, and the rows read and written once at a copy's rate:
+//   2 heads x 20,000 of 128 bytes   84  9.5   2.0    4 heads x 2500 of 1024 bytes   19   13   4.0
+//   8 x 20,000 of 256               88   35    16    8 x 1024 of 256               5.6  9.8   0.8
+//   22 x 4382 of 192                25   18   7.2    48 x 4695 of 256               36   46    22
+//   32 x 2048 of 130                32   14   3.3    256 x 4096 of 256             102  188   104
+// 8 x 20,000 of 256, traced: 17.2 us to scratch and 17.2 back, each 41 MB read and 41 written.
 struct MovePlan {
     int piece, cols;
     size_t bytes;
@@ -858,7 +858,14 @@ MovePlan move_plan(int64_t heads, int64_t keep, int64_t row_bytes, int elem) {
 }
 
 // Splits of a head: of 8192 positions where that gives up to 512 workgroups,
-// else of 32,768, and longer ones where there would be over 64 of a head.
+// else of 32,768, and longer ones where there would be over 64 of a head. us a call,
+// one workgroup a head against splits of 8192 (of 16,384):
+//   8 x 20,000     18.0  16.1      128 x 20,000    19.8  28.4      320 x 20,000     37  53 (47)
+//   64 x 20,000    19.5  18.3      128 x 32,768    22.2  33.7      320 x 32,768     42  73 (63)
+// (the border is right for longer heads; the 128 would take the other side), and splits
+// of 8192 against 32,768:
+//   8 x 65,536     18.3  33.0      64 x 65,536     36.1  38.0      320 x 65,536    170  111
+//   8 x 131,072    20.3  34.3      80 x 65,536     47.2  38.6      320 x 131,072   348  186
 struct EvictPlan {
     uint32_t splits, span;
     size_t found, before, bytes;  // offsets into the scratch

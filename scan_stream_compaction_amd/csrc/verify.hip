@@ -40,6 +40,14 @@ constexpr int kDrawBlock = 256;
 //   1        12.6 16.7 ( 7.9  7.1)     12.5 16.7 (10.4  6.9)     15.5 16.7 (15.4  6.8)
 //   64       12.6 16.7 ( 9.0  7.7)     12.7 16.7 (11.6  9.4)     19.0 16.4 (19.0 15.2)
 //   192      12.5 16.8 (10.9 12.3)     17.3 18.4 (17.3 18.1)     27.2 28.9 (27.1 28.8)
+// and by prepared alone, bf16 (the rows partly in the last-level cache), around the borders:
+//   rows of      65,536       98,304      131,072      152,000      256,000
+//   128       12.8 12.3    15.9 14.4    18.6 16.8    20.9 18.7    30.4 25.7
+//   160       13.4 13.5    16.7 16.3    19.7 19.2    21.5 21.1    31.7 29.9
+//   192       14.2 14.4    17.4 17.6    20.9 21.4    22.7 23.9    34.6 35.2
+//   256       15.7 16.5    19.7 20.8    24.5 25.4    26.6 29.0    43.9 50.4
+// so that from 192 rows on longer vocabularies would gain by one launch, too: they
+// take two, for the sums of 128 segments that the form holds.
 constexpr int kRowBlock = 1024;
 constexpr int kRowSegs = 128;
 constexpr int kRowMany = 160;
