@@ -246,3 +246,17 @@ def test_the_binding_refuses_cpu_tensors_and_wrong_shapes():
     for f in (ssc.route_rows, ssc.evict_rows):
         with pytest.raises(TypeError):
             f([1.0], 1)
+
+
+def test_outputs_in_the_gaps_of_views_are_refused():
+    """Rows that are apart are one span where overlaps are checked."""
+    route = dict(logits=A, dtype=0, tokens=100, experts=16, stride=32, live=None, per=4, normalize=1, ids=A + 64, weights=C,
+                 counts=None, share=None, loss=None, scratch=None, sbytes=0, stream=None)
+    assert _call("ssc_route_rows", route) == ALIAS
+    grad = dict(logits=A, dtype=0, tokens=100, experts=16, stride=32, live=None, ids=B, per=4, normalize=0, dweights=C,
+                counts=None, dloss=None, dlogits=A + 64, stream=None)
+    assert _call("ssc_route_rows_grad", grad) == ALIAS
+    # keys and values in one buffer, moved from the one half to the other
+    move = dict(cache=A, es=2, batch=1, heads=3, capacity=100, width=16, cb=9600, ch=32, cr=96, kept=B, keep=50, out=A + 32,
+                ob=9600, oh=32, orow=96, scratch=None, sbytes=0, stream=None)
+    assert _call("ssc_move_rows", move) == ALIAS
